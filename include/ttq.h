@@ -337,6 +337,134 @@ size_t ttq_linear_shared_workspace_bytes(const ttq_linear_args* layers, int n);
 #define TTQ_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)
 ttq_status ttq_linear_noalloc(const ttq_linear_args* args, void* stream);
 
+/*
+ * Projections whose weights each token chooses.  [TTQ §method b7] the
+ * quantized projection kernel, where the tokens of one launch do not share
+ * their weights: the experts of a mixture-of-experts layer, and low-rank
+ * adapters (the B A of [TTQ §method b5]) of many requests beside one shared
+ * projection.
+ */
+
+typedef enum {
+    TTQ_SCORE_SOFTMAX = 0,    /* exp(l) / sum of exp(l) over all experts    */
+    TTQ_SCORE_SIGMOID = 1     /* 1 / (1 + exp(-l))                          */
+} ttq_score;
+
+typedef enum {
+    TTQ_ACT_SILU = 0,         /* x / (1 + exp(-x))                          */
+    TTQ_ACT_GELU_TANH = 1     /* x (1 + tanh(sqrt(2/pi)(x + 0.044715 x^3))) / 2 */
+} ttq_act;
+
+/*
+ * ttq_moe_route — the top-k experts of each token and their weights.
+ *   logits: [T][E] fp32 or bf16 (lt), row stride ldl >= E.  ids, w: [T][topk]
+ *   dense.  ids[t][j] is the expert of the j-th largest logit of token t,
+ *   equal logits in the order of their index; w[t][j] is its score (in fp32:
+ *   softmax over all E logits, or sigmoid), divided by the sum of the topk
+ *   scores if renormalize != 0.  A logit that is -inf or NaN is never chosen
+ *   and has score 0: where fewer than topk others are left, the remaining
+ *   slots get id -1 and weight 0 (all of them for a row without any).  +inf
+ *   logits share the softmax equally.
+ *   1 <= E <= 1024, 1 <= topk <= min(E, 32).  logits, ids and w aligned to
+ *   their element size.  T == 0 is an empty call.  No workspace.
+ */
+ttq_status ttq_moe_route(const void* logits, int lt, int64_t T, int64_t E, int64_t ldl, int topk,
+                         int score, int renormalize, int32_t* ids, float* w, void* stream);
+
+/* Quantized state of E weights of equal shape: codes [E][rows][K*bits/32],
+ * scale_f16 and zero_f16 [E][rows][K/group], dense, each expert's part as
+ * ttq_quantize_groups writes it (experts that share s can be quantized in
+ * one call with E*rows rows); expert e is scaled by s + e * s_stride
+ * (s_stride 0: one s for all; else a multiple of 4, at least K). */
+typedef struct ttq_expert_state {
+    const float* s;  int64_t s_stride;
+    const int32_t* codes;  const uint16_t* scale_f16;  const uint16_t* zero_f16;
+} ttq_expert_state;
+
+/*
+ * ttq_moe — a gated mixture-of-experts layer on quantized experts, for few
+ * tokens (decode steps; longer prompts in chunks of at most 1024 tokens).
+ *   Y[t] = sum_j w[t][j] D_e (h / s_down),  h = act(g) * u,
+ *   [g; u] = G_e (X[t] / s_in),  e = ids[t][j],
+ *   G_e [2 I][K] and D_e [M][I] the dequantized gate_up and down weights of
+ *   expert e (gate rows first), s_in and s_down their scales.
+ *   X: [T][K] (xt), stride ldx.  ids, w: [T][topk] dense, e.g. from
+ *   ttq_moe_route; a slot whose id is not in [0, E) adds nothing (its weight
+ *   is not read), a token without any gets zeros, an expert named twice by a
+ *   token counts twice.  Y: [T][M] (yt), overwritten.
+ *   h and all sums are kept in fp32; Y is rounded once.  x / s and h enter
+ *   the matrix products with at least 16 significant bits for bf16 X and 24
+ *   for fp32 X, codes exactly.  Results of a token do not depend on the other
+ *   tokens of the call beyond fp32 rounding, and are reproducible run to run.
+ *   K and I multiples of 32 and of group, at most 2^18; E <= 1024;
+ *   1 <= topk <= 32; T > 1024 returns TTQ_ERR_UNSUPPORTED.  T == 0 or M == 0
+ *   is an empty call.  ws: ttq_moe_workspace_bytes(T, topk, K, I, M, E, bits,
+ *   group) bytes, 256-byte aligned; calls that may run at the same time need
+ *   workspaces of their own.
+ */
+typedef struct ttq_moe_args {
+    const void* X;  int xt;  int64_t T;  int64_t K;  int64_t ldx;
+    const int32_t* ids;  const float* w;  int64_t topk;
+    int64_t E;  int64_t I;  int64_t M;
+    ttq_expert_state gate_up;  ttq_expert_state down;
+    int bits;  int group;  int act;
+    void* Y;  int yt;  int64_t ldy;
+} ttq_moe_args;
+
+ttq_status ttq_moe(const ttq_moe_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes for ttq_moe (0 for sizes it does not accept). */
+size_t ttq_moe_workspace_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E,
+                               int bits, int group);
+
+/* Low-rank adapters: A [n][rank][K] and B [n][M][rank], dense, both fp32 or
+ * bf16 (dt).  Adapter a uses its first r_a = clamp(ranks[a], 0, rank) rows of
+ * A and columns of B (ranks NULL: all; the rest is not used) and is
+ * multiplied by scale[a] (scale NULL: 1).  ids[t]: token t's adapter; an id
+ * outside [0, n) means none.  1 <= rank <= 64, 0 <= n <= 65536; A and B
+ * 16-byte aligned. */
+typedef struct ttq_adapters {
+    const void* A;  const void* B;  int dt;
+    int64_t n;  int rank;
+    const int32_t* ranks;  const float* scale;
+    const int32_t* ids;
+} ttq_adapters;
+
+/*
+ * ttq_adapters_add — each token's own low-rank adapter, added to a projection.
+ * [TTQ §method b5] the term B (A X) of ttq_lowrank_add, with a (B, A) per
+ * request.
+ *   Y[t] = C[t] + scale_a B_a (A_a X[t]),  a = ids[t]; without an adapter
+ *   Y[t] = C[t].  In fp32, rounded once to Y.
+ *   X: [T][K] (xt).  C: [T][M] of Y's dtype, stride ldc, or NULL for zeros;
+ *   it may be Y itself (ldc == ldy), else it must not overlap Y.  Any order
+ *   of ids is accepted; runs of tokens of one adapter (prompts) cost least.
+ *   K a multiple of 8, at most 2^18.  T == 0 or M == 0 is an empty call.
+ *   ws: ttq_adapters_workspace_bytes(T, K, M, rank) bytes, 256-byte aligned.
+ */
+ttq_status ttq_adapters_add(const void* X, int xt, int64_t T, int64_t K, int64_t ldx,
+                            const ttq_adapters* adapters, int64_t M, const void* C, int64_t ldc,
+                            void* Y, int yt, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes for ttq_adapters_add (0 for sizes it does not accept). */
+size_t ttq_adapters_workspace_bytes(int64_t T, int64_t K, int64_t M, int rank);
+
+/*
+ * ttq_qgemm_adapters — a quantized projection shared by the tokens' requests,
+ * plus their adapters.  [TTQ §method b5, b7].
+ *   Y[t] = W_hat (X[t] / s) + scale_a B_a (A_a X[t]),  a = ids[t]:
+ *   ttq_qgemm followed by ttq_adapters_add, with Y rounded once.  The
+ *   arguments are those of the two calls, and K is a multiple of 32.
+ *   ws: ttq_qgemm_adapters_workspace_bytes(...) bytes, 256-byte aligned.
+ */
+ttq_status ttq_qgemm_adapters(const void* X, int xt, int64_t T, int64_t K, int64_t ldx, const float* s,
+                              const int32_t* codes, const uint16_t* scale_f16, const uint16_t* zero_f16,
+                              int64_t M, int bits, int group, const ttq_adapters* adapters,
+                              void* Y, int yt, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes for ttq_qgemm_adapters (0 for sizes it does not accept). */
+size_t ttq_qgemm_adapters_workspace_bytes(int64_t T, int64_t K, int64_t M, int bits, int group, int rank);
+
 /* Static text for a status code. */
 const char* ttq_status_str(int status);
 

@@ -139,6 +139,55 @@ bool factors_supported(bool wf32, int64_t M, int64_t K, int64_t ldw, int l, int 
 hipError_t launch_factors(const uint16_t* W, int64_t M, int64_t K, int64_t ldw, const float* s, const float* om,
                           int l, int q, int rank, float* B, float* A, char* ws, hipStream_t st);
 
+// Router (route.hip): E <= kMoeMaxExperts, topk <= min(E, kRouteMaxTopk).
+constexpr int kMoeMaxExperts = 1024;
+constexpr int kRouteMaxTopk = 32;
+hipError_t launch_moe_route(const void* L, bool lf32, int64_t T, int E, int64_t ldl, int topk, int score, int renorm,
+                            int32_t* ids, float* w, hipStream_t st);
+
+// Mixture-of-experts layer (moe.hip), T <= kMoeMaxT.
+constexpr int64_t kMoeMaxT = 1024;
+struct MoeTile {
+    int expert, first, count;   // `count` slots from position `first` of the slots sorted by expert
+};
+// One of the layer's two products, for tiles of slots of one expert.
+struct MoeProduct {
+    const MoeTile* tiles;
+    const int32_t* order;       // slots sorted by expert
+    const void* X;              // rows of K: tokens (row slot / topk), or h (row slot)
+    int64_t ldx, K, rows;       // rows: outputs per slot
+    int topk, group, act;
+    const float* s;             // per expert, at s_stride
+    int64_t s_stride;
+    const uint32_t* codes;
+    const uint16_t* scale;
+    const uint16_t* zero;
+    const float* w;             // weight of each slot
+    const float* s_out;         // scales of the second product's input
+    int64_t s_out_stride;
+    float* out;                 // [slots][rows]
+};
+struct MoeLayout {
+    size_t order, tiles, h, p, total;
+};
+MoeLayout moe_layout(int64_t T, int64_t topk, int64_t I, int64_t M, int64_t E);
+hipError_t launch_moe(const ttq_moe_args* a, char* ws, hipStream_t st);
+
+// Adapters of many requests (adapters.hip).
+struct AdapterTable {
+    const void* A;
+    const void* B;
+    bool f32;                   // dtype of A and B
+    int n, rank;
+    const int32_t* ranks;
+    const float* scale;
+    const int32_t* ids;
+};
+size_t adapters_ws_bytes(int64_t T, int64_t K, int rank);
+hipError_t launch_adapters(const void* X, bool xf32, int64_t T, int64_t K, int64_t ldx, const AdapterTable& ad,
+                           const void* C, bool cf32, int64_t ldc, int64_t M, void* Y, bool yf32, int64_t ldy, float* Z,
+                           hipStream_t st);
+
 // ttq_linear's argument checks (clearing the calling thread's error text
 // first) and the workspace bytes the call needs (0 for an empty call).
 ttq_status linear_check(const ttq_linear_args* a, size_t* need);

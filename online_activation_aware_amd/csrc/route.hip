@@ -1,0 +1,118 @@
+// Router of a mixture-of-experts layer: each token's top-k experts and their
+// weights from its logits.
+//
+//   ids[t][j]: the experts of the j-th largest logit, ties to the lowest
+//   index; softmax: w = exp(l_j - m) / sum_e exp(l_e - m), m the row's
+//   maximum; sigmoid: w = 1 / (1 + exp(-l_j)); renormalised: w / sum_j w.
+//
+// One wave per token: lane l holds the logits l, l + 64, ... as keys that
+// order like the floats (NaN and -inf as the key 0, which is never chosen),
+// and k rounds of a 64-bit wave maximum over (key, ~index) pick the experts;
+// the lane that owns the winner retires it.  The maximum and the sum of the
+// softmax come from the same registers, in fp32 and in a fixed order.  The
+// pass reads the logits once; a call is bound by its launch.
+#include "common.hpp"
+#include "launch.hpp"
+
+namespace ttq {
+
+constexpr int kRouteWaves = 4;                    // tokens per workgroup
+
+__device__ __forceinline__ uint32_t order_key(float x) {
+    if (!(x > -__builtin_inff())) return 0u;      // -inf and NaN
+    const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);   // -0 equals +0
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    return __builtin_bit_cast(float, (k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+// exp(v - m) with exp(m - m) = 1 for an infinite m.
+__device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.f : expf(v - m); }
+
+template <int NV, bool LF32>
+__global__ __launch_bounds__(kRouteWaves * kWave) void k_moe_route(const void* __restrict__ L, int64_t T, int E,
+                                                                   int64_t ldl, int topk, int score, int renorm,
+                                                                   int32_t* __restrict__ ids,
+                                                                   float* __restrict__ wts) {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int64_t t = (int64_t)blockIdx.x * kRouteWaves + threadIdx.x / kWave;
+    if (t >= T) return;
+    uint32_t key[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane + kWave * i;
+        float v = -__builtin_inff();
+        if (e < E) {
+            if constexpr (LF32) v = ((const float*)L)[t * ldl + e];
+            else v = bf16_to_f32(((const uint16_t*)L)[t * ldl + e]);
+        }
+        key[i] = order_key(v);
+    }
+    uint32_t mine = 0, mine_id = 0xFFFFFFFFu;     // the lane-th choice
+    float m = 0.f, sum = 1.f;
+    uint32_t taken = 0;                           // bit i: this lane's value i is chosen already
+    for (int j = 0; j < topk; ++j) {
+        uint32_t bk = 0, be = 0xFFFFFFFFu;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool better = key[i] > bk && !((taken >> i) & 1u);
+            bk = better ? key[i] : bk;
+            be = better ? (uint32_t)(lane + kWave * i) : be;
+        }
+#pragma unroll
+        for (int s = 1; s < kWave; s <<= 1) {
+            const uint32_t ok = __shfl_xor(bk, s), oe = __shfl_xor(be, s);
+            const bool better = ok > bk || (ok == bk && oe < be);
+            bk = better ? ok : bk;
+            be = better ? oe : be;
+        }
+        if (bk == 0) break;                       // wave-uniform: nothing is left to choose
+        if ((be & (kWave - 1)) == (uint32_t)lane) taken |= 1u << (be / kWave);
+        if (lane == j) {
+            mine = bk;
+            mine_id = be;
+        }
+        if (j == 0) m = key_value(bk);
+    }
+    if (score == TTQ_SCORE_SOFTMAX) {
+        float part = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) part += key[i] ? exp_below(key_value(key[i]), m) : 0.f;
+#pragma unroll
+        for (int s = 1; s < kWave; s <<= 1) part += __shfl_xor(part, s);
+        sum = part;
+    }
+    float w = 0.f;
+    if (mine) {
+        const float v = key_value(mine);
+        w = score == TTQ_SCORE_SOFTMAX ? exp_below(v, m) / sum : 1.f / (1.f + expf(-v));
+    }
+    if (renorm) {
+        float tot = w;
+#pragma unroll
+        for (int s = 1; s < kWave; s <<= 1) tot += __shfl_xor(tot, s);
+        w = tot > 0.f ? w / tot : 0.f;
+    }
+    if (lane < topk) {
+        ids[t * topk + lane] = mine ? (int32_t)mine_id : -1;
+        wts[t * topk + lane] = w;
+    }
+}
+
+hipError_t launch_moe_route(const void* L, bool lf32, int64_t T, int E, int64_t ldl, int topk, int score, int renorm,
+                            int32_t* ids, float* w, hipStream_t st) {
+    const dim3 grid((unsigned)((T + kRouteWaves - 1) / kRouteWaves)), block(kRouteWaves * kWave);
+#define TTQ_ROUTE(NV)                                                                                             \
+    return lf32 ? launch_kernel(k_moe_route<NV, true>, grid, block, 0, st, nullptr, nullptr, L, T, E, ldl, topk,  \
+                                score, renorm, ids, w)                                                            \
+                : launch_kernel(k_moe_route<NV, false>, grid, block, 0, st, nullptr, nullptr, L, T, E, ldl, topk, \
+                                score, renorm, ids, w)
+    if (E <= 64) TTQ_ROUTE(1);
+    if (E <= 128) TTQ_ROUTE(2);
+    if (E <= 256) TTQ_ROUTE(4);
+    if (E <= 512) TTQ_ROUTE(8);
+    TTQ_ROUTE(16);
+#undef TTQ_ROUTE
+}
+
+}  // namespace ttq

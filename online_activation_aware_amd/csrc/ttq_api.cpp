@@ -564,3 +564,163 @@ ttq_status ttq_linear_shared(const ttq_linear_args* layers, int n, void* ws, siz
 }
 
 }  // extern "C"
+
+// ------------------------------------------------- weights chosen per token
+
+namespace {
+
+constexpr int64_t kMaxAdapters = 65536;
+
+ttq_status check_experts(const char* name, const ttq_expert_state& q, int64_t K) {
+    TTQ_REQUIRE(q.s != nullptr && aligned(q.s, 16), "%s.s: null or not 16-byte aligned", name);
+    TTQ_REQUIRE(q.s_stride == 0 || (q.s_stride >= K && q.s_stride % 4 == 0 && q.s_stride <= kMaxDim),
+                "%s.s_stride: neither 0 nor a multiple of 4 of at least the row length", name);
+    return check_state(q.s, q.codes, q.scale_f16, q.zero_f16, true);
+}
+
+ttq_status check_moe_sizes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E, int bits, int group) {
+    TTQ_REQUIRE(dim_ok(T), "T out of range");
+    TTQ_REQUIRE(E >= 1 && E <= ttq::kMoeMaxExperts, "E (experts) must be in [1, %d]", ttq::kMoeMaxExperts);
+    TTQ_REQUIRE(topk >= 1 && topk <= ttq::kRouteMaxTopk, "topk must be in [1, %d]", ttq::kRouteMaxTopk);
+    if (ttq_status e = check_quant_shape(M, K, bits, group)) return e;
+    TTQ_REQUIRE(I > 0 && I <= kMaxK && I % 32 == 0 && I % group == 0,
+                "I must be a positive multiple of 32 and of the group size, at most 2^18");
+    if (T > ttq::kMoeMaxT)
+        return fail(TTQ_ERR_UNSUPPORTED, "at most %d tokens a call (got %lld): pass a longer prompt in chunks",
+                    (int)ttq::kMoeMaxT, (long long)T);
+    return TTQ_OK;
+}
+
+// X, C and Y are checked by the caller.
+ttq_status check_adapters(const ttq_adapters* ad, int64_t T, int64_t K) {
+    TTQ_REQUIRE(ad != nullptr, "adapters: null pointer");
+    TTQ_REQUIRE(dtype_ok(ad->dt), "adapters: unknown dtype %d", ad->dt);
+    TTQ_REQUIRE(ad->n >= 0 && ad->n <= kMaxAdapters, "adapters: n must be in [0, %d]", (int)kMaxAdapters);
+    TTQ_REQUIRE(ad->rank >= 1 && ad->rank <= kMaxRank, "adapters: rank must be in [1, %d] (got %d)", kMaxRank, ad->rank);
+    TTQ_REQUIRE(K > 0 && K <= kMaxK && K % 8 == 0, "K must be a positive multiple of 8, at most 2^18");
+    TTQ_REQUIRE(ad->n == 0 || (ad->A != nullptr && aligned(ad->A, 16) && ad->B != nullptr && aligned(ad->B, 16)),
+                "adapters: A or B null or not 16-byte aligned");
+    TTQ_REQUIRE(aligned(ad->ranks, 4) && aligned(ad->scale, 4), "adapters: ranks or scale misaligned");
+    TTQ_REQUIRE(T == 0 || (ad->ids != nullptr && aligned(ad->ids, 4)), "adapters: ids null or misaligned");
+    return TTQ_OK;
+}
+
+ttq::AdapterTable adapter_table(const ttq_adapters* ad) {
+    return {ad->A, ad->B, ad->dt == TTQ_F32, (int)ad->n, ad->rank, ad->ranks, ad->scale, ad->ids};
+}
+
+// Workspace of ttq_qgemm_adapters: the adapters' sums, the projection in
+// fp32, the projection's own workspace.
+struct SharedLayout {
+    size_t z, c, q, total;
+};
+SharedLayout shared_layout(int64_t T, int64_t K, int64_t M, int rank) {
+    SharedLayout L{};
+    L.z = 0;
+    L.c = L.z + round_up(ttq::adapters_ws_bytes(T, K, rank));
+    L.q = L.c + round_up((size_t)T * (size_t)M * 4);
+    L.total = L.q + ws_qgemm(T, K, M);
+    return L;
+}
+
+}  // namespace
+
+extern "C" {
+
+ttq_status ttq_moe_route(const void* logits, int lt, int64_t T, int64_t E, int64_t ldl, int topk, int score,
+                         int renormalize, int32_t* ids, float* w, void* stream) {
+    g_last_error.clear();
+    TTQ_REQUIRE(dim_ok(T), "T out of range");
+    TTQ_REQUIRE(E >= 1 && E <= ttq::kMoeMaxExperts, "E (experts) must be in [1, %d]", ttq::kMoeMaxExperts);
+    TTQ_REQUIRE(topk >= 1 && topk <= E && topk <= ttq::kRouteMaxTopk, "topk must be in [1, min(E, %d)]",
+                ttq::kRouteMaxTopk);
+    TTQ_REQUIRE(dtype_ok(lt), "logits: unknown dtype %d", lt);
+    TTQ_REQUIRE(ldl >= E && ldl <= kMaxDim, "logits: row stride %lld < E", (long long)ldl);
+    TTQ_REQUIRE(score == TTQ_SCORE_SOFTMAX || score == TTQ_SCORE_SIGMOID, "score: unknown value %d", score);
+    if (T == 0) return TTQ_OK;
+    TTQ_REQUIRE(logits != nullptr && aligned(logits, esize(lt)), "logits: null or misaligned");
+    TTQ_REQUIRE(ids != nullptr && aligned(ids, 4) && w != nullptr && aligned(w, 4), "ids or w: null or misaligned");
+    return device_status(ttq::launch_moe_route(logits, lt == TTQ_F32, T, (int)E, ldl, topk, score, renormalize != 0,
+                                               ids, w, as_stream(stream)),
+                         "ttq_moe_route launch");
+}
+
+size_t ttq_moe_workspace_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E, int bits,
+                               int group) {
+    if (check_moe_sizes(T, topk, K, I, M, E, bits, group)) return 0;
+    return ttq::moe_layout(T, topk, I, M, E).total + kAlign;
+}
+
+ttq_status ttq_moe(const ttq_moe_args* a, void* ws, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    TTQ_REQUIRE(a != nullptr, "args: null pointer");
+    if (ttq_status e = check_moe_sizes(a->T, a->topk, a->K, a->I, a->M, a->E, a->bits, a->group)) return e;
+    TTQ_REQUIRE(a->act == TTQ_ACT_SILU || a->act == TTQ_ACT_GELU_TANH, "act: unknown value %d", a->act);
+    if (ttq_status e = check_matrix("X", a->X, a->xt, a->T, a->K, a->ldx)) return e;
+    if (ttq_status e = check_output(a->Y, a->yt, a->T, a->M, a->ldy)) return e;
+    if (a->T == 0 || a->M == 0) return TTQ_OK;
+    TTQ_REQUIRE(a->ids != nullptr && aligned(a->ids, 4) && a->w != nullptr && aligned(a->w, 4),
+                "ids or w: null or misaligned");
+    if (ttq_status e = check_experts("gate_up", a->gate_up, a->K)) return e;
+    if (ttq_status e = check_experts("down", a->down, a->I)) return e;
+    if (ttq_status e = check_ws(ws, ws_bytes, ttq::moe_layout(a->T, a->topk, a->I, a->M, a->E).total)) return e;
+    return device_status(ttq::launch_moe(a, (char*)ws, as_stream(stream)), "ttq_moe launch");
+}
+
+size_t ttq_adapters_workspace_bytes(int64_t T, int64_t K, int64_t M, int rank) {
+    if (!dim_ok(T) || !dim_ok(M) || K <= 0 || K > kMaxK || K % 8 || rank < 1 || rank > kMaxRank) return 0;
+    return round_up(ttq::adapters_ws_bytes(T, K, rank)) + kAlign;
+}
+
+ttq_status ttq_adapters_add(const void* X, int xt, int64_t T, int64_t K, int64_t ldx, const ttq_adapters* ad,
+                            int64_t M, const void* C, int64_t ldc, void* Y, int yt, int64_t ldy, void* ws,
+                            size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    TTQ_REQUIRE(dim_ok(T) && dim_ok(M), "T or M out of range");
+    if (ttq_status e = check_adapters(ad, T, K)) return e;
+    if (ttq_status e = check_matrix("X", X, xt, T, K, ldx)) return e;
+    if (ttq_status e = check_output(Y, yt, T, M, ldy)) return e;
+    if (C != nullptr) {
+        TTQ_REQUIRE(aligned(C, esize(yt)), "C: pointer not aligned to its element size");
+        TTQ_REQUIRE(ldc >= M && ldc <= kMaxDim, "C: row stride %lld < row length %lld", (long long)ldc, (long long)M);
+        TTQ_REQUIRE(C != Y || ldc == ldy, "C: in place with another row stride than Y");
+    }
+    if (T == 0 || M == 0) return TTQ_OK;
+    if (ttq_status e = check_ws(ws, ws_bytes, ttq_adapters_workspace_bytes(T, K, M, ad->rank))) return e;
+    return device_status(ttq::launch_adapters(X, xt == TTQ_F32, T, K, ldx, adapter_table(ad), C, yt == TTQ_F32, ldc, M,
+                                              Y, yt == TTQ_F32, ldy, (float*)ws, as_stream(stream)),
+                         "ttq_adapters_add launch");
+}
+
+size_t ttq_qgemm_adapters_workspace_bytes(int64_t T, int64_t K, int64_t M, int bits, int group, int rank) {
+    if (!dim_ok(T) || !dim_ok(M) || K <= 0 || K > kMaxK || K % 32 || !bits_ok(bits) || !group_ok(group) ||
+        K % group || rank < 1 || rank > kMaxRank)
+        return 0;
+    return shared_layout(T, K, M, rank).total + kAlign;
+}
+
+ttq_status ttq_qgemm_adapters(const void* X, int xt, int64_t T, int64_t K, int64_t ldx, const float* s,
+                              const int32_t* codes, const uint16_t* scale_f16, const uint16_t* zero_f16, int64_t M,
+                              int bits, int group, const ttq_adapters* ad, void* Y, int yt, int64_t ldy, void* ws,
+                              size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    TTQ_REQUIRE(dim_ok(T), "T out of range");
+    if (ttq_status e = check_quant_shape(M, K, bits, group)) return e;
+    if (ttq_status e = check_adapters(ad, T, K)) return e;
+    if (ttq_status e = check_matrix("X", X, xt, T, K, ldx)) return e;
+    if (ttq_status e = check_output(Y, yt, T, M, ldy)) return e;
+    if (T == 0 || M == 0) return TTQ_OK;
+    if (ttq_status e = check_state(s, codes, scale_f16, zero_f16, true)) return e;
+    const SharedLayout L = shared_layout(T, K, M, ad->rank);
+    if (ttq_status e = check_ws(ws, ws_bytes, L.total)) return e;
+    char* w = (char*)ws;
+    float* C = (float*)(w + L.c);
+    if (ttq_status e = ttq_qgemm(X, xt, T, K, ldx, s, codes, scale_f16, zero_f16, M, bits, group, C, TTQ_F32, M,
+                                 w + L.q, ws_qgemm(T, K, M), stream))
+        return e;
+    return device_status(ttq::launch_adapters(X, xt == TTQ_F32, T, K, ldx, adapter_table(ad), C, true, M, M, Y,
+                                              yt == TTQ_F32, ldy, (float*)(w + L.z), as_stream(stream)),
+                         "ttq_qgemm_adapters launch");
+}
+
+}  // extern "C"

@@ -23,7 +23,9 @@ TTQ_F32, TTQ_BF16 = 0, 1
 EXPORTS = ("ttq_stats", "ttq_stats_p", "ttq_awq_scales", "ttq_quantize_groups", "ttq_qgemm", "ttq_qgemm_batched",
            "ttq_lowrank_add", "ttq_lowrank_factors", "ttq_lowrank_factors_workspace_bytes",
            "ttq_workspace_bytes", "ttq_linear", "ttq_linear_shared", "ttq_linear_shared_workspace_bytes",
-           "ttq_linear_noalloc", "ttq_status_str", "ttq_last_error")
+           "ttq_linear_noalloc", "ttq_moe_route", "ttq_moe", "ttq_moe_workspace_bytes", "ttq_adapters_add",
+           "ttq_adapters_workspace_bytes", "ttq_qgemm_adapters", "ttq_qgemm_adapters_workspace_bytes",
+           "ttq_status_str", "ttq_last_error")
 
 
 class TTQError(RuntimeError):
@@ -46,6 +48,28 @@ class LinearArgs(ctypes.Structure):
         ("scale_f16", ctypes.c_void_p), ("zero_f16", ctypes.c_void_p),
         ("stage_events", ctypes.c_void_p),
     ]
+
+
+class ExpertState(ctypes.Structure):
+    _fields_ = [("s", ctypes.c_void_p), ("s_stride", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scale_f16", ctypes.c_void_p), ("zero_f16", ctypes.c_void_p)]
+
+
+class MoeArgs(ctypes.Structure):
+    _fields_ = [
+        ("X", ctypes.c_void_p), ("xt", ctypes.c_int), ("T", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("ldx", ctypes.c_int64), ("ids", ctypes.c_void_p), ("w", ctypes.c_void_p), ("topk", ctypes.c_int64),
+        ("E", ctypes.c_int64), ("I", ctypes.c_int64), ("M", ctypes.c_int64),
+        ("gate_up", ExpertState), ("down", ExpertState),
+        ("bits", ctypes.c_int), ("group", ctypes.c_int), ("act", ctypes.c_int),
+        ("Y", ctypes.c_void_p), ("yt", ctypes.c_int), ("ldy", ctypes.c_int64),
+    ]
+
+
+class AdaptersArgs(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("dt", ctypes.c_int), ("n", ctypes.c_int64),
+                ("rank", ctypes.c_int), ("ranks", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("ids", ctypes.c_void_p)]
 
 
 _lib_handle = None
@@ -76,6 +100,15 @@ def lib() -> ctypes.CDLL:
         "ttq_linear_noalloc": [ctypes.POINTER(LinearArgs), vp],
         "ttq_linear_shared": [ctypes.POINTER(LinearArgs), i32, vp, sz, vp],
         "ttq_linear_shared_workspace_bytes": [ctypes.POINTER(LinearArgs), i32],
+        "ttq_moe_route": [vp, i32, i64, i64, i64, i32, i32, i32, vp, vp, vp],
+        "ttq_moe": [ctypes.POINTER(MoeArgs), vp, sz, vp],
+        "ttq_moe_workspace_bytes": [i64, i64, i64, i64, i64, i64, i32, i32],
+        "ttq_adapters_add": [vp, i32, i64, i64, i64, ctypes.POINTER(AdaptersArgs), i64, vp, i64, vp, i32, i64, vp, sz,
+                             vp],
+        "ttq_adapters_workspace_bytes": [i64, i64, i64, i32],
+        "ttq_qgemm_adapters": [vp, i32, i64, i64, i64, vp, vp, vp, vp, i64, i32, i32, ctypes.POINTER(AdaptersArgs),
+                               vp, i32, i64, vp, sz, vp],
+        "ttq_qgemm_adapters_workspace_bytes": [i64, i64, i64, i32, i32, i32],
         "ttq_status_str": [i32],
         "ttq_last_error": [],
     }
@@ -86,6 +119,8 @@ def lib() -> ctypes.CDLL:
     L.ttq_workspace_bytes.restype = ctypes.c_size_t
     L.ttq_lowrank_factors_workspace_bytes.restype = ctypes.c_size_t
     L.ttq_linear_shared_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("ttq_moe_workspace_bytes", "ttq_adapters_workspace_bytes", "ttq_qgemm_adapters_workspace_bytes"):
+        getattr(L, name).restype = ctypes.c_size_t
     L.ttq_status_str.restype = ctypes.c_char_p
     L.ttq_last_error.restype = ctypes.c_char_p
     _lib_handle = L
@@ -401,6 +436,229 @@ def ttq_linear_shared(X: torch.Tensor, layers: list, alpha: float, lambda_rel: f
     wp, wn = _ws(ws, X.device)
     _check(lib().ttq_linear_shared(arr, len(layers), wp, wn, _stream(stream)))
     return outs
+
+
+# ------------------------------------------------------------------ weights chosen per token
+
+TTQ_SCORES = {"softmax": 0, "sigmoid": 1}
+TTQ_ACTS = {"silu": 0, "gelu": 1}
+
+
+def _on_tensor_device(fn):
+    """Run a call on its first tensor's device and on ``stream`` (default:
+    that device's current stream); what the call allocates belongs to that
+    stream."""
+    @functools.wraps(fn)
+    def call(X, *args, stream=None, **kwargs):
+        if not isinstance(X, torch.Tensor) or not X.is_cuda:
+            raise TypeError("the first argument must be a device tensor")
+        if stream is None and X.device.index == torch.cuda.current_device():
+            return fn(X, *args, stream=torch.cuda.current_stream().cuda_stream, **kwargs)
+        with torch.cuda.device(X.device):
+            ts = _torch_stream(stream)
+            with torch.cuda.stream(ts):
+                return fn(X, *args, stream=ts.cuda_stream, **kwargs)
+    return call
+
+
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device) -> int:
+    """The address of a dense tensor of this dtype and shape on this device."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {list(shape)} (got {list(t.shape)})")
+    return t.data_ptr()
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Row stride of a matrix; that of a single row does not matter."""
+    ld = _ld(t, name)
+    return ld if t.shape[0] > 1 else t.shape[1]
+
+
+def _output(Y: Optional[torch.Tensor], shape: tuple, y_dtype, device, name: str = "Y") -> torch.Tensor:
+    if Y is None:
+        return torch.empty(shape, dtype=y_dtype, device=device)
+    if Y.device != device or tuple(Y.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)} on {device}")
+    return Y
+
+
+def _scratch(ws: Optional[torch.Tensor], n: int, device) -> tuple:
+    """(address, bytes, tensor) of the workspace, allocated where none is given."""
+    if ws is None:
+        if n == 0:
+            raise ValueError("no call accepts these sizes")
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on {device}")
+    return _ws(ws, device) + (ws,)
+
+
+def _bytes_tensor(n: int, device) -> torch.Tensor:
+    if n == 0:
+        raise ValueError("no call accepts these sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+@_on_tensor_device
+def ttq_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax", renormalize: bool = False,
+                  ids: Optional[torch.Tensor] = None, w: Optional[torch.Tensor] = None, stream=None):
+    """Each token's topk experts (int32 [T][topk], -1 where none is left) and
+    their weights (float32 [T][topk]) from its logits [T][E]."""
+    if score not in TTQ_SCORES:
+        raise ValueError(f"score must be one of {sorted(TTQ_SCORES)}")
+    ld = _row_stride(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    if ids is None:
+        ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=dev)
+    if w is None:
+        w = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=dev)
+    _check(lib().ttq_moe_route(logits.data_ptr(), _dtype_code(logits), T, E, ld, topk, TTQ_SCORES[score],
+                               int(bool(renormalize)), _dense(ids, "ids", torch.int32, (T, topk), dev),
+                               _dense(w, "w", torch.float32, (T, topk), dev), stream))
+    return ids, w
+
+
+def ttq_moe_workspace_bytes(T: int, topk: int, K: int, I: int, M: int, E: int, bits: int, group: int) -> int:
+    return int(lib().ttq_moe_workspace_bytes(T, topk, K, I, M, E, bits, group))
+
+
+def moe_workspace(T: int, topk: int, K: int, I: int, M: int, E: int, bits: int, group: int,
+                  device="cuda") -> torch.Tensor:
+    """Allocate a workspace tensor of ttq_moe_workspace_bytes() bytes."""
+    return _bytes_tensor(ttq_moe_workspace_bytes(T, topk, K, I, M, E, bits, group), device)
+
+
+def _expert_state(name: str, q: dict, E: int, rows: int, K: int, bits: int, group: int, dev) -> ExpertState:
+    s = q["s"]
+    per = isinstance(s, torch.Tensor) and s.dim() == 2
+    return ExpertState(
+        s=_dense(s, f"{name} s", torch.float32, (E, K) if per else (K,), dev), s_stride=K if per else 0,
+        codes=_dense(q["codes"], f"{name} codes", torch.int32, (E, rows, K * bits // 32), dev),
+        scale_f16=_dense(q["scale_f16"], f"{name} scale_f16", torch.float16, (E, rows, K // group), dev),
+        zero_f16=_dense(q["zero_f16"], f"{name} zero_f16", torch.float16, (E, rows, K // group), dev))
+
+
+@_on_tensor_device
+def ttq_moe(X: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up: dict, down: dict, bits: int, group: int,
+            act: str = "silu", Y: Optional[torch.Tensor] = None, y_dtype=torch.float32,
+            ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A gated mixture-of-experts layer on quantized experts: X [T][K], ids
+    and w [T][topk] (ttq_moe_route); gate_up and down: dicts of ``codes``
+    [E][rows][.], ``scale_f16`` / ``zero_f16`` [E][rows][K/group] and ``s``
+    ([K], or [E][K] for scales per expert), with 2 I rows of K channels (gate
+    first) and M rows of I channels.  Returns Y [T][M]."""
+    if act not in TTQ_ACTS:
+        raise ValueError(f"act must be one of {sorted(TTQ_ACTS)}")
+    ldx = _row_stride(X, "X")
+    T, K = X.shape
+    dev = X.device
+    if ids.dim() != 2 or gate_up["codes"].dim() != 3 or down["codes"].dim() != 3:
+        raise ValueError("ids must be [T][topk] and codes [E][rows][words]")
+    topk = ids.shape[1]
+    E, rows2, _ = gate_up["codes"].shape
+    M, I = down["codes"].shape[1], rows2 // 2
+    if rows2 % 2 or bits <= 0 or group <= 0:
+        raise ValueError("gate_up must have an even number of rows; bits and group must be positive")
+    Y = _output(Y, (T, M), y_dtype, dev)
+    wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_moe_workspace_bytes(T, topk, K, I, M, E, bits, group),
+                          dev)
+    a = MoeArgs(X=X.data_ptr(), xt=_dtype_code(X), T=T, K=K, ldx=ldx,
+                ids=_dense(ids, "ids", torch.int32, (T, topk), dev), w=_dense(w, "w", torch.float32, (T, topk), dev),
+                topk=topk, E=E, I=I, M=M, gate_up=_expert_state("gate_up", gate_up, E, rows2, K, bits, group, dev),
+                down=_expert_state("down", down, E, M, I, bits, group, dev), bits=bits, group=group,
+                act=TTQ_ACTS[act], Y=Y.data_ptr(), yt=_dtype_code(Y), ldy=_row_stride(Y, "Y"))
+    _check(lib().ttq_moe(ctypes.byref(a), wp, wn, stream))
+    return Y
+
+
+def ttq_adapters_workspace_bytes(T: int, K: int, M: int, rank: int) -> int:
+    return int(lib().ttq_adapters_workspace_bytes(T, K, M, rank))
+
+
+def adapters_workspace(T: int, K: int, M: int, rank: int, device="cuda") -> torch.Tensor:
+    """Allocate a workspace tensor of ttq_adapters_workspace_bytes() bytes."""
+    return _bytes_tensor(ttq_adapters_workspace_bytes(T, K, M, rank), device)
+
+
+def _adapters(A, B, ids, ranks, scale, T: int, K: int, M: Optional[int], dev) -> AdaptersArgs:
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be [n][rank][K] and B [n][M][rank]")
+    n, rank, _ = A.shape
+    dt = _dtype_code(A)
+    return AdaptersArgs(
+        A=_dense(A, "A", A.dtype, (n, rank, K), dev),
+        B=_dense(B, "B", A.dtype, (n, B.shape[1] if M is None else M, rank), dev), dt=dt, n=n, rank=rank,
+        ranks=None if ranks is None else _dense(ranks, "ranks", torch.int32, (n,), dev),
+        scale=None if scale is None else _dense(scale, "scale", torch.float32, (n,), dev),
+        ids=_dense(ids, "ids", torch.int32, (T,), dev))
+
+
+@_on_tensor_device
+def ttq_adapters_add(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor,
+                     C: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,
+                     scale: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None, y_dtype=None,
+                     ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y[t] = C[t] + scale[a] B[a] (A[a] X[t]), a = ids[t] (outside [0, n):
+    none): A [n][rank][K], B [n][M][rank], ranks int32 [n] (rows of A in use),
+    scale float32 [n].  C (default zeros) has Y's dtype; Y=C works in place."""
+    ldx = _row_stride(X, "X")
+    T, K = X.shape
+    dev = X.device
+    ad = _adapters(A, B, ids, ranks, scale, T, K, None, dev)
+    M = B.shape[1]
+    if y_dtype is None:
+        y_dtype = torch.float32 if C is None else C.dtype
+    Y = _output(Y, (T, M), y_dtype, dev)
+    cp, ldc = None, 0
+    if C is not None:
+        _output(C, (T, M), C.dtype, dev, "C")
+        if C.dtype != Y.dtype:
+            raise TypeError("C must have Y's dtype")
+        cp, ldc = C.data_ptr(), _row_stride(C, "C")
+    wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_adapters_workspace_bytes(T, K, M, ad.rank), dev)
+    _check(lib().ttq_adapters_add(X.data_ptr(), _dtype_code(X), T, K, ldx, ctypes.byref(ad), M, cp, ldc, Y.data_ptr(),
+                                  _dtype_code(Y), _row_stride(Y, "Y"), wp, wn, stream))
+    return Y
+
+
+def ttq_qgemm_adapters_workspace_bytes(T: int, K: int, M: int, bits: int, group: int, rank: int) -> int:
+    return int(lib().ttq_qgemm_adapters_workspace_bytes(T, K, M, bits, group, rank))
+
+
+def qgemm_adapters_workspace(T: int, K: int, M: int, bits: int, group: int, rank: int, device="cuda") -> torch.Tensor:
+    """Allocate a workspace tensor of ttq_qgemm_adapters_workspace_bytes() bytes."""
+    return _bytes_tensor(ttq_qgemm_adapters_workspace_bytes(T, K, M, bits, group, rank), device)
+
+
+@_on_tensor_device
+def ttq_qgemm_adapters(X: torch.Tensor, s: torch.Tensor, codes: torch.Tensor, scale_f16: torch.Tensor,
+                       zero_f16: torch.Tensor, M: int, bits: int, group: int, A: torch.Tensor, B: torch.Tensor,
+                       ids: torch.Tensor, ranks: Optional[torch.Tensor] = None,
+                       scale: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
+                       y_dtype=torch.float32, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """ttq_qgemm on one shared quantized state plus each token's adapter (see
+    ttq_adapters_add); Y is rounded once."""
+    ldx = _row_stride(X, "X")
+    T, K = X.shape
+    dev = X.device
+    if bits <= 0 or group <= 0:
+        raise ValueError("bits and group must be positive")
+    ad = _adapters(A, B, ids, ranks, scale, T, K, M, dev)
+    Y = _output(Y, (T, M), y_dtype, dev)
+    wp, wn, ws = _scratch(
+        ws, 0 if ws is not None else lib().ttq_qgemm_adapters_workspace_bytes(T, K, M, bits, group, ad.rank), dev)
+    _check(lib().ttq_qgemm_adapters(
+        X.data_ptr(), _dtype_code(X), T, K, ldx, _dense(s, "s", torch.float32, (K,), dev),
+        _dense(codes, "codes", torch.int32, (M, K * bits // 32), dev),
+        _dense(scale_f16, "scale_f16", torch.float16, (M, K // group), dev),
+        _dense(zero_f16, "zero_f16", torch.float16, (M, K // group), dev), M, bits, group, ctypes.byref(ad),
+        Y.data_ptr(), _dtype_code(Y), _row_stride(Y, "Y"), wp, wn, stream))
+    return Y
 
 
 TTQ_LINEAR_STAGE_EVENTS = 8
