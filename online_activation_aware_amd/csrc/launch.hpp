@@ -147,30 +147,7 @@ hipError_t launch_moe_route(const void* L, bool lf32, int64_t T, int E, int64_t 
 
 // Mixture-of-experts layer (moe.hip), T <= kMoeMaxT.
 constexpr int64_t kMoeMaxT = 1024;
-struct MoeTile {
-    int expert, first, count;   // `count` slots from position `first` of the slots sorted by expert
-};
-// One of the layer's two products, for tiles of slots of one expert.
-struct MoeProduct {
-    const MoeTile* tiles;
-    const int32_t* order;       // slots sorted by expert
-    const void* X;              // rows of K: tokens (row slot / topk), or h (row slot)
-    int64_t ldx, K, rows;       // rows: outputs per slot
-    int topk, group, act;
-    const float* s;             // per expert, at s_stride
-    int64_t s_stride;
-    const uint32_t* codes;
-    const uint16_t* scale;
-    const uint16_t* zero;
-    const float* w;             // weight of each slot
-    const float* s_out;         // scales of the second product's input
-    int64_t s_out_stride;
-    float* out;                 // [slots][rows]
-};
-struct MoeLayout {
-    size_t order, tiles, h, p, total;
-};
-MoeLayout moe_layout(int64_t T, int64_t topk, int64_t I, int64_t M, int64_t E);
+size_t moe_ws_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E);
 hipError_t launch_moe(const ttq_moe_args* a, char* ws, hipStream_t st);
 
 // Adapters of many requests (adapters.hip).

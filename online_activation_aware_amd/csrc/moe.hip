@@ -12,63 +12,31 @@
 #include "codes.hpp"
 #include "common.hpp"
 #include "launch.hpp"
+#include "moe.hpp"
 
 namespace ttq {
 
-// ------------------------------------------------------------------ plan
-
-constexpr int kPlanThreads = 1024;
-
-// Upper bound of the number of tiles (up to `tile` slots of one expert).
-static int64_t moe_tiles(int64_t n, int64_t E, int64_t tile) {
-    const int64_t a = n < E ? n : E;
-    return a + (n - a) / tile;
-}
-
-// One workgroup: slots sorted by expert (slot order within an expert) into
-// `order`, and tiles {expert, first position, count} of at most `tile`
-// slots; unused tiles get count 0.
-__global__ __launch_bounds__(kPlanThreads) void k_moe_plan(const int32_t* __restrict__ ids, int n, int E, int tile,
-                                                           int ntiles, int32_t* __restrict__ order,
-                                                           MoeTile* __restrict__ tiles) {
-    __shared__ int cnt[kMoeMaxExperts], pos[kMoeMaxExperts], tpos[kMoeMaxExperts];
-    const int tid = threadIdx.x;
-    for (int e = tid; e < E; e += kPlanThreads) cnt[e] = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kPlanThreads) {
-        const int e = ids[i];
-        if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
-    }
-    __syncthreads();
-    if (tid == 0) {
-        int p = 0, q = 0;
-        for (int e = 0; e < E; ++e) {
-            pos[e] = p;
-            tpos[e] = q;
-            p += cnt[e];
-            q += (cnt[e] + tile - 1) / tile;
-        }
-    }
-    __syncthreads();
-    for (int i = tid; i < ntiles; i += kPlanThreads) tiles[i] = MoeTile{0, 0, 0};
-    __syncthreads();
-    for (int e = tid; e < E; e += kPlanThreads) {
-        for (int j = 0; j * tile < cnt[e]; ++j)
-            tiles[tpos[e] + j] = MoeTile{e, pos[e] + j * tile, min(tile, cnt[e] - j * tile)};
-        int p = pos[e];
-        if (cnt[e] > 0)
-            for (int i = 0; i < n; ++i)
-                if (ids[i] == e) order[p++] = i;
-    }
-}
+__global__ __launch_bounds__(kPlanThreads) void k_moe_plan(MoePlan a) { moe_plan(a); }
 
 // ------------------------------------------------------------------ products
 
-__device__ __forceinline__ float moe_act(float x, int act) {
-    if (act == TTQ_ACT_SILU) return x / (1.f + expf(-x));
-    const float u = 0.7978845608028654f * (x + 0.044715f * x * x * x);
-    return x * (1.f - 1.f / (1.f + expf(2.f * u)));      // x (1 + tanh u) / 2
-}
+// One of the layer's two products, for tiles of slots of one expert.
+struct MoeProduct {
+    const MoeTile* tiles;
+    const int32_t* order;       // slots sorted by expert
+    const void* X;              // rows of K: tokens (row slot / topk), or h (row slot)
+    int64_t ldx, K, rows;       // rows: outputs per slot
+    int topk, group, act;
+    const float* s;             // per expert, at s_stride
+    int64_t s_stride;
+    const uint32_t* codes;
+    const uint16_t* scale;
+    const uint16_t* zero;
+    const float* w;             // weight of each slot
+    const float* s_out;         // scales of the second product's input
+    int64_t s_out_stride;
+    float* out;                 // [slots][rows]
+};
 
 constexpr int kMtRows = 16;                       // code rows per workgroup
 constexpr int kMtTok = 4;                         // slots per tile
@@ -209,33 +177,54 @@ __global__ __launch_bounds__(kMtWaves * kWave) void k_moe_rows(MoeProduct a) {
     }
 }
 
-// Y[t] = the sum of the token's slots that have an expert, in slot order.
 template <bool YF32>
-__global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ P, const int32_t* __restrict__ ids, int topk,
-                                                 int E, int64_t M, void* __restrict__ Y, int64_t ldy) {
+__global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ P, int slices, const int32_t* __restrict__ ids,
+                                                 int topk, int E, int64_t n, int64_t M, void* __restrict__ Y,
+                                                 int64_t ldy) {
     const int64_t t = blockIdx.y, o = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (o >= M) return;
     float y = 0.f;
     for (int j = 0; j < topk; ++j) {
         const int e = ids[t * topk + j];
-        if (e >= 0 && e < E) y += P[(t * topk + j) * M + o];
+        if (e < 0 || e >= E) continue;
+        float v = P[(t * topk + j) * M + o];
+        for (int s = 1; s < slices; ++s) v += P[(s * n + t * topk + j) * M + o];
+        y += v;
     }
     if constexpr (YF32) ((float*)Y)[t * ldy + o] = y;
     else ((uint16_t*)Y)[t * ldy + o] = (uint16_t)f32_to_bf16(y);
 }
 
+hipError_t launch_moe_sum(const ttq_moe_args* a, const float* p, int slices, hipStream_t st) {
+    const dim3 grid((unsigned)((a->M + 255) / 256), (unsigned)a->T);
+    const int64_t n = a->T * a->topk;
+    return a->yt == TTQ_F32 ? launch_kernel(k_moe_sum<true>, grid, dim3(256), 0, st, nullptr, nullptr, p, slices,
+                                            a->ids, (int)a->topk, (int)a->E, n, a->M, a->Y, a->ldy)
+                            : launch_kernel(k_moe_sum<false>, grid, dim3(256), 0, st, nullptr, nullptr, p, slices,
+                                            a->ids, (int)a->topk, (int)a->E, n, a->M, a->Y, a->ldy);
+}
+
 // ------------------------------------------------------------------ host
 
-MoeLayout moe_layout(int64_t T, int64_t topk, int64_t I, int64_t M, int64_t E) {
+// Regions of both paths: the operand terms take at most 3 x 2 bytes per
+// padded channel, h in fp32 less than that.
+static MoeLayout layout(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-    const int64_t n = T * topk;
+    const int64_t n = T * topk, kp = moe_pad(K), ip = moe_pad(I);
     MoeLayout L{};
     L.order = 0;
     L.tiles = L.order + up((size_t)n * 4);
-    L.h = L.tiles + up((size_t)moe_tiles(n, E, kMtTok) * sizeof(MoeTile));
-    L.p = L.h + up((size_t)n * I * 4);
-    L.total = L.p + up((size_t)n * M * 4);
+    L.xt = L.tiles + up((size_t)moe_tiles(n, E, kMtTok) * sizeof(MoeTile));
+    L.xs = L.xt + up((size_t)n * kp * 6);
+    L.h = L.xs + up((size_t)n * (kp / 32) * 4);
+    L.hs = L.h + up((size_t)n * ip * 6);
+    L.p = L.hs + up((size_t)n * (ip / 32) * 4);
+    L.total = L.p + up((size_t)moe_slices(n, E, I, M) * n * M * 4);
     return L;
+}
+
+size_t moe_ws_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E) {
+    return layout(T, topk, K, I, M, E).total;
 }
 
 template <bool XF32, bool GU>
@@ -260,13 +249,13 @@ static hipError_t launch_rows(const MoeProduct& p, int bits, int64_t ntiles, hip
 
 hipError_t launch_moe(const ttq_moe_args* a, char* ws, hipStream_t st) {
     const int64_t n = a->T * a->topk;
-    const MoeLayout L = moe_layout(a->T, a->topk, a->I, a->M, a->E);
+    const MoeLayout L = layout(a->T, a->topk, a->K, a->I, a->M, a->E);
+    if (moe_mfma_ok(a)) return launch_moe_mfma(a, L, ws, st);
     int32_t* order = (int32_t*)(ws + L.order);
     MoeTile* tiles = (MoeTile*)(ws + L.tiles);
     const int64_t nt = moe_tiles(n, a->E, kMtTok);
-    if (hipError_t e = launch_kernel(k_moe_plan, dim3(1), dim3(kPlanThreads), 0, st, nullptr, nullptr, a->ids, (int)n,
-                                     (int)a->E, kMtTok, (int)nt, order, tiles))
-        return e;
+    const MoePlan pl{a->ids, (int)n, (int)a->E, kMtTok, (int)nt, order, tiles};
+    if (hipError_t e = launch_kernel(k_moe_plan, dim3(1), dim3(kPlanThreads), 0, st, nullptr, nullptr, pl)) return e;
     MoeProduct p{};
     p.tiles = tiles; p.order = order;
     p.X = a->X; p.ldx = a->ldx; p.K = a->K; p.rows = a->I; p.topk = (int)a->topk; p.group = a->group; p.act = a->act;
@@ -283,12 +272,7 @@ hipError_t launch_moe(const ttq_moe_args* a, char* ws, hipStream_t st) {
     d.codes = (const uint32_t*)a->down.codes; d.scale = a->down.scale_f16; d.zero = a->down.zero_f16;
     d.out = (float*)(ws + L.p);
     if (hipError_t e = launch_rows<true, false>(d, a->bits, nt, st)) return e;
-    const dim3 grid((unsigned)((a->M + 255) / 256), (unsigned)a->T);
-    return a->yt == TTQ_F32
-               ? launch_kernel(k_moe_sum<true>, grid, dim3(256), 0, st, nullptr, nullptr, (const float*)(ws + L.p),
-                               a->ids, (int)a->topk, (int)a->E, a->M, a->Y, a->ldy)
-               : launch_kernel(k_moe_sum<false>, grid, dim3(256), 0, st, nullptr, nullptr, (const float*)(ws + L.p),
-                               a->ids, (int)a->topk, (int)a->E, a->M, a->Y, a->ldy);
+    return launch_moe_sum(a, d.out, 1, st);
 }
 
 }  // namespace ttq

@@ -648,7 +648,7 @@ ttq_status ttq_moe_route(const void* logits, int lt, int64_t T, int64_t E, int64
 size_t ttq_moe_workspace_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E, int bits,
                                int group) {
     if (check_moe_sizes(T, topk, K, I, M, E, bits, group)) return 0;
-    return ttq::moe_layout(T, topk, I, M, E).total + kAlign;
+    return ttq::moe_ws_bytes(T, topk, K, I, M, E) + kAlign;
 }
 
 ttq_status ttq_moe(const ttq_moe_args* a, void* ws, size_t ws_bytes, void* stream) {
@@ -663,7 +663,7 @@ ttq_status ttq_moe(const ttq_moe_args* a, void* ws, size_t ws_bytes, void* strea
                 "ids or w: null or misaligned");
     if (ttq_status e = check_experts("gate_up", a->gate_up, a->K)) return e;
     if (ttq_status e = check_experts("down", a->down, a->I)) return e;
-    if (ttq_status e = check_ws(ws, ws_bytes, ttq::moe_layout(a->T, a->topk, a->I, a->M, a->E).total)) return e;
+    if (ttq_status e = check_ws(ws, ws_bytes, ttq::moe_ws_bytes(a->T, a->topk, a->K, a->I, a->M, a->E))) return e;
     return device_status(ttq::launch_moe(a, (char*)ws, as_stream(stream)), "ttq_moe launch");
 }
 

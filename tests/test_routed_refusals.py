@@ -63,7 +63,8 @@ def test_moe(T):
     assert L.ttq_moe(None, FAKE, BIG, None) == T.TTQ_ERR_INVALID
     assert call(T=0, X=None, ids=None, w=None, Y=None, ws=None, n=0) == T.TTQ_OK
     assert call(M=0, Y=None, ws=None, n=0) == T.TTQ_OK
-    assert T.ttq_moe_workspace_bytes(4, 2, 256, 128, 64, 8, 4, 32) > 0
+    for good in ((4, 2, 256, 128, 64, 8, 4, 32), (0, 2, 256, 128, 64, 8, 4, 32), (4, 2, 256, 128, 0, 8, 4, 32), (1024, 32, 256, 32, 1, 1, 2, 16)):
+        assert T.ttq_moe_workspace_bytes(*good) > 0    # an empty call's, too
     for bad in ((1025, 2, 256, 128, 64, 8, 4, 32), (4, 0, 256, 128, 64, 8, 4, 32), (4, 2, 100, 128, 64, 8, 4, 32), (4, 2, 256, 128, 64, 0, 4, 32),
                 (4, 2, 256, 128, 64, 8, 7, 32)):
         assert T.ttq_moe_workspace_bytes(*bad) == 0
