@@ -216,9 +216,9 @@ static MoeLayout layout(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M
     L.tiles = L.order + up((size_t)n * 4);
     L.xt = L.tiles + up((size_t)moe_tiles(n, E, kMtTok) * sizeof(MoeTile));
     L.xs = L.xt + up((size_t)n * kp * 6);
-    L.h = L.xs + up((size_t)n * (kp / 32) * 4);
+    L.h = L.xs + up((size_t)n * (kp / 16) * 4);
     L.hs = L.h + up((size_t)n * ip * 6);
-    L.p = L.hs + up((size_t)n * (ip / 32) * 4);
+    L.p = L.hs + up((size_t)n * (ip / 16) * 4);
     L.total = L.p + up((size_t)moe_slices(n, E, I, M) * n * M * 4);
     return L;
 }

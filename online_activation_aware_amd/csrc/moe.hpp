@@ -98,7 +98,7 @@ struct MoePrep {
     const int32_t* ids;
     int topk, E;
     uint16_t* xt;               // [rows][terms][kp]
-    float* xs;                  // [rows][kp / 32]
+    float* xs;                  // [rows][kp / 16]: sums of 16 channels
 };
 struct MoeMm {
     const MoeTile* tiles;
@@ -107,7 +107,7 @@ struct MoeMm {
     const uint16_t* xt;         // operand rows: slot / div
     const float* xs;
     int64_t K, kp, rows;
-    int div, per_slice, act;
+    int div, per_slice, ksplit, act;
     const uint32_t* codes;
     const uint16_t* scale;
     const uint16_t* zero;

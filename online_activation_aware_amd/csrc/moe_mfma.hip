@@ -37,7 +37,8 @@
 namespace ttq {
 
 constexpr int kMmMaxWaves = 8;
-constexpr int kMmRows = 64;                       // code rows per workgroup
+constexpr int kMmRows = 32;                       // code rows per wave
+constexpr int kMmLds = 52 * 1024;                 // x~ and its sums: two workgroups of eight waves on a compute unit
 constexpr int kMmChunk = 128;
 
 int64_t moe_pad(int64_t K) { return (K + kMmChunk - 1) / kMmChunk * kMmChunk; }
@@ -123,15 +124,21 @@ __global__ __launch_bounds__(kPlanThreads) void k_moe_prep(MoePlan pl, MoePrep a
     float sum = 0.f;
     if (in) sum = store_terms<NS>(x, a.xt + row * NS * a.kp + k0, a.kp);
     sum += __shfl_xor(sum, 1);
-    sum += __shfl_xor(sum, 2);
-    if (in && (threadIdx.x & 3) == 0) a.xs[row * (a.kp / 32) + k0 / 32] = sum;
+    if (in && (threadIdx.x & 1) == 0) a.xs[row * (a.kp / 16) + k0 / 16] = sum;
 }
 
 // ------------------------------------------------------------------ products
 
+// (x & m) | c in one instruction (the compiler makes two with literals).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t c) {
+    uint32_t r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "s"(m), "v"(c));
+    return r;
+}
+
 // The bf16 numbers 16 + q of the eight codes of a word, slot order 0 2 4 6 1 3 5 7.
 __device__ __forceinline__ u32x4 codes_plus16(uint32_t w) {
-    const uint32_t lo = ((w << 3) & 0x78787878u) | 0x80808080u, hi = ((w >> 1) & 0x78787878u) | 0x80808080u;
+    const uint32_t lo = and_or(w << 3, 0x78787878u, 0x80808080u), hi = and_or(w >> 1, 0x78787878u, 0x80808080u);
     constexpr uint32_t k41 = 0x41414141u;
     return u32x4{__builtin_amdgcn_perm(k41, lo, 0x04010400u), __builtin_amdgcn_perm(k41, lo, 0x04030402u),
                  __builtin_amdgcn_perm(k41, hi, 0x04010400u), __builtin_amdgcn_perm(k41, hi, 0x04030402u)};
@@ -147,28 +154,21 @@ __device__ __forceinline__ void exchange_quarters(u32x4& w) {
     w = u32x4{c[0], c[1], d[0], d[1]};
 }
 
-template <int GROUP, int NS>
-struct MmStage {
-    static constexpr int NG = kMmChunk / GROUP;   // groups per chunk
-    u32x4 cw[4];
-    uint32_t sw[4][(NG + 1) / 2], zw[4][(NG + 1) / 2];
-    u32x4 xa[NS][4];
-    float si;
-};
+__device__ __forceinline__ float half_of(uint32_t d, bool hi) { return f16_to_f32((uint16_t)(hi ? d >> 16 : d & 0xFFFFu)); }
 
-// NG fp16 values at byte offset `off` as packed words; W2: two-byte loads
-// (rows of the array that are aligned to nothing more).
-template <int NG, bool W2>
-__device__ __forceinline__ void load_groups(uint32_t (&d)[(NG + 1) / 2], rsrc_t r, uint32_t off) {
-    if constexpr (NG == 1) {
-        d[0] = __builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
-    } else if constexpr (W2) {
+// NH fp16 values at byte offset `off` of a buffer as packed words; W2: in
+// two-byte loads (rows of the array that are aligned to nothing more).
+template <int NH, bool W2>
+__device__ __forceinline__ void load_steps(uint32_t (&d)[NH / 2], rsrc_t r, uint32_t off) {
+    if constexpr (W2) {
 #pragma unroll
-        for (int v = 0; v < NG / 2; ++v)
+        for (int v = 0; v < NH / 2; ++v)
             d[v] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(off + 4 * v), 0, 0) |
                    ((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(off + 4 * v + 2), 0, 0) << 16);
-    } else if constexpr (NG == 2) {
-        d[0] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
+    } else if constexpr (NH == 8) {
+        const u32x4 a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+#pragma unroll
+        for (int v = 0; v < 4; ++v) d[v] = a[v];
     } else {
         const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
         d[0] = a[0];
@@ -176,214 +176,273 @@ __device__ __forceinline__ void load_groups(uint32_t (&d)[(NG + 1) / 2], rsrc_t 
     }
 }
 
-__device__ __forceinline__ float half_of(uint32_t d, bool hi) { return f16_to_f32((uint16_t)(hi ? d >> 16 : d & 0xFFFFu)); }
+constexpr int kMmBlock = 4;                       // chunks whose codes a wave has in flight
+constexpr int kMmStepLds = 3 * 1024;              // a wave's steps (fp16) and step (zero + 16) (fp32) of a block
 
 template <int GROUP, int NS, bool W2, bool GU>
-__global__ __launch_bounds__(kMmMaxWaves * kWave) void k_moe_mfma(MoeMm a) {
-    constexpr int NG = kMmChunk / GROUP;
+__global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
+    constexpr int NG = kMmChunk / GROUP;          // groups per chunk
     constexpr int SPG = GROUP / 32;               // subgroups per group
-    __shared__ f32x4 red[kMmMaxWaves][4][kWave];
+    constexpr int D = kMmBlock;
+    constexpr int NB = NG * D;                    // groups per block: 16, 8 or 4
+    constexpr int NH = NB > 8 ? 8 : NB;           // steps a lane loads
+    __shared__ __attribute__((aligned(16))) unsigned char smem[kMmLds];
+    __shared__ __attribute__((aligned(16))) unsigned char steps[kMmMaxWaves][kMmStepLds];
+    __shared__ int srow[kMmTile];
     const MoeTile tl = a.tiles[blockIdx.y];
     if (tl.count == 0) return;
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int nw = blockDim.x / kWave;
+    const int tid = threadIdx.x, nth = blockDim.x;
+    const int lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int nk = a.ksplit, kx = wave % nk;      // this wave's blocks: kx, kx + nk, ...
+    const int rw = wave / nk, nr = nth / kWave / nk;
     const int r16 = lane & 15, q = lane >> 4;
     const int64_t K = a.K, R = GU ? 2 * a.rows : a.rows;
     const int64_t wpr = K / 8, gpr = K / GROUP;
-    const int64_t o0 = (int64_t)blockIdx.x * (GU ? kMmRows / 2 : kMmRows);
+    const int64_t o0 = ((int64_t)blockIdx.x * nr + rw) * (GU ? kMmRows / 2 : kMmRows);
     const rsrc_t rc = make_rsrc(a.codes + (int64_t)tl.expert * R * wpr, R * wpr * 4);
     const rsrc_t rsc = make_rsrc(a.scale + (int64_t)tl.expert * R * gpr, R * gpr * 2);
     const rsrc_t rze = make_rsrc(a.zero + (int64_t)tl.expert * R * gpr, R * gpr * 2);
-    // Row of this lane in each column tile; rows past the end are clamped and
-    // their outputs not used.
-    uint32_t co[4], go[4];
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-        int64_t o;
-        if constexpr (GU) o = min(o0 + 16 * (rt & 1) + r16, a.rows - 1) + (rt >= 2 ? a.rows : 0);
-        else o = min(o0 + 16 * rt + r16, a.rows - 1);
-        co[rt] = (uint32_t)(o * wpr * 4 + 16 * q);
-        go[rt] = (uint32_t)(o * gpr * 2);
-    }
-    // Slot of this lane's row of the token operand (lanes past the tile's
-    // slots repeat its first one; their outputs are not used).
-    const int slot = a.order[tl.first + (r16 < tl.count ? r16 : 0)];
-    const int64_t xrow = slot / a.div;
-    // In quarter q, MFMA j takes channels 32 j + 8 q ..+7 of the chunk (the
-    // codes after the exchange of quarters), with one group per chunk
-    // 32 q + 8 j ..+7 (no exchange needed).
-    constexpr int kXq = GROUP < 128 ? 8 : 32, kXj = GROUP < 128 ? 32 : 8;
-    const uint16_t* xp = a.xt + xrow * NS * a.kp + kXq * q;
-    const float* sp = a.xs + xrow * (a.kp / 32) + q;
-
-    // Chunks of this slice, in pairs; pair p of the slice belongs to wave
-    // p % nw.  cnt: this wave's chunks.
+    // Code row of column r of column tile rt; rows past the end are clamped
+    // and their outputs not used.
+    auto row_of = [&](int rt, int r) -> int64_t {
+        if constexpr (GU) return min(o0 + r, a.rows - 1) + (rt ? a.rows : 0);
+        else return min(o0 + 16 * rt + r, a.rows - 1);
+    };
+    const uint32_t co[2] = {(uint32_t)(row_of(0, r16) * wpr * 4 + 16 * q), (uint32_t)(row_of(1, r16) * wpr * 4 + 16 * q)};
+    // Steps and zeros of a block: lane (row, part) of the 32 rows.
+    constexpr int kParts = NB / NH;
+    const int grow = lane / kParts & 31, gpart = lane % kParts;
+    const uint32_t go = (uint32_t)((row_of(grow >> 4, grow & 15) * gpr + gpart * NH) * 2);
     const int nch = (int)(a.kp / kMmChunk);
     const int cb = (int)blockIdx.z * a.per_slice;
-    const int ce = min(nch, cb + a.per_slice);
-    auto chunk = [&](int i) { return cb + 2 * ((i >> 1) * nw + wave) + (i & 1); };
-    int cnt = 0;
-    if (const int left = ce - cb - 2 * wave; left > 0) {
-        const int full = left / (2 * nw), rest = left - full * 2 * nw;
-        cnt = 2 * full + min(rest, 2);
+    const int cnt = min(nch, cb + a.per_slice) - cb;   // chunks of this slice
+
+    u32x4 ring[D][2];
+    uint32_t sw[NH / 2], zw[NH / 2];
+    auto load = [&](int u, int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt)
+            ring[u][rt] = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(co[rt] + (uint32_t)(cb + i) * 64), 0, 2));
+    };
+    auto load_sz = [&](int i) __attribute__((always_inline)) {
+        const uint32_t off = go + (uint32_t)(cb + i) * (NG * 2);
+        load_steps<NH, W2>(sw, rsc, off);
+        load_steps<NH, W2>(zw, rze, off);
+    };
+    const int b0 = D * kx;
+    if (b0 < cnt) {                               // uniform, as every condition on cnt below
+        load_sz(b0);
+#pragma unroll
+        for (int u = 0; u < D; ++u)
+            if (b0 + u < cnt) load(u, b0 + u);
     }
 
-    f32x4 acc[4];
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // Operand rows of the tile's slots; x~ and its sums of kb chunks at a
+    // time in LDS, rows 16 bytes apart modulo the banks.
+    if (tid < kMmTile) srow[tid] = a.order[tl.first + min(tid, tl.count - 1)] / a.div;
+    const int rows = tl.count;
+    constexpr int kUnit = NS * 256 + 16;          // bytes of a chunk of a row: x~ and four sums
+    static_assert(kMmLds >= kMmTile * (D * kUnit + 32), "a block of every slot's row fits");
+    int kb = (kMmLds / rows - 32) / kUnit & ~(D - 1);   // 32: the row ends; at least one block
+    kb = min(kb, (cnt + D - 1) & ~(D - 1));
+    const int rowb = NS * kb * 256 + 16, srowb = kb * 4 + 4;       // bytes; floats
+    float* ssum = (float*)(smem + rows * rowb);
+    __syncthreads();
+    auto stage = [&](int i0) __attribute__((always_inline)) {
+        const int nc = min(kb, cnt - i0);
+        const int per = NS * nc * 16;             // 16-byte pieces a row
+        for (int p = tid; p < rows * per; p += nth) {
+            const int r = p / per, w = p - r * per;
+            const int n = w / (nc * 16), k = w - n * nc * 16;
+            const u32x4 v = *(const u32x4*)(a.xt + ((int64_t)srow[r] * NS + n) * a.kp + (int64_t)(cb + i0) * kMmChunk + k * 8);
+            *(u32x4*)(smem + r * rowb + n * kb * 256 + k * 16) = v;
+        }
+        for (int p = tid; p < rows * nc * 4; p += nth) {
+            const int r = p / (nc * 4), k = p - r * nc * 4;
+            const float* s = a.xs + (int64_t)srow[r] * (a.kp / 16) + (int64_t)(cb + i0) * 8 + 2 * k;
+            ssum[r * srowb + k] = s[0] + s[1];
+        }
+    };
+    // Lanes past the tile's slots repeat its first one; their outputs are not
+    // used.  In quarter q, MFMA j takes channels 32 j + 8 q ..+7 of the chunk
+    // (the codes after the exchange of quarters), with one group per chunk
+    // 32 q + 8 j ..+7 (no exchange needed).
+    constexpr int kXq = GROUP < 128 ? 16 : 64, kXj = GROUP < 128 ? 64 : 16;
+    const int rl = r16 < rows ? r16 : 0;
+    const unsigned char* xl = smem + rl * rowb + kXq * q;
+    const float* sl = ssum + rl * srowb + q;
+    unsigned char* const my = steps[wave];
+    uint16_t* const st_l = (uint16_t*)my;         // [32][NB]
+    float* const nb_l = (float*)(my + 1024);      // [32][NB]
+    const int gq = NG == 4 ? q : NG == 2 ? q >> 1 : 0;   // group of subgroup q within a chunk
 
-    auto load = [&](MmStage<GROUP, NS>& s, int i) __attribute__((always_inline)) {
-        const uint32_t c = (uint32_t)chunk(i);
+    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    auto multiply = [&](int u, int i) __attribute__((always_inline)) {   // i: chunk within the stage
+        const float si = sl[4 * i];
+        f32x4 p[2];
+        uint32_t st[2][(NG + 1) / 2];
+        float nb[2];
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
-            s.cw[rt] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(co[rt] + c * 64), 0, 2));
+        for (int rt = 0; rt < 2; ++rt) {
+            if constexpr (GROUP < 128) exchange_quarters(ring[u][rt]);
+            p[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+            const int g = (16 * rt + r16) * NB + u * NG;
+            if constexpr (NG == 1) st[rt][0] = st_l[g];
+            else
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-            load_groups<NG, W2>(s.sw[rt], rsc, go[rt] + c * (NG * 2));
-            load_groups<NG, W2>(s.zw[rt], rze, go[rt] + c * (NG * 2));
+                for (int v = 0; v < NG / 2; ++v) st[rt][v] = ((const uint32_t*)(st_l + g))[v];
+            nb[rt] = nb_l[g + gq];
         }
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
+        for (int j = 0; j < 4; ++j) {
+            u32x4 b[2];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s.xa[n][j] = *(const u32x4*)(xp + n * a.kp + c * kMmChunk + kXj * j);
-        s.si = sp[c * 4];
-    };
-    auto multiply = [&](const MmStage<GROUP, NS>& s) __attribute__((always_inline)) {
+            for (int rt = 0; rt < 2; ++rt) b[rt] = codes_plus16(ring[u][rt][j]);
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-            u32x4 w = s.cw[rt];
-            if constexpr (GROUP < 128) exchange_quarters(w);
-            f32x4 p = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int n = NS - 1; n >= 0; --n) {
+                const u32x4 x = *(const u32x4*)(xl + n * kb * 256 + i * 256 + kXj * j);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const u32x4 b = codes_plus16(w[j]);
+                for (int rt = 0; rt < 2; ++rt) p[rt] = mfma_16x16x32(x, b[rt], p[rt]);
+            }
+            if ((j + 1) % SPG == 0) {
+                const int g = j / SPG;
 #pragma unroll
-                for (int n = NS - 1; n >= 0; --n) p = mfma_16x16x32(s.xa[n][j], b, p);
-                if ((j + 1) % SPG == 0) {
-                    const int g = j / SPG;
-                    const float st = half_of(s.sw[rt][g / 2], g & 1);
+                for (int rt = 0; rt < 2; ++rt) {
+                    const float s = half_of(st[rt][g / 2], g & 1);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[rt][e] = __builtin_fmaf(st, p[e], acc[rt][e]);
-                    p = f32x4{0.f, 0.f, 0.f, 0.f};
+                    for (int e = 0; e < 4; ++e) acc[rt][e] = __builtin_fmaf(s, p[rt][e], acc[rt][e]);
+                    p[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
                 }
             }
-            // step (zero + 16) of the group of subgroup q.
-            uint32_t sd = s.sw[rt][0], zd = s.zw[rt][0];
-            bool hi = false;
-            if constexpr (NG == 4) {
-                sd = q >= 2 ? s.sw[rt][1] : sd;
-                zd = q >= 2 ? s.zw[rt][1] : zd;
-                hi = q & 1;
-            } else if constexpr (NG == 2) {
-                hi = q >= 2;
-            }
-            const float nb = -(half_of(sd, hi) * (half_of(zd, hi) + 16.f));
-            acc[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(s.si, nb, acc[rt], 0, 0, 0);
         }
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) acc[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(si, nb[rt], acc[rt], 0, 0, 0);
     };
-    if (cnt > 0) {                                // as every condition on cnt below: wave-uniform
-        MmStage<GROUP, NS> s0, s1;
-        load(s0, 0);
-        for (int i = 0; i < cnt; i += 2) {
-            if (i + 1 < cnt) load(s1, i + 1);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(s0);
-            if (i + 1 >= cnt) break;
-            if (i + 2 < cnt) load(s0, i + 2);
-            __builtin_amdgcn_sched_barrier(0);
-            multiply(s1);
+    int b = b0;                                   // first chunk of the block
+    for (int i0 = 0; i0 < cnt; i0 += kb) {
+        if (i0 > 0) __syncthreads();              // the previous chunks have been read
+        stage(i0);
+        __syncthreads();
+        const int e = min(cnt, i0 + kb);
+        for (; b < e; b += D * nk) {
+            // This block's steps into the wave's part of LDS (its reads of the
+            // block before are done: LDS operations of a wave keep their order).
+            if (lane < 32 * kParts) {
+                float nb[NH];
+#pragma unroll
+                for (int v = 0; v < NH; ++v)
+                    nb[v] = -(half_of(sw[v / 2], v & 1) * (half_of(zw[v / 2], v & 1) + 16.f));
+#pragma unroll
+                for (int v = 0; v < NH / 2; ++v) ((uint32_t*)(st_l + grow * NB + gpart * NH))[v] = sw[v];
+#pragma unroll
+                for (int v = 0; v < NH; ++v) nb_l[grow * NB + gpart * NH + v] = nb[v];
+            }
+            __builtin_amdgcn_wave_barrier();
+            const int bn = b + D * nk;
+            if (bn < cnt) load_sz(bn);
+#pragma unroll
+            for (int u = 0; u < D; ++u) {
+                if (b + u < e) multiply(u, b + u - i0);
+                if (bn + u < cnt) load(u, bn + u);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     }
+    if (nk > 1) {                                 // uniform: the waves of a row group added in order
+        __syncthreads();                          // x~ has been read
+        f32x4* red = (f32x4*)smem;
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) red[(wave * 2 + rt) * kWave + lane] = acc[rt];
+        __syncthreads();
+        if (kx == 0)
+            for (int w = 1; w < nk; ++w)
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt) {
+                    const f32x4 v = red[((wave + w) * 2 + rt) * kWave + lane];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[rt][e] += v[e];
+                }
+    }
+    if (kx != 0) return;
 
-    // Lane: slots 4 q + e of row r16 of each column tile.  Waves added in
-    // wave order.
+    // Lane: slots 4 q + e of row r16 of each column tile.
+    if constexpr (!GU) {
 #pragma unroll
-    for (int rt = 0; rt < 4; ++rt) red[wave][rt][lane] = acc[rt];
-    __syncthreads();
-    const int nsum = GU ? 2 : 4;
-    f32x4 sum[2];
-    for (int rt = wave; rt < nsum; rt += nw) {
-#pragma unroll
-        for (int b = 0; b < (GU ? 2 : 1); ++b) {
-            f32x4 v = red[0][rt + 2 * b][lane];
-            for (int w = 1; w < nw; ++w) {
-                const f32x4 u = red[w][rt + 2 * b][lane];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += u[e];
-            }
-            sum[b] = v;
-        }
-        if constexpr (!GU) {
+        for (int rt = 0; rt < 2; ++rt) {
             const int64_t o = o0 + 16 * rt + r16;
             if (o < a.rows) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (4 * q + e < tl.count)
-                        a.p[((int64_t)blockIdx.z * a.slots + a.order[tl.first + 4 * q + e]) * a.rows + o] = sum[0][e];
+                    if (4 * q + e < rows)
+                        a.p[((int64_t)blockIdx.z * a.slots + a.order[tl.first + 4 * q + e]) * a.rows + o] = acc[rt][e];
             }
-        } else {
-            // h = act(g) u w / s_down of 4 slots and one channel, into the
-            // gate tile's part of red (read by this wave alone so far).
-            const int64_t o = o0 + 16 * rt + r16;
-            f32x4 h;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int t = 4 * q + e;
-                h[e] = 0.f;
-                if (o < a.rows && t < tl.count) {
-                    const float f = a.w[a.order[tl.first + t]] / a.s_out[tl.expert * a.s_out_stride + o];
-                    h[e] = moe_act(sum[0][e], a.act) * sum[1][e] * f;
-                }
-            }
-            red[0][rt][lane] = h;
         }
-    }
-    if constexpr (GU) {
-        // The 32 channels of 16 slots as the second product's operand: thread
-        // (slot, 8 channels).
-        __syncthreads();
-        if (wave == 0) {
-            const int t = lane >> 2, c8 = lane & 3;   // channels 8 c8 ..+7: rows 8 (c8 & 1) ..+7 of tile c8 / 2
-            float x[8];
+    } else {
+        // h = act(g) u w / s_down of 4 slots and one channel; through the
+        // wave's part of LDS to the second product's operand: lane (slot, 8
+        // channels).
+        const int64_t o = o0 + r16;
+        f32x4 h;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float* v = (const float*)&red[0][c8 >> 1][16 * (t >> 2) + 8 * (c8 & 1) + e];
-                x[e] = v[t & 3];
+        for (int e = 0; e < 4; ++e) {
+            const int t = 4 * q + e;
+            h[e] = 0.f;
+            if (o < a.rows && t < rows) {
+                const float f = a.w[a.order[tl.first + t]] / a.s_out[tl.expert * a.s_out_stride + o];
+                h[e] = moe_act(acc[0][e], a.act) * acc[1][e] * f;
             }
-            const bool in = t < tl.count;
-            const int64_t hs = a.order[tl.first + (in ? t : 0)];
-            float s = 0.f;
-            if (in) s = store_terms<NS>(x, a.ht + hs * NS * a.hp + o0 + 8 * c8, a.hp);
-            s += __shfl_xor(s, 1);
-            s += __shfl_xor(s, 2);
-            if (in && c8 == 0) a.hs[hs * (a.hp / 32) + o0 / 32] = s;
         }
+        f32x4* hb = (f32x4*)my;
+        __builtin_amdgcn_wave_barrier();
+        hb[lane] = h;
+        __builtin_amdgcn_wave_barrier();
+        const int t = (lane >> 1) & 15, c8 = lane & 1;
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = ((const float*)&hb[16 * (t >> 2) + 8 * c8 + e])[t & 3];
+        const bool in = lane < 32 && t < rows && o0 < a.hp;
+        const int64_t hs = a.order[tl.first + (in ? t : 0)];
+        float s = 0.f;
+        if (in) s = store_terms<NS>(x, a.ht + hs * NS * a.hp + o0 + 8 * c8, a.hp);
+        s += __shfl_xor(s, 1);
+        if (in && c8 == 0) a.hs[hs * (a.hp / 16) + o0 / 16] = s;
     }
 }
 
 // ------------------------------------------------------------------ host
 
-// Waves of a workgroup: one per pair of chunks, at most eight.
-static int mm_waves(int64_t chunks) {
-    const int64_t p = (chunks + 1) / 2;
-    return (int)(p < kMmMaxWaves ? p : kMmMaxWaves);
+// Waves of a workgroup: row groups of 32 code rows (they share x~ in LDS), up
+// to eight; fewer where the chip would not get two workgroups per compute
+// unit.  Where there are fewer than 4096 waves (four per SIMD), the blocks of
+// a row group's channels go to up to four waves.
+struct MmShape {
+    int nr, nk;
+};
+static MmShape mm_shape(int64_t waves, int64_t tiles, int64_t chunks) {
+    MmShape s{kMmMaxWaves, 1};
+    while (s.nk < 4 && waves * tiles * s.nk < 3072 && chunks >= 2 * kMmBlock * s.nk) s.nk *= 2;
+    s.nr = kMmMaxWaves / s.nk;
+    while (s.nr > 1 && s.nr * s.nk > 2 && (waves + s.nr - 1) / s.nr * tiles < 512) s.nr /= 2;
+    return s;
 }
 
-// Slices of the second product's channels: enough workgroups for every
-// compute unit, at least 16 chunks (a round of eight waves) each.
+// Slices of the second product's channels: enough waves to fill the chip, at
+// least eight chunks each.
 int moe_slices(int64_t n, int64_t E, int64_t I, int64_t M) {
-    const int64_t tiles = moe_tiles(n, E, kMmTile), wgs = (M + kMmRows - 1) / kMmRows * tiles;
-    const int64_t chunks = moe_pad(I) / kMmChunk, most = chunks / 16 > 0 ? chunks / 16 : 1;
-    if (wgs == 0) return 1;                       // an empty call
-    int64_t s = (512 + wgs - 1) / wgs;
+    const int64_t tiles = moe_tiles(n, E, kMmTile), waves = (M + kMmRows - 1) / kMmRows * tiles;
+    if (waves == 0) return 1;                     // an empty call
+    const int64_t chunks = moe_pad(I) / kMmChunk, most = chunks / 8 > 0 ? chunks / 8 : 1;
+    int64_t s = (2048 + waves - 1) / waves;
     if (s > most) s = most;
     return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
 }
 
 template <int NS, bool GU>
 static hipError_t launch_mm(const MoeMm& p, int group, dim3 grid, int waves, hipStream_t st) {
-    const bool w2 = p.K % 128 != 0;
+    // Steps of a block (four chunks) in one or two 16- or 8-byte loads where the rows of the array keep that alignment.
+    const bool w2 = p.K / group * 2 % (group == 128 ? 8 : 16) != 0;
 #define TTQ_MM(G)                                                                                                     \
     return w2 ? launch_kernel(k_moe_mfma<G, NS, true, GU>, grid, dim3(waves * kWave), 0, st, nullptr, nullptr, p)     \
               : launch_kernel(k_moe_mfma<G, NS, false, GU>, grid, dim3(waves * kWave), 0, st, nullptr, nullptr, p)
@@ -418,20 +477,26 @@ static hipError_t launch_ns(const ttq_moe_args* a, const MoeLayout& L, char* ws,
     p.per_slice = (int)(kp / kMmChunk);
     p.w = a->w; p.s_out = a->down.s; p.s_out_stride = a->down.s_stride; p.act = a->act;
     p.ht = (uint16_t*)(ws + L.h); p.hs = (float*)(ws + L.hs); p.hp = ip;
-    if (hipError_t e = launch_mm<NS, true>(p, a->group, dim3((unsigned)(ip / 32), (unsigned)nt), mm_waves(p.per_slice), st))
+    const int64_t gw = ip / 16;
+    const MmShape g = mm_shape(gw, nt, p.per_slice);
+    p.ksplit = g.nk;
+    if (hipError_t e = launch_mm<NS, true>(p, a->group, dim3((unsigned)((gw + g.nr - 1) / g.nr), (unsigned)nt),
+                                           g.nr * g.nk, st))
         return e;
     MoeMm d{};
     d.tiles = pl.tiles; d.order = pl.order; d.slots = n;
     d.xt = p.ht; d.xs = p.hs; d.K = a->I; d.kp = ip; d.rows = a->M; d.div = 1;
     d.codes = (const uint32_t*)a->down.codes; d.scale = a->down.scale_f16; d.zero = a->down.zero_f16;
     d.p = (float*)(ws + L.p);
-    const int sl = moe_slices(n, a->E, a->I, a->M);
-    const int chunks = (int)(ip / kMmChunk);
-    d.per_slice = ((chunks + sl - 1) / sl + 1) / 2 * 2;
+    const int chunks = (int)(ip / kMmChunk), sl = moe_slices(n, a->E, a->I, a->M);
+    d.per_slice = (chunks + sl - 1) / sl;
     const int nsl = (chunks + d.per_slice - 1) / d.per_slice;
+    const int64_t dw = (a->M + kMmRows - 1) / kMmRows;
+    const MmShape v = mm_shape(dw, nt * nsl, d.per_slice);
+    d.ksplit = v.nk;
     if (hipError_t e = launch_mm<NS, false>(d, a->group,
-                                            dim3((unsigned)((a->M + kMmRows - 1) / kMmRows), (unsigned)nt, (unsigned)nsl),
-                                            mm_waves(d.per_slice), st))
+                                            dim3((unsigned)((dw + v.nr - 1) / v.nr), (unsigned)nt, (unsigned)nsl),
+                                            v.nr * v.nk, st))
         return e;
     return launch_moe_sum(a, d.p, nsl, st);
 }
