@@ -439,7 +439,8 @@ typedef struct ttq_adapters {
  *   X: [T][K] (xt).  C: [T][M] of Y's dtype, stride ldc, or NULL for zeros;
  *   it may be Y itself (ldc == ldy), else it must not overlap Y.  Any order
  *   of ids is accepted; runs of tokens of one adapter (prompts) cost least.
- *   K a multiple of 8, at most 2^18.  T == 0 or M == 0 is an empty call.
+ *   K a multiple of 8, at most 2^18; ldx above 2^24 returns
+ *   TTQ_ERR_UNSUPPORTED.  T == 0 or M == 0 is an empty call.
  *   ws: ttq_adapters_workspace_bytes(T, K, M, rank) bytes, 256-byte aligned.
  */
 ttq_status ttq_adapters_add(const void* X, int xt, int64_t T, int64_t K, int64_t ldx,

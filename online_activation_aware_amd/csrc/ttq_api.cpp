@@ -570,6 +570,7 @@ ttq_status ttq_linear_shared(const ttq_linear_args* layers, int n, void* ws, siz
 namespace {
 
 constexpr int64_t kMaxAdapters = 65536;
+constexpr int64_t kMaxAdapterLdx = (int64_t)1 << 24;
 
 ttq_status check_experts(const char* name, const ttq_expert_state& q, int64_t K) {
     TTQ_REQUIRE(q.s != nullptr && aligned(q.s, 16), "%s.s: null or not 16-byte aligned", name);
@@ -592,7 +593,7 @@ ttq_status check_moe_sizes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_
 }
 
 // X, C and Y are checked by the caller.
-ttq_status check_adapters(const ttq_adapters* ad, int64_t T, int64_t K) {
+ttq_status check_adapters(const ttq_adapters* ad, int64_t T, int64_t K, int64_t ldx) {
     TTQ_REQUIRE(ad != nullptr, "adapters: null pointer");
     TTQ_REQUIRE(dtype_ok(ad->dt), "adapters: unknown dtype %d", ad->dt);
     TTQ_REQUIRE(ad->n >= 0 && ad->n <= kMaxAdapters, "adapters: n must be in [0, %d]", (int)kMaxAdapters);
@@ -602,6 +603,8 @@ ttq_status check_adapters(const ttq_adapters* ad, int64_t T, int64_t K) {
                 "adapters: A or B null or not 16-byte aligned");
     TTQ_REQUIRE(aligned(ad->ranks, 4) && aligned(ad->scale, 4), "adapters: ranks or scale misaligned");
     TTQ_REQUIRE(T == 0 || (ad->ids != nullptr && aligned(ad->ids, 4)), "adapters: ids null or misaligned");
+    if (ldx > kMaxAdapterLdx)   // 16 rows lie within one buffer descriptor
+        return fail(TTQ_ERR_UNSUPPORTED, "X: row stride above 2^24 elements");
     return TTQ_OK;
 }
 
@@ -677,7 +680,7 @@ ttq_status ttq_adapters_add(const void* X, int xt, int64_t T, int64_t K, int64_t
                             size_t ws_bytes, void* stream) {
     g_last_error.clear();
     TTQ_REQUIRE(dim_ok(T) && dim_ok(M), "T or M out of range");
-    if (ttq_status e = check_adapters(ad, T, K)) return e;
+    if (ttq_status e = check_adapters(ad, T, K, ldx)) return e;
     if (ttq_status e = check_matrix("X", X, xt, T, K, ldx)) return e;
     if (ttq_status e = check_output(Y, yt, T, M, ldy)) return e;
     if (C != nullptr) {
@@ -706,7 +709,7 @@ ttq_status ttq_qgemm_adapters(const void* X, int xt, int64_t T, int64_t K, int64
     g_last_error.clear();
     TTQ_REQUIRE(dim_ok(T), "T out of range");
     if (ttq_status e = check_quant_shape(M, K, bits, group)) return e;
-    if (ttq_status e = check_adapters(ad, T, K)) return e;
+    if (ttq_status e = check_adapters(ad, T, K, ldx)) return e;
     if (ttq_status e = check_matrix("X", X, xt, T, K, ldx)) return e;
     if (ttq_status e = check_output(Y, yt, T, M, ldy)) return e;
     if (T == 0 || M == 0) return TTQ_OK;

@@ -93,6 +93,7 @@ def test_adapters_add(T):
     for bad in (dict(K=250, ldx=256), dict(K=0), dict(xt=2), dict(ldx=128), dict(X=None), dict(X=FAKE + 4), dict(Y=None), dict(yt=5), dict(ldy=60),
                 dict(ldc=63), dict(C=FAKE + 1), dict(C=2 * FAKE, ldc=65), dict(T=-1), dict(M=-1), dict(ws=None), dict(n=8), dict(ws=FAKE + 16)):
         assert call(**bad) == T.TTQ_ERR_INVALID, bad
+    assert call(ldx=(1 << 24) + 8) == T.TTQ_ERR_UNSUPPORTED
     a = [FAKE, 1, 4, 256, 256, None, 64, FAKE, 64, FAKE, 1, 64, FAKE, BIG, None]
     assert L.ttq_adapters_add(*a) == T.TTQ_ERR_INVALID
     assert call(T=0, X=None, ad=dict(ids=None), Y=None, ws=None, n=0) == T.TTQ_OK
