@@ -444,6 +444,15 @@ TTQ_SCORES = {"softmax": 0, "sigmoid": 1}
 TTQ_ACTS = {"silu": 0, "gelu": 1}
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream(index: int) -> int:
+    """The device's current stream as a handle (the direct accessor, where
+    torch has it, costs a thirtieth of making a stream object)."""
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _on_tensor_device(fn):
     """Run a call on its first tensor's device and on ``stream`` (default:
     that device's current stream); what the call allocates belongs to that
@@ -452,22 +461,23 @@ def _on_tensor_device(fn):
     def call(X, *args, stream=None, **kwargs):
         if not isinstance(X, torch.Tensor) or not X.is_cuda:
             raise TypeError("the first argument must be a device tensor")
-        if stream is None and X.device.index == torch.cuda.current_device():
-            return fn(X, *args, stream=torch.cuda.current_stream().cuda_stream, **kwargs)
-        with torch.cuda.device(X.device):
+        index = X.get_device()
+        if stream is None and index == torch.cuda.current_device():
+            return fn(X, *args, stream=_current_stream(index), **kwargs)
+        with torch.cuda.device(index):
             ts = _torch_stream(stream)
             with torch.cuda.stream(ts):
                 return fn(X, *args, stream=ts.cuda_stream, **kwargs)
     return call
 
 
-def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device) -> int:
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
     """The address of a dense tensor of this dtype and shape on this device."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on device {device}")
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {list(shape)} (got {list(t.shape)})")
     return t.data_ptr()
 
@@ -478,23 +488,23 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     return ld if t.shape[0] > 1 else t.shape[1]
 
 
-def _output(Y: Optional[torch.Tensor], shape: tuple, y_dtype, device, name: str = "Y") -> torch.Tensor:
+def _output(Y: Optional[torch.Tensor], shape: tuple, y_dtype, X: torch.Tensor, name: str = "Y") -> torch.Tensor:
     if Y is None:
-        return torch.empty(shape, dtype=y_dtype, device=device)
-    if Y.device != device or tuple(Y.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)} on {device}")
+        return X.new_empty(shape, dtype=y_dtype)
+    if Y.get_device() != X.get_device() or Y.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} on {X.device}")
     return Y
 
 
-def _scratch(ws: Optional[torch.Tensor], n: int, device) -> tuple:
+def _scratch(ws: Optional[torch.Tensor], n: int, X: torch.Tensor) -> tuple:
     """(address, bytes, tensor) of the workspace, allocated where none is given."""
     if ws is None:
         if n == 0:
             raise ValueError("no call accepts these sizes")
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-    elif ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be contiguous on {device}")
-    return _ws(ws, device) + (ws,)
+        ws = X.new_empty(n, dtype=torch.uint8)
+    elif ws.get_device() != X.get_device() or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous on {X.device}")
+    return _ws(ws, X.device) + (ws,)
 
 
 def _bytes_tensor(n: int, device) -> torch.Tensor:
@@ -512,14 +522,19 @@ def ttq_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax", renor
         raise ValueError(f"score must be one of {sorted(TTQ_SCORES)}")
     ld = _row_stride(logits, "logits")
     T, E = logits.shape
-    dev = logits.device
+    dev = logits.get_device()
     if ids is None:
-        ids = torch.empty((T, max(topk, 0)), dtype=torch.int32, device=dev)
+        ids = logits.new_empty((T, max(topk, 0)), dtype=torch.int32)
+        ip = ids.data_ptr()
+    else:
+        ip = _dense(ids, "ids", torch.int32, (T, topk), dev)
     if w is None:
-        w = torch.empty((T, max(topk, 0)), dtype=torch.float32, device=dev)
+        w = logits.new_empty((T, max(topk, 0)), dtype=torch.float32)
+        wp = w.data_ptr()
+    else:
+        wp = _dense(w, "w", torch.float32, (T, topk), dev)
     _check(lib().ttq_moe_route(logits.data_ptr(), _dtype_code(logits), T, E, ld, topk, TTQ_SCORES[score],
-                               int(bool(renormalize)), _dense(ids, "ids", torch.int32, (T, topk), dev),
-                               _dense(w, "w", torch.float32, (T, topk), dev), stream))
+                               int(bool(renormalize)), ip, wp, stream))
     return ids, w
 
 
@@ -556,7 +571,7 @@ def ttq_moe(X: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up: dict, 
         raise ValueError(f"act must be one of {sorted(TTQ_ACTS)}")
     ldx = _row_stride(X, "X")
     T, K = X.shape
-    dev = X.device
+    dev = X.get_device()
     if ids.dim() != 2 or gate_up["codes"].dim() != 3 or down["codes"].dim() != 3:
         raise ValueError("ids must be [T][topk] and codes [E][rows][words]")
     topk = ids.shape[1]
@@ -564,9 +579,9 @@ def ttq_moe(X: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up: dict, 
     M, I = down["codes"].shape[1], rows2 // 2
     if rows2 % 2 or bits <= 0 or group <= 0:
         raise ValueError("gate_up must have an even number of rows; bits and group must be positive")
-    Y = _output(Y, (T, M), y_dtype, dev)
+    Y = _output(Y, (T, M), y_dtype, X)
     wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_moe_workspace_bytes(T, topk, K, I, M, E, bits, group),
-                          dev)
+                          X)
     a = MoeArgs(X=X.data_ptr(), xt=_dtype_code(X), T=T, K=K, ldx=ldx,
                 ids=_dense(ids, "ids", torch.int32, (T, topk), dev), w=_dense(w, "w", torch.float32, (T, topk), dev),
                 topk=topk, E=E, I=I, M=M, gate_up=_expert_state("gate_up", gate_up, E, rows2, K, bits, group, dev),
@@ -608,19 +623,19 @@ def ttq_adapters_add(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: tor
     scale float32 [n].  C (default zeros) has Y's dtype; Y=C works in place."""
     ldx = _row_stride(X, "X")
     T, K = X.shape
-    dev = X.device
+    dev = X.get_device()
     ad = _adapters(A, B, ids, ranks, scale, T, K, None, dev)
     M = B.shape[1]
     if y_dtype is None:
         y_dtype = torch.float32 if C is None else C.dtype
-    Y = _output(Y, (T, M), y_dtype, dev)
+    Y = _output(Y, (T, M), y_dtype, X)
     cp, ldc = None, 0
     if C is not None:
-        _output(C, (T, M), C.dtype, dev, "C")
+        _output(C, (T, M), C.dtype, X, "C")
         if C.dtype != Y.dtype:
             raise TypeError("C must have Y's dtype")
         cp, ldc = C.data_ptr(), _row_stride(C, "C")
-    wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_adapters_workspace_bytes(T, K, M, ad.rank), dev)
+    wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_adapters_workspace_bytes(T, K, M, ad.rank), X)
     _check(lib().ttq_adapters_add(X.data_ptr(), _dtype_code(X), T, K, ldx, ctypes.byref(ad), M, cp, ldc, Y.data_ptr(),
                                   _dtype_code(Y), _row_stride(Y, "Y"), wp, wn, stream))
     return Y
@@ -645,13 +660,13 @@ def ttq_qgemm_adapters(X: torch.Tensor, s: torch.Tensor, codes: torch.Tensor, sc
     ttq_adapters_add); Y is rounded once."""
     ldx = _row_stride(X, "X")
     T, K = X.shape
-    dev = X.device
+    dev = X.get_device()
     if bits <= 0 or group <= 0:
         raise ValueError("bits and group must be positive")
     ad = _adapters(A, B, ids, ranks, scale, T, K, M, dev)
-    Y = _output(Y, (T, M), y_dtype, dev)
+    Y = _output(Y, (T, M), y_dtype, X)
     wp, wn, ws = _scratch(
-        ws, 0 if ws is not None else lib().ttq_qgemm_adapters_workspace_bytes(T, K, M, bits, group, ad.rank), dev)
+        ws, 0 if ws is not None else lib().ttq_qgemm_adapters_workspace_bytes(T, K, M, bits, group, ad.rank), X)
     _check(lib().ttq_qgemm_adapters(
         X.data_ptr(), _dtype_code(X), T, K, ldx, _dense(s, "s", torch.float32, (K,), dev),
         _dense(codes, "codes", torch.int32, (M, K * bits // 32), dev),
