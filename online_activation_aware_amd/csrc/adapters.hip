@@ -91,9 +91,10 @@ __device__ __forceinline__ int tile_adapters(int id, int rk, int* dist, int* dr,
 
 // ------------------------------------------------------------------ z
 
-// A workgroup owns 16 tokens and one K slice; its items (distinct adapter d,
-// part c of the slice) go to the waves, C parts per adapter so that few
-// adapters still use all of them.  RT: 16-row tiles of the rank.
+// A workgroup owns 16 tokens, one K slice and a share (grid.z) of the tile's
+// distinct adapters; its items (adapter d, part c of the slice) go to the
+// waves, several parts per adapter so that few adapters still use all of
+// them.  RT: 16-row tiles of the rank.
 constexpr int kAzWaves = 8;
 
 template <bool XF32, bool AF32, int RT>
@@ -113,22 +114,25 @@ __global__ __launch_bounds__(kAzWaves * kWave) void k_adapter_z(const void* __re
     const int rk = adapter_rank(ad, id);
     const int nd = tile_adapters(id, rk, dist, dr, dof);
     __syncthreads();
-    const int parts = nd == 0 ? 1 : kAzWaves / nd > 0 ? kAzWaves / nd : 1;
+    const int ng = (nd + (int)gridDim.z - 1) / (int)gridDim.z;       // adapters of this share
+    const int dbeg = (int)blockIdx.z * ng, dn = min(ng, nd - dbeg);
+    if (dn <= 0) return;
+    const int parts = kAzWaves / dn > 0 ? kAzWaves / dn : 1;
     const int64_t steps = (k1 - k0 + 31) / 32, sp = (steps + parts - 1) / parts;
     const rsrc_t rx = make_rsrc((const char*)X + t0 * ldx * XE, ((rows - 1) * ldx + K) * XE);
     const int R = ad.rank;
     // Items in rounds of one per wave; after a round its adapters' sums go out.
-    for (int base = 0; base < nd * parts; base += kAzWaves) {
-        const int item = base + wave, d = item / parts, c = item - d * parts;
+    for (int base = 0; base < dn * parts; base += kAzWaves) {
+        const int item = base + wave, d = dbeg + item / parts, c = item % parts;
         f32x4 acc[RT];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (item < nd * parts) {
+        if (item < dn * parts) {
             const int a = __builtin_amdgcn_readfirstlane(dist[d]);
             const int ra = __builtin_amdgcn_readfirstlane(dr[d]);
             const rsrc_t rA = make_rsrc((const char*)ad.A + (int64_t)a * R * K * AE, (int64_t)ra * K * AE);
             const int64_t sb = c * sp, se = min(steps, sb + sp);
-            constexpr int U = RT >= 4 ? 2 : 4;    // steps whose loads are in flight together
+            constexpr int U = XF32 || AF32 ? 2 : 4;   // steps whose loads are in flight together
             for (int64_t s0 = sb; s0 < se; s0 += U) {
                 Eight<XF32> x[U];
                 Eight<AF32> w[U][RT];
@@ -153,8 +157,8 @@ __global__ __launch_bounds__(kAzWaves * kWave) void k_adapter_z(const void* __re
         __syncthreads();
         // Lane of tile rt: z^T[16 rt + 4 q + i][r16], parts in order.
         for (int rt = wave; rt < RT; rt += kAzWaves) {
-            const int d0 = base / parts, pl = dof[r16];
-            if (pl >= d0 && pl < d0 + kAzWaves / parts) {
+            const int d0 = dbeg + base / parts, pl = dof[r16];
+            if (pl >= d0 && pl < min(d0 + kAzWaves / parts, dbeg + dn)) {
                 f32x4 z = red[(pl - d0) * parts][rt][lane];
                 for (int w = 1; w < parts; ++w) {
                     const f32x4 v = red[(pl - d0) * parts + w][rt][lane];
@@ -173,28 +177,35 @@ __global__ __launch_bounds__(kAzWaves * kWave) void k_adapter_z(const void* __re
 
 // ------------------------------------------------------------------ Y
 
-// A wave owns 16 tokens and RT 16-row tiles of M at a time; workgroup: 4
-// waves on the same tokens.  VEC: rows of B and of C and Y allow 16-byte
-// (B) and 4-value (C, Y) accesses.  ST: 32-slot steps of the rank.
+// Few tokens (or odd sizes): a wave owns 16 tokens and 16 rows of M at a time;
+// workgroup: 4 waves on the same tokens.  Its items, batches of U adapters,
+// are loaded one ahead (the first before z is summed).  VEC: R % 8 == 0.
+// ST: 32-slot steps of the rank.  C comes as `cparts` fp32 partial sums where
+// it is a projection split over K, added in order.
 constexpr int kAyWaves = 4;
 
-// Four consecutive values of C (zeros without C) as fp32.
+// Four consecutive values of C as loaded: fp32 bits, or bf16 pairs in the
+// first two words.
 template <bool CF32>
-__device__ __forceinline__ f32x4 load_c4(const void* C, int64_t i, int64_t avail, bool vec) {
-    f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (C == nullptr || avail <= 0) return v;
+__device__ __forceinline__ u32x4 load_c4(const void* C, int64_t i, int64_t avail, bool vec) {
+    u32x4 v = u32x4{0u, 0u, 0u, 0u};
     if (vec && avail >= 4) {
-        if constexpr (CF32) return *(const f32x4*)((const float*)C + i);
+        if constexpr (CF32) return *(const u32x4*)((const uint32_t*)C + i);
         const u32x2 c = *(const u32x2*)((const uint16_t*)C + i);
-        return f32x4{bf16lo_to_f32(c[0]), bf16hi_to_f32(c[0]), bf16lo_to_f32(c[1]), bf16hi_to_f32(c[1])};
+        return u32x4{c[0], c[1], 0u, 0u};
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         if (r < avail) {
-            if constexpr (CF32) v[r] = ((const float*)C)[i + r];
-            else v[r] = bf16_to_f32(((const uint16_t*)C)[i + r]);
+            if constexpr (CF32) v[r] = ((const uint32_t*)C)[i + r];
+            else v[r / 2] |= (uint32_t)((const uint16_t*)C)[i + r] << (16 * (r & 1));
         }
     return v;
+}
+template <bool CF32>
+__device__ __forceinline__ f32x4 c4_values(const u32x4& c) {
+    if constexpr (CF32) return __builtin_bit_cast(f32x4, c);
+    else return f32x4{bf16lo_to_f32(c[0]), bf16hi_to_f32(c[0]), bf16lo_to_f32(c[1]), bf16hi_to_f32(c[1])};
 }
 
 template <bool BF32, bool VEC>
@@ -270,13 +281,14 @@ __device__ __forceinline__ f32x4 mac_z(const Eight<BF32>& b, const ZOp<BF32>& z,
     return acc;
 }
 
-template <bool CF32, bool BF32, bool YF32, bool VEC, int RT, int ST>
+template <bool CF32, bool BF32, bool YF32, bool VEC, int ST>
 __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_y(const float* __restrict__ Z, int slices, int64_t T,
-                                                                AdapterTable ad, const void* C, int64_t ldc, int64_t M,
-                                                                void* Y, int64_t ldy, int blocks, int cvec, int yvec) {
+                                                                AdapterTable ad, ProjectionIn ci, int64_t M, void* Y,
+                                                                int64_t ldy, int blocks, int cvec, int yvec) {
     constexpr int BE = BF32 ? 4 : 2;
-    constexpr int U = RT == 1 ? 4 : 1;            // adapters whose rows are in flight together
+    constexpr int RT = 1, U = 4;
     constexpr int kZRow = 32 * ST + 4;
+    constexpr int kZn = 32 * ST * 16 / (kAyWaves * kWave);   // z values a thread sums
     __shared__ __attribute__((aligned(16))) float zl[16][kZRow];
     __shared__ int dist[16], dr[16], dof[16];
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -287,30 +299,80 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_y(const float* __r
     const int id = t < T ? ad.ids[t] : -1;
     const int rk = adapter_rank(ad, id);
     const int nd = tile_adapters(id, rk, dist, dr, dof);
-    // z of the tile, slices in order, times the adapters' scales.
-    {
-        const int zt = tid & 15;                  // 16 threads on each token's ranks
-        const int zr = __shfl(rk, zt);            // every wave's lanes 0..15 hold the tokens
-        const float sc = zr > 0 && ad.scale != nullptr ? ad.scale[__shfl(id, zt)] : 1.f;
-        const int64_t step = T * R;
-        for (int k = tid >> 4; k < 32 * ST; k += kAyWaves * kWave / 16) {
-            float v = 0.f;
-            if (k < zr) {
-                const float* p = Z + (t0 + zt) * R + k;
-                int i = 0;
-                for (; i + 8 <= slices; i += 8) {
-                    float x[8];
+    const int batches = nd == 0 ? 1 : (nd + U - 1) / U;
+    const int64_t wb0 = (int64_t)blockIdx.y * blocks;        // row blocks of 16 RT kAyWaves rows
+    auto row0 = [&](int bi) -> int64_t { return ((wb0 + bi) * kAyWaves + wave) * (16 * RT); };
+    int nblk = 0;                                 // blocks this wave has rows in
+    while (nblk < blocks && row0(nblk) < M) ++nblk;
+    const int items = nblk * batches;
+    sync_lds();                                   // dist, dr, dof
+
+    // z of the tile, slices in order, times the adapters' scales: the tile's
+    // 16 R values are consecutive.
+    float zv[kZn];
+    int zt[kZn], zk[kZn];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = p[(i + j) * step];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v += x[j];
-                }
-                for (; i < slices; ++i) v += p[i * step];
-            }
-            zl[zt][k] = v * sc;
-        }
+    for (int n = 0; n < kZn; ++n) {
+        const int i = tid + n * kAyWaves * kWave;
+        zt[n] = i / R;
+        zk[n] = i - zt[n] * R;
+        zv[n] = 0.f;
     }
-    __syncthreads();
+    const float sl = rk > 0 && ad.scale != nullptr ? ad.scale[id] : 1.f;
+    const int64_t zstep = T * R;
+    const float* zp = Z + t0 * R + tid;
+    for (int i0 = 0; i0 < slices; i0 += 4) {
+        float x[kZn][4];
+#pragma unroll
+        for (int n = 0; n < kZn; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[n][j] = zt[n] < 16 && t0 + zt[n] < T && i0 + j < slices
+                              ? zp[(i0 + j) * zstep + n * kAyWaves * kWave] : 0.f;
+#pragma unroll
+        for (int n = 0; n < kZn; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) zv[n] += x[n][j];
+    }
+
+    struct Item {
+        Eight<BF32> b[U][RT][ST];
+        u32x4 c[RT];
+    };
+    auto load = [&](Item& it, int i) __attribute__((always_inline)) {
+        const int bi = i / batches, d0 = (i - bi * batches) * U;
+        const int64_t o0 = row0(bi);
+        if (d0 == 0 && ci.C != nullptr)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const int64_t o = o0 + 16 * rt + 4 * q;
+                it.c[rt] = load_c4<CF32>(ci.C, t * ci.ldc + o, t < T ? M - o : 0, cvec);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (d0 + u < nd) {                    // uniform
+                const int a = __builtin_amdgcn_readfirstlane(dist[d0 + u]);
+                const int ra = __builtin_amdgcn_readfirstlane(dr[d0 + u]);
+                const rsrc_t rB = make_rsrc((const char*)ad.B + ((int64_t)a * M + o0) * R * BE,
+                                            min((int64_t)16 * RT, M - o0) * R * BE);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                    for (int s = 0; s < ST; ++s) {
+                        const int r = 16 * rt + r16;
+                        it.b[u][rt][s] = load_b<BF32, VEC>(rB, r, 32 * s + 8 * q, ra, R, o0 + r < M);
+                    }
+            }
+    };
+    Item i0, i1;
+    if (items > 0) load(i0, 0);
+#pragma unroll
+    for (int n = 0; n < kZn; ++n) {
+        const int zr = __shfl(rk, zt[n] & 15);    // lanes 0..15 of every wave hold the tokens
+        const float sc = __shfl(sl, zt[n] & 15);
+        if (zt[n] < 16) zl[zt[n]][zk[n]] = zk[n] < zr ? zv[n] * sc : 0.f;
+    }
+    sync_lds();
     ZOp<BF32> zo[ST];
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
@@ -319,55 +381,47 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_y(const float* __r
         for (int h = 0; h < 2; ++h) {
             const f32x4 v = *(const f32x4*)&zl[r16][32 * s + 8 * q + 4 * h];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) z[4 * h + e] = v[e];
+            for (int e = 0; e < 4; ++e) z[4 * h + e] = 32 * s + 8 * q + 4 * h + e < rk ? v[e] : 0.f;
         }
         zo[s] = z_operand<BF32>(z);
     }
     const int place = dof[r16];
-    // `blocks` row blocks of 16 RT kAyWaves rows per workgroup.
-    for (int bi = 0; bi < blocks; ++bi) {
-        const int64_t o0 = (((int64_t)blockIdx.y * blocks + bi) * kAyWaves + wave) * (16 * RT);
-        if (o0 >= M) break;
-        f32x4 acc[RT], c[RT];
+    f32x4 acc[RT], c[RT];
+    auto compute = [&](const Item& it, int i) __attribute__((always_inline)) {
+        const int bi = i / batches, d0 = (i - bi * batches) * U;
+        const int64_t o0 = row0(bi);
+        if (d0 == 0)
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const int64_t o = o0 + 16 * rt + 4 * q;
-            acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
-            c[rt] = load_c4<CF32>(C, t * ldc + o, t < T ? M - o : 0, cvec);
-        }
-        for (int d0 = 0; d0 < nd; d0 += U) {
-            Eight<BF32> b[U][RT][ST];
+            for (int rt = 0; rt < RT; ++rt) {
+                acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+                c[rt] = acc[rt];
+                if (ci.C != nullptr) {
+                    c[rt] = c4_values<CF32>(it.c[rt]);
+                    if constexpr (CF32)
+                        for (int p = 1; p < ci.parts; ++p) {
+                            const int64_t o = o0 + 16 * rt + 4 * q;
+                            const f32x4 v = c4_values<true>(load_c4<true>(
+                                (const float*)ci.C + p * ci.stride, t * ci.ldc + o, t < T ? M - o : 0, cvec));
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (d0 + u < nd) {                // uniform
-                    const int a = __builtin_amdgcn_readfirstlane(dist[d0 + u]);
-                    const int ra = __builtin_amdgcn_readfirstlane(dr[d0 + u]);
-                    const rsrc_t rB = make_rsrc((const char*)ad.B + ((int64_t)a * M + o0) * R * BE,
-                                                min((int64_t)16 * RT, M - o0) * R * BE);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                        for (int s = 0; s < ST; ++s) {
-                            const int r = 16 * rt + r16;
-                            b[u][rt][s] = load_b<BF32, VEC>(rB, r, 32 * s + 8 * q, ra, R, o0 + r < M);
+                            for (int e = 0; e < 4; ++e) c[rt][e] += v[e];
                         }
                 }
+            }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (d0 + u < nd) {
-                    const bool mine = place == d0 + u;
+        for (int u = 0; u < U; ++u)
+            if (d0 + u < nd) {
+                const bool mine = place == d0 + u;
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        f32x4 p = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int rt = 0; rt < RT; ++rt) {
+                    f32x4 p = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int s = 0; s < ST; ++s) p = mac_z<BF32>(b[u][rt][s], zo[s], p);
+                    for (int s = 0; s < ST; ++s) p = mac_z<BF32>(it.b[u][rt][s], zo[s], p);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[rt][e] = mine ? p[e] : acc[rt][e];
-                    }
+                    for (int e = 0; e < 4; ++e) acc[rt][e] = mine ? p[e] : acc[rt][e];
                 }
-        }
+            }
         // Lane: rows 16 rt + 4 q + i of token t.
-        if (t < T)
+        if (d0 + U >= nd && t < T)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 const int64_t o = o0 + 16 * rt + 4 * q;
@@ -376,19 +430,176 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_y(const float* __r
                 for (int e = 0; e < 4; ++e) y[e] += acc[rt][e];
                 if (o < M) store_y4<YF32>(Y, t * ldy + o, M - o, yvec, y);
             }
+    };
+    for (int i = 0; i < items; i += 2) {
+        if (i + 1 < items) load(i1, i + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(i0, i);
+        if (i + 1 >= items) break;
+        if (i + 2 < items) load(i0, i + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(i1, i + 1);
+    }
+}
+
+// 128 tokens or more, mostly runs of one adapter: a wave owns 64 rows of M,
+// keeps their B in registers and goes through four tiles of 16 tokens, the
+// next tile's z and C in flight; a tile of several adapters, or another one
+// than the last, loads its B.  Column m of row tile rt is row 16 (m / 4) +
+// 4 rt + m % 4 of the 64, so that a lane ends with 16 consecutive outputs of
+// one token.  R, M and the strides multiples of 8, 16-byte aligned C and Y.
+constexpr int kArTiles = 4;
+
+template <bool CF32, bool BF32, bool YF32, int ST>
+__global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* __restrict__ Z, int slices, int64_t T,
+                                                                   AdapterTable ad, ProjectionIn ci, int64_t M, void* Y,
+                                                                   int64_t ldy) {
+    constexpr int BE = BF32 ? 4 : 2;
+    constexpr int CW = CF32 ? 4 : 2;              // 16-byte pieces of 16 values
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r16 = lane & 15, q = lane >> 4;
+    const int64_t tb = (int64_t)blockIdx.y * (16 * kArTiles);
+    const int64_t o0 = ((int64_t)blockIdx.x * kAyWaves + wave) * 64;
+    if (o0 >= M) return;
+    const int R = ad.rank;
+    const int64_t mrows = min((int64_t)64, M - o0);
+    // Lane l: token tb + l of the four tiles.
+    const int id_l = tb + lane < T ? ad.ids[tb + lane] : -1;
+    const int rk_l = adapter_rank(ad, id_l);
+    const float sc_l = rk_l > 0 && ad.scale != nullptr ? ad.scale[id_l] : 1.f;
+
+    struct Tile {
+        u32x4 c[CW];
+        f32x4 z[ST][2];
+    };
+    const bool oin = o0 + 16 * q < M;             // 16 consecutive rows, in eights
+    auto load = [&](Tile& s, int i) __attribute__((always_inline)) {
+        const int64_t t = tb + 16 * i + r16;
+        if (t >= T) return;
+#pragma unroll
+        for (int h = 0; h < ST; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int k = 32 * h + 8 * q + 4 * e;
+                if (k < R) s.z[h][e] = *(const f32x4*)(Z + t * R + k);
+            }
+        for (int p = 1; p < slices; ++p)
+#pragma unroll
+            for (int h = 0; h < ST; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int k = 32 * h + 8 * q + 4 * e;
+                    if (k < R) {
+                        const f32x4 v = *(const f32x4*)(Z + ((int64_t)p * T + t) * R + k);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) s.z[h][e][j] += v[j];
+                    }
+                }
+        if (ci.C != nullptr) {
+            const char* cp = (const char*)ci.C + (t * ci.ldc + o0 + 16 * q) * (CF32 ? 4 : 2);
+#pragma unroll
+            for (int w = 0; w < CW; ++w)
+                if (o0 + 16 * q + w * (CF32 ? 4 : 8) < M) s.c[w] = *(const u32x4*)(cp + 16 * w);
+        }
+    };
+    Tile s0{}, s1{};
+    load(s0, 0);
+    int cur = -1;                                 // the adapter whose B is held
+    Eight<BF32> b[4][ST];
+    auto compute = [&](const Tile& s, int i) __attribute__((always_inline)) {
+        const int id = __shfl(id_l, 16 * i + r16), rk = __shfl(rk_l, 16 * i + r16);
+        const float sc = __shfl(sc_l, 16 * i + r16);
+        ZOp<BF32> zo[ST];
+#pragma unroll
+        for (int h = 0; h < ST; ++h) {
+            float z[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = 32 * h + 8 * q + e < rk ? s.z[h][e / 4][e % 4] * sc : 0.f;
+            zo[h] = z_operand<BF32>(z);
+        }
+        f32x4 acc[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        uint32_t left = (uint32_t)__ballot(rk > 0) & 0xFFFFu;
+        while (left) {                            // at most 16 rounds
+            const int f = __builtin_ctz(left);
+            const int a = __builtin_amdgcn_readlane(id, f);
+            const bool mine = rk > 0 && id == a;
+            left &= ~((uint32_t)__ballot(mine) & 0xFFFFu);
+            if (a != cur) {                       // uniform
+                cur = a;
+                const int ra = __builtin_amdgcn_readlane(rk, f);
+                const rsrc_t rB = make_rsrc((const char*)ad.B + ((int64_t)a * M + o0) * R * BE, mrows * R * BE);
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+                    for (int h = 0; h < ST; ++h) {
+                        const int r = 16 * (r16 >> 2) + 4 * rt + (r16 & 3);
+                        b[rt][h] = load_b<BF32, true>(rB, r, 32 * h + 8 * q, ra, R, r < mrows);
+                    }
+            }
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                f32x4 p = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < ST; ++h) p = mac_z<BF32>(b[rt][h], zo[h], p);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[rt][e] = mine ? p[e] : acc[rt][e];
+            }
+        }
+        // Lane: rows 16 q + 4 rt + e of token t.
+        const int64_t t = tb + 16 * i + r16;
+        if (t >= T || !oin) return;
+        if (ci.C != nullptr)
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                f32x4 c;
+                if constexpr (CF32) c = c4_values<true>(s.c[rt]);
+                else c = c4_values<false>(u32x4{s.c[rt / 2][2 * (rt & 1)], s.c[rt / 2][2 * (rt & 1) + 1], 0u, 0u});
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[rt][e] += c[e];
+            }
+        const int64_t o = o0 + 16 * q;
+        if constexpr (YF32) {
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt)
+                if (o + 4 * rt < M) *(f32x4*)((float*)Y + t * ldy + o + 4 * rt) = acc[rt];
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (o + 8 * h < M)
+                    *(u32x4*)((uint16_t*)Y + t * ldy + o + 8 * h) =
+                        u32x4{pack_bf16x2(acc[2 * h][0], acc[2 * h][1]), pack_bf16x2(acc[2 * h][2], acc[2 * h][3]),
+                              pack_bf16x2(acc[2 * h + 1][0], acc[2 * h + 1][1]),
+                              pack_bf16x2(acc[2 * h + 1][2], acc[2 * h + 1][3])};
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kArTiles; i += 2) {
+        load(s1, i + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(s0, i);
+        if (i + 2 < kArTiles) load(s0, i + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(s1, i + 1);
     }
 }
 
 // ------------------------------------------------------------------ host
 
-// K slices of z: enough workgroups (of 16 tokens and a slice) for every
-// compute unit, at least 128 channels each, at most 32 partials to add.
+// K slices of z, whose partials every workgroup of the second launch adds:
+// at most eight, of at least 256 channels.  A tile of a few requests spreads
+// over the chip by its adapters as well (four shares); 128 tokens or more
+// (runs of few adapters) by their tiles, with two slices at most where those
+// fill it.
+static int z_shares(int64_t T) { return T < 128 ? 4 : 1; }
 static int64_t z_slices(int64_t T, int64_t K, int64_t* per) {
     const int64_t tiles = (T + 15) / 16;
-    int64_t s = (512 + tiles - 1) / (tiles > 0 ? tiles : 1);
-    const int64_t most = K / 128 > 0 ? K / 128 : 1;
+    int64_t s = tiles > 0 ? (T < 128 ? 8 : (256 + tiles - 1) / tiles) : 1;
+    const int64_t most = K / 256 > 0 ? K / 256 : 1;
     s = s > most ? most : s;
-    s = s > 32 ? 32 : s < 1 ? 1 : s;
+    s = s > 8 ? 8 : s;
     *per = ((K + s - 1) / s + 31) / 32 * 32;
     return (K + *per - 1) / *per;
 }
@@ -403,7 +614,7 @@ static hipError_t launch_z(const void* X, int64_t T, int64_t K, int64_t ldx, con
                            hipStream_t st) {
     int64_t per;
     const int64_t s = z_slices(T, K, &per);
-    const dim3 grid((unsigned)((T + 15) / 16), (unsigned)s);
+    const dim3 grid((unsigned)((T + 15) / 16), (unsigned)s, (unsigned)z_shares(T));
 #define TTQ_AZ(RT)                                                                                                     \
     return launch_kernel(k_adapter_z<XF32, AF32, RT>, grid, dim3(kAzWaves * kWave), 0, st, nullptr, nullptr, X, T, K, \
                          ldx, ad, per, Z)
@@ -414,46 +625,54 @@ static hipError_t launch_z(const void* X, int64_t T, int64_t K, int64_t ldx, con
 }
 
 template <bool CF32, bool BF32, bool YF32>
-static hipError_t launch_y(const float* Z, int64_t T, int64_t K, const AdapterTable& ad, const void* C, int64_t ldc,
+static hipError_t launch_y(const float* Z, int64_t T, int64_t K, const AdapterTable& ad, const ProjectionIn& ci,
                            int64_t M, void* Y, int64_t ldy, hipStream_t st) {
     int64_t per;
     const int s = (int)z_slices(T, K, &per);
+    // Rows of four values (the vector accesses of k_adapter_y), and what
+    // k_adapter_runs needs.
     auto vec = [](const void* p, int64_t ld, bool f32) { return (uintptr_t)p % (f32 ? 16 : 8) == 0 && ld % 4 == 0; };
-    const int cv = C != nullptr && vec(C, ldc, CF32), yv = vec(Y, ldy, YF32);
-    const int64_t tiles = (T + 15) / 16;
-#define TTQ_AY3(VEC, RT, ST)                                                                                          \
-    do {                                                                                                              \
-        const int64_t rb = (M + 16 * RT * kAyWaves - 1) / (16 * RT * kAyWaves);                                       \
-        int64_t blocks = rb * tiles / 2048;                                                                           \
-        blocks = blocks < 1 ? 1 : blocks > rb ? rb : blocks;                                                          \
-        if ((rb + blocks - 1) / blocks > 65535) blocks = (rb + 65534) / 65535;                                        \
-        return launch_kernel(k_adapter_y<CF32, BF32, YF32, VEC, RT, ST>,                                              \
-                             dim3((unsigned)tiles, (unsigned)((rb + blocks - 1) / blocks)), dim3(kAyWaves * kWave),   \
-                             0, st, nullptr, nullptr, Z, s, T, ad, C, ldc, M, Y, ldy, (int)blocks, cv, yv);           \
-    } while (0)
-#define TTQ_AY2(VEC, RT)                 \
-    do {                                 \
-        if (ad.rank <= 32) TTQ_AY3(VEC, RT, 1); \
-        TTQ_AY3(VEC, RT, 2);             \
-    } while (0)
-    if (ad.rank % 8 != 0) TTQ_AY2(false, 1);
-    if (T < 128) TTQ_AY2(true, 1);
-    TTQ_AY2(true, 4);
+    auto vec16 = [](const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; };
+    const int cv = ci.C != nullptr && vec(ci.C, ci.ldc, CF32) && ci.stride % 4 == 0, yv = vec(Y, ldy, YF32);
+    if (T >= 128 && ad.rank % 8 == 0 && M % 8 == 0 && vec16(Y, ldy) && ci.parts == 1 &&
+        (ci.C == nullptr || vec16(ci.C, ci.ldc))) {
+        const dim3 grid((unsigned)((M + 64 * kAyWaves - 1) / (64 * kAyWaves)),
+                        (unsigned)((T + 16 * kArTiles - 1) / (16 * kArTiles)));
+        if (grid.y <= 65535)
+            return ad.rank <= 32
+                       ? launch_kernel(k_adapter_runs<CF32, BF32, YF32, 1>, grid, dim3(kAyWaves * kWave), 0, st, nullptr,
+                                       nullptr, Z, s, T, ad, ci, M, Y, ldy)
+                       : launch_kernel(k_adapter_runs<CF32, BF32, YF32, 2>, grid, dim3(kAyWaves * kWave), 0, st, nullptr,
+                                       nullptr, Z, s, T, ad, ci, M, Y, ldy);
+    }
+    const int64_t tiles = (T + 15) / 16, rb = (M + 16 * kAyWaves - 1) / (16 * kAyWaves);
+    int64_t blocks = rb * tiles / 2048;           // row blocks per workgroup, once the chip is full
+    blocks = blocks < 1 ? 1 : blocks > rb ? rb : blocks;
+    if ((rb + blocks - 1) / blocks > 65535) blocks = (rb + 65534) / 65535;
+    const dim3 grid((unsigned)tiles, (unsigned)((rb + blocks - 1) / blocks));
+#define TTQ_AY2(VEC, ST)                                                                                            \
+    return launch_kernel(k_adapter_y<CF32, BF32, YF32, VEC, ST>, grid, dim3(kAyWaves * kWave), 0, st, nullptr,      \
+                         nullptr, Z, s, T, ad, ci, M, Y, ldy, (int)blocks, cv, yv)
+    if (ad.rank % 8 != 0) {
+        if (ad.rank <= 32) TTQ_AY2(false, 1);
+        TTQ_AY2(false, 2);
+    }
+    if (ad.rank <= 32) TTQ_AY2(true, 1);
+    TTQ_AY2(true, 2);
 #undef TTQ_AY2
-#undef TTQ_AY3
 }
 
 hipError_t launch_adapters(const void* X, bool xf32, int64_t T, int64_t K, int64_t ldx, const AdapterTable& ad,
-                           const void* C, bool cf32, int64_t ldc, int64_t M, void* Y, bool yf32, int64_t ldy, float* Z,
+                           const ProjectionIn& ci, int64_t M, void* Y, bool yf32, int64_t ldy, float* Z,
                            hipStream_t st) {
     hipError_t e;
     if (xf32) e = ad.f32 ? launch_z<true, true>(X, T, K, ldx, ad, Z, st) : launch_z<true, false>(X, T, K, ldx, ad, Z, st);
     else e = ad.f32 ? launch_z<false, true>(X, T, K, ldx, ad, Z, st) : launch_z<false, false>(X, T, K, ldx, ad, Z, st);
     if (e != hipSuccess) return e;
-#define TTQ_AY(CF, YF)                                                                        \
-    return ad.f32 ? launch_y<CF, true, YF>(Z, T, K, ad, C, ldc, M, Y, ldy, st)                \
-                  : launch_y<CF, false, YF>(Z, T, K, ad, C, ldc, M, Y, ldy, st)
-    if (cf32) {
+#define TTQ_AY(CF, YF)                                                                 \
+    return ad.f32 ? launch_y<CF, true, YF>(Z, T, K, ad, ci, M, Y, ldy, st)             \
+                  : launch_y<CF, false, YF>(Z, T, K, ad, ci, M, Y, ldy, st)
+    if (ci.f32) {
         if (yf32) TTQ_AY(true, true);
         TTQ_AY(true, false);
     }

@@ -161,8 +161,17 @@ struct AdapterTable {
     const int32_t* ids;
 };
 size_t adapters_ws_bytes(int64_t T, int64_t K, int rank);
+// What the adapters are added to: C [T][M] (nullptr: zeros), or `parts` fp32
+// partial sums of it, `stride` floats apart.
+struct ProjectionIn {
+    const void* C;
+    bool f32;
+    int64_t ldc;
+    int parts = 1;
+    int64_t stride = 0;
+};
 hipError_t launch_adapters(const void* X, bool xf32, int64_t T, int64_t K, int64_t ldx, const AdapterTable& ad,
-                           const void* C, bool cf32, int64_t ldc, int64_t M, void* Y, bool yf32, int64_t ldy, float* Z,
+                           const ProjectionIn& c, int64_t M, void* Y, bool yf32, int64_t ldy, float* Z,
                            hipStream_t st);
 
 // ttq_linear's argument checks (clearing the calling thread's error text

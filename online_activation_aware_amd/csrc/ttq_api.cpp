@@ -690,8 +690,8 @@ ttq_status ttq_adapters_add(const void* X, int xt, int64_t T, int64_t K, int64_t
     }
     if (T == 0 || M == 0) return TTQ_OK;
     if (ttq_status e = check_ws(ws, ws_bytes, ttq_adapters_workspace_bytes(T, K, M, ad->rank))) return e;
-    return device_status(ttq::launch_adapters(X, xt == TTQ_F32, T, K, ldx, adapter_table(ad), C, yt == TTQ_F32, ldc, M,
-                                              Y, yt == TTQ_F32, ldy, (float*)ws, as_stream(stream)),
+    return device_status(ttq::launch_adapters(X, xt == TTQ_F32, T, K, ldx, adapter_table(ad), {C, yt == TTQ_F32, ldc},
+                                              M, Y, yt == TTQ_F32, ldy, (float*)ws, as_stream(stream)),
                          "ttq_adapters_add launch");
 }
 
@@ -721,7 +721,7 @@ ttq_status ttq_qgemm_adapters(const void* X, int xt, int64_t T, int64_t K, int64
     if (ttq_status e = ttq_qgemm(X, xt, T, K, ldx, s, codes, scale_f16, zero_f16, M, bits, group, C, TTQ_F32, M,
                                  w + L.q, ws_qgemm(T, K, M), stream))
         return e;
-    return device_status(ttq::launch_adapters(X, xt == TTQ_F32, T, K, ldx, adapter_table(ad), C, true, M, M, Y,
+    return device_status(ttq::launch_adapters(X, xt == TTQ_F32, T, K, ldx, adapter_table(ad), {C, true, M}, M, Y,
                                               yt == TTQ_F32, ldy, (float*)(w + L.z), as_stream(stream)),
                          "ttq_qgemm_adapters launch");
 }
