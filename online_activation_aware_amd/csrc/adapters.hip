@@ -71,22 +71,23 @@ __device__ __forceinline__ f32x4 mac32(const Eight<F32A>& u, const Eight<F32B>& 
 // into LDS by the first wave: list and ranks in `dist` and `dr`, each token's
 // place in the list, or -1, in `dof`.  Returns their number, in every wave.
 __device__ __forceinline__ int tile_adapters(int id, int rk, int* dist, int* dr, int* dof) {
-    int nd = 0, place = -1;
-    uint32_t left = (uint32_t)__ballot(rk > 0) & 0xFFFFu;
-    while (left) {                                // at most 16 rounds: each takes its first token's bit
-        const int f = __builtin_ctz(left);
-        const int a = __builtin_amdgcn_readlane(id, f), r = __builtin_amdgcn_readlane(rk, f);
-        const bool mine = rk > 0 && id == a;
-        left &= ~((uint32_t)__ballot(mine) & 0xFFFFu);
-        if (mine) place = nd;
-        if (threadIdx.x == 0) {
-            dist[nd] = a;
-            dr[nd] = r;
-        }
-        ++nd;
+    const int r16 = threadIdx.x & 15;
+    int first = r16;                              // the first token of this token's adapter
+#pragma unroll
+    for (int s = 1; s < 16; ++s) {
+        const int other = __shfl(id, (r16 - s) & 15);
+        if (s <= r16 && other == id) first = r16 - s;
     }
-    if (threadIdx.x < 16) dof[threadIdx.x] = place;
-    return nd;
+    const uint32_t lead = (uint32_t)__ballot(rk > 0 && first == r16) & 0xFFFFu;
+    const int place = rk > 0 ? __builtin_popcount(lead & ((1u << first) - 1)) : -1;
+    if (threadIdx.x < 16) {
+        dof[r16] = place;
+        if ((lead >> r16) & 1u) {
+            dist[place] = id;
+            dr[place] = rk;
+        }
+    }
+    return __builtin_popcount(lead);
 }
 
 // ------------------------------------------------------------------ z
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(kAzWaves * kWave) void k_adapter_z(const void* __re
             const int ra = __builtin_amdgcn_readfirstlane(dr[d]);
             const rsrc_t rA = make_rsrc((const char*)ad.A + (int64_t)a * R * K * AE, (int64_t)ra * K * AE);
             const int64_t sb = c * sp, se = min(steps, sb + sp);
-            constexpr int U = XF32 || AF32 ? 2 : 4;   // steps whose loads are in flight together
+            constexpr int U = XF32 || AF32 ? 2 : RT <= 2 ? 8 : 4;   // steps whose loads are in flight together
             for (int64_t s0 = sb; s0 < se; s0 += U) {
                 Eight<XF32> x[U];
                 Eight<AF32> w[U][RT];
@@ -284,9 +285,10 @@ __device__ __forceinline__ f32x4 mac_z(const Eight<BF32>& b, const ZOp<BF32>& z,
 template <bool CF32, bool BF32, bool YF32, bool VEC, int ST>
 __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_y(const float* __restrict__ Z, int slices, int64_t T,
                                                                 AdapterTable ad, ProjectionIn ci, int64_t M, void* Y,
-                                                                int64_t ldy, int blocks, int cvec, int yvec) {
+                                                                int64_t ldy, int blocks, int share, int cvec,
+                                                                int yvec) {
     constexpr int BE = BF32 ? 4 : 2;
-    constexpr int RT = 1, U = 4;
+    constexpr int U = 4;
     constexpr int kZRow = 32 * ST + 4;
     constexpr int kZn = 32 * ST * 16 / (kAyWaves * kWave);   // z values a thread sums
     __shared__ __attribute__((aligned(16))) float zl[16][kZRow];
@@ -299,9 +301,12 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_y(const float* __r
     const int id = t < T ? ad.ids[t] : -1;
     const int rk = adapter_rank(ad, id);
     const int nd = tile_adapters(id, rk, dist, dr, dof);
-    const int batches = nd == 0 ? 1 : (nd + U - 1) / U;
-    const int64_t wb0 = (int64_t)blockIdx.y * blocks;        // row blocks of 16 RT kAyWaves rows
-    auto row0 = [&](int bi) -> int64_t { return ((wb0 + bi) * kAyWaves + wave) * (16 * RT); };
+    // share: the waves on one row tile, wave j of them with the tile's adapters
+    // j, j + share, ... (1, or all four where rows alone leave the chip idle).
+    const int dw = wave % share, mine_n = nd > dw ? (nd - dw + share - 1) / share : 0;
+    const int batches = mine_n == 0 ? 1 : (mine_n + U - 1) / U;
+    const int64_t wb0 = (int64_t)blockIdx.y * blocks;        // row blocks of 16 rows per wave on its own
+    auto row0 = [&](int bi) -> int64_t { return ((wb0 + bi) * (kAyWaves / share) + wave / share) * 16; };
     int nblk = 0;                                 // blocks this wave has rows in
     while (nblk < blocks && row0(nblk) < M) ++nblk;
     const int items = nblk * batches;
@@ -335,33 +340,35 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_y(const float* __r
             for (int j = 0; j < 4; ++j) zv[n] += x[n][j];
     }
 
+    constexpr int kParts = CF32 ? 4 : 1;          // partial sums of C loaded ahead
     struct Item {
-        Eight<BF32> b[U][RT][ST];
-        u32x4 c[RT];
+        Eight<BF32> b[U][ST];
+        u32x4 c[kParts];
     };
+    const int place = dof[r16];
+    // Tokens whose outputs this wave writes.
+    const bool own = t < T && (place >= 0 ? place % share == dw : dw == 0);
     auto load = [&](Item& it, int i) __attribute__((always_inline)) {
         const int bi = i / batches, d0 = (i - bi * batches) * U;
-        const int64_t o0 = row0(bi);
+        const int64_t o0 = row0(bi), o = o0 + 4 * q;
         if (d0 == 0 && ci.C != nullptr)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const int64_t o = o0 + 16 * rt + 4 * q;
-                it.c[rt] = load_c4<CF32>(ci.C, t * ci.ldc + o, t < T ? M - o : 0, cvec);
-            }
+            for (int p = 0; p < kParts; ++p)
+                if (p < ci.parts) {
+                    const char* c = (const char*)ci.C + p * ci.stride * 4;
+                    it.c[p] = load_c4<CF32>(c, t * ci.ldc + o, own ? M - o : 0, cvec);
+                }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (d0 + u < nd) {                    // uniform
-                const int a = __builtin_amdgcn_readfirstlane(dist[d0 + u]);
-                const int ra = __builtin_amdgcn_readfirstlane(dr[d0 + u]);
+            if (d0 + u < mine_n) {                // uniform
+                const int d = dw + (d0 + u) * share;
+                const int a = __builtin_amdgcn_readfirstlane(dist[d]);
+                const int ra = __builtin_amdgcn_readfirstlane(dr[d]);
                 const rsrc_t rB = make_rsrc((const char*)ad.B + ((int64_t)a * M + o0) * R * BE,
-                                            min((int64_t)16 * RT, M - o0) * R * BE);
+                                            min((int64_t)16, M - o0) * R * BE);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                    for (int s = 0; s < ST; ++s) {
-                        const int r = 16 * rt + r16;
-                        it.b[u][rt][s] = load_b<BF32, VEC>(rB, r, 32 * s + 8 * q, ra, R, o0 + r < M);
-                    }
+                for (int s = 0; s < ST; ++s)
+                    it.b[u][s] = load_b<BF32, VEC>(rB, r16, 32 * s + 8 * q, ra, R, o0 + r16 < M);
             }
     };
     Item i0, i1;
@@ -385,51 +392,47 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_y(const float* __r
         }
         zo[s] = z_operand<BF32>(z);
     }
-    const int place = dof[r16];
-    f32x4 acc[RT], c[RT];
+    f32x4 acc, c;
     auto compute = [&](const Item& it, int i) __attribute__((always_inline)) {
         const int bi = i / batches, d0 = (i - bi * batches) * U;
-        const int64_t o0 = row0(bi);
-        if (d0 == 0)
+        const int64_t o = row0(bi) + 4 * q;
+        if (d0 == 0) {
+            acc = c = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (ci.C != nullptr) {
+                c = c4_values<CF32>(it.c[0]);
+                if constexpr (CF32) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                acc[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
-                c[rt] = acc[rt];
-                if (ci.C != nullptr) {
-                    c[rt] = c4_values<CF32>(it.c[rt]);
-                    if constexpr (CF32)
-                        for (int p = 1; p < ci.parts; ++p) {
-                            const int64_t o = o0 + 16 * rt + 4 * q;
-                            const f32x4 v = c4_values<true>(load_c4<true>(
-                                (const float*)ci.C + p * ci.stride, t * ci.ldc + o, t < T ? M - o : 0, cvec));
+                    for (int p = 1; p < kParts; ++p)
+                        if (p < ci.parts) {
+                            const f32x4 v = c4_values<true>(it.c[p]);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) c[rt][e] += v[e];
+                            for (int e = 0; e < 4; ++e) c[e] += v[e];
                         }
+                    for (int p = kParts; p < ci.parts; ++p) {
+                        const f32x4 v = c4_values<true>(
+                            load_c4<true>((const float*)ci.C + p * ci.stride, t * ci.ldc + o, own ? M - o : 0, cvec));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[e] += v[e];
+                    }
                 }
             }
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (d0 + u < nd) {
-                const bool mine = place == d0 + u;
+            if (d0 + u < mine_n) {
+                const bool mine = place == dw + (d0 + u) * share;
+                f32x4 p = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    f32x4 p = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int s = 0; s < ST; ++s) p = mac_z<BF32>(it.b[u][s], zo[s], p);
 #pragma unroll
-                    for (int s = 0; s < ST; ++s) p = mac_z<BF32>(it.b[u][rt][s], zo[s], p);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[rt][e] = mine ? p[e] : acc[rt][e];
-                }
+                for (int e = 0; e < 4; ++e) acc[e] = mine ? p[e] : acc[e];
             }
-        // Lane: rows 16 rt + 4 q + i of token t.
-        if (d0 + U >= nd && t < T)
+        // Lane: rows 4 q + e of token t.
+        if (d0 + U >= mine_n && own && o < M) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const int64_t o = o0 + 16 * rt + 4 * q;
-                f32x4 y = c[rt];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] += acc[rt][e];
-                if (o < M) store_y4<YF32>(Y, t * ldy + o, M - o, yvec, y);
-            }
+            for (int e = 0; e < 4; ++e) c[e] += acc[e];
+            store_y4<YF32>(Y, t * ldy + o, M - o, yvec, c);
+        }
     };
     for (int i = 0; i < items; i += 2) {
         if (i + 1 < items) load(i1, i + 1);
@@ -589,15 +592,16 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* 
 // ------------------------------------------------------------------ host
 
 // K slices of z, whose partials every workgroup of the second launch adds:
-// at most eight, of at least 256 channels.  A tile of a few requests spreads
-// over the chip by its adapters as well (four shares); 128 tokens or more
+// at most eight, of at least 512 channels.  A tile of a few requests spreads
+// over the chip by its adapters as well (eight shares), its slices are of at
+// least 1024; 128 tokens or more
 // (runs of few adapters) by their tiles, with two slices at most where those
 // fill it.
-static int z_shares(int64_t T) { return T < 128 ? 4 : 1; }
+static int z_shares(int64_t T) { return T == 1 || T >= 128 ? 1 : 8; }
 static int64_t z_slices(int64_t T, int64_t K, int64_t* per) {
     const int64_t tiles = (T + 15) / 16;
     int64_t s = tiles > 0 ? (T < 128 ? 8 : (256 + tiles - 1) / tiles) : 1;
-    const int64_t most = K / 256 > 0 ? K / 256 : 1;
+    const int64_t least = T > 1 && T < 128 ? 1024 : 512, most = K / least > 0 ? K / least : 1;
     s = s > most ? most : s;
     s = s > 8 ? 8 : s;
     *per = ((K + s - 1) / s + 31) / 32 * 32;
@@ -645,14 +649,18 @@ static hipError_t launch_y(const float* Z, int64_t T, int64_t K, const AdapterTa
                        : launch_kernel(k_adapter_runs<CF32, BF32, YF32, 2>, grid, dim3(kAyWaves * kWave), 0, st, nullptr,
                                        nullptr, Z, s, T, ad, ci, M, Y, ldy);
     }
-    const int64_t tiles = (T + 15) / 16, rb = (M + 16 * kAyWaves - 1) / (16 * kAyWaves);
+    const int64_t tiles = (T + 15) / 16;
+    // All four waves on one row tile while that gives fewer than four waves
+    // per SIMD and there can be several adapters.
+    const int share = T > 1 && tiles * ((M + 15) / 16) * kAyWaves <= 4096 ? kAyWaves : 1;
+    const int64_t rows = 16 * (kAyWaves / share), rb = (M + rows - 1) / rows;
     int64_t blocks = rb * tiles / 2048;           // row blocks per workgroup, once the chip is full
     blocks = blocks < 1 ? 1 : blocks > rb ? rb : blocks;
     if ((rb + blocks - 1) / blocks > 65535) blocks = (rb + 65534) / 65535;
     const dim3 grid((unsigned)tiles, (unsigned)((rb + blocks - 1) / blocks));
 #define TTQ_AY2(VEC, ST)                                                                                            \
     return launch_kernel(k_adapter_y<CF32, BF32, YF32, VEC, ST>, grid, dim3(kAyWaves * kWave), 0, st, nullptr,      \
-                         nullptr, Z, s, T, ad, ci, M, Y, ldy, (int)blocks, cv, yv)
+                         nullptr, Z, s, T, ad, ci, M, Y, ldy, (int)blocks, share, cv, yv)
     if (ad.rank % 8 != 0) {
         if (ad.rank <= 32) TTQ_AY2(false, 1);
         TTQ_AY2(false, 2);

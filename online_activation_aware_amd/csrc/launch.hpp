@@ -104,7 +104,10 @@ size_t qgemv_gs_ws_bytes(int64_t T, int64_t K, int64_t M);
 hipError_t launch_qgemv_gs(const void* X, bool xf32, int64_t T, int64_t K, int64_t ldx, const float* s,
                            const uint32_t* codes, const uint16_t* scale, const uint16_t* zero, int64_t M, int bits,
                            int group, void* Y, bool yf32, int64_t ldy, void* ws, hipStream_t st,
-                           StageTimer tm = {});
+                           StageTimer tm = {}, bool partials = false);
+// K slices of the sums path.  With `partials` and several of them, the call
+// leaves their fp32 partials [slices][T][M] in ws and Y unwritten.
+int qgemv_gs_slices(int64_t T, int64_t K, int64_t M);
 // kSkMinT <= T <= 16, bf16 X, K a multiple of 128: split-K variant with an
 // fp32 partial workspace P of qgemv_sk_ws_bytes(T, K, M) bytes.
 constexpr int64_t kSkMinT = 12;

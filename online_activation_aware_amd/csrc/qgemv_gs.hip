@@ -370,11 +370,12 @@ bool qgemv_gs_eligible(int64_t T, int64_t K, int64_t M, int bits, int group, boo
 }
 
 size_t qgemv_gs_ws_bytes(int64_t T, int64_t K, int64_t M) { return gs_ws_bytes(T, K, M); }
+int qgemv_gs_slices(int64_t T, int64_t K, int64_t M) { return (int)gs_plan(T, K, M).slices; }
 
 template <int GROUP, bool YF32, int SZW>
 static hipError_t launch_gs3(const GsPlan& pl, const uint16_t* X, int64_t T, int64_t K, int64_t ldx, const float* s,
                              const uint32_t* codes, const uint16_t* scale, const uint16_t* zero, int64_t M, void* Y,
-                             int64_t ldy, void* ws, hipStream_t st, StageTimer tm) {
+                             int64_t ldy, void* ws, hipStream_t st, StageTimer tm, bool partials) {
     float* P = (float*)ws;
     const dim3 grid((unsigned)pl.rb, (unsigned)pl.slices), block((unsigned)(pl.gps * kWave));
     if (pl.slices == 1)
@@ -383,6 +384,7 @@ static hipError_t launch_gs3(const GsPlan& pl, const uint16_t* X, int64_t T, int
     if (hipError_t e = launch_kernel(k_qgemv_gs<GROUP, YF32, SZW>, grid, block, 0, st, tm.start, nullptr, X, T, K, ldx,
                                      s, codes, scale, zero, M, Y, ldy, P, pl.gps))
         return e;
+    if (partials) return hipSuccess;
     return launch_kernel(k_gs_reduce<YF32>, dim3((unsigned)((T * M + 255) / 256)), dim3(256), 0, st, nullptr, tm.stop,
                          (const float*)P, pl.slices, T, M, Y, ldy);
 }
@@ -394,13 +396,13 @@ static hipError_t launch_gs3(const GsPlan& pl, const uint16_t* X, int64_t T, int
 template <int GROUP, bool YF32>
 static hipError_t launch_gs2(const GsPlan& pl, const uint16_t* X, int64_t T, int64_t K, int64_t ldx,
                              const float* s, const uint32_t* codes, const uint16_t* scale, const uint16_t* zero,
-                             int64_t M, void* Y, int64_t ldy, void* ws, hipStream_t st, StageTimer tm) {
+                             int64_t M, void* Y, int64_t ldy, void* ws, hipStream_t st, StageTimer tm, bool partials) {
     constexpr int kSetBytes = kGsSet * (kGsChunk / GROUP) * 2;
     constexpr int kMinW = GROUP == 32 ? 8 : GROUP == 64 ? 4 : 2;
     const int64_t rowb = K / GROUP * 2;
     int w = kMinW;
     while (w < 16 && w < kSetBytes && rowb % (2 * w) == 0) w *= 2;
-#define TTQ_GS(W) return launch_gs3<GROUP, YF32, W>(pl, X, T, K, ldx, s, codes, scale, zero, M, Y, ldy, ws, st, tm)
+#define TTQ_GS(W) return launch_gs3<GROUP, YF32, W>(pl, X, T, K, ldx, s, codes, scale, zero, M, Y, ldy, ws, st, tm, partials)
     if constexpr (kSetBytes >= 16)
         if (w == 16) TTQ_GS(16);
     if (w == 8) TTQ_GS(8);
@@ -413,13 +415,14 @@ static hipError_t launch_gs2(const GsPlan& pl, const uint16_t* X, int64_t T, int
 
 hipError_t launch_qgemv_gs(const void* X, bool xf32, int64_t T, int64_t K, int64_t ldx, const float* s,
                            const uint32_t* codes, const uint16_t* scale, const uint16_t* zero, int64_t M, int bits,
-                           int group, void* Y, bool yf32, int64_t ldy, void* ws, hipStream_t st, StageTimer tm) {
+                           int group, void* Y, bool yf32, int64_t ldy, void* ws, hipStream_t st, StageTimer tm,
+                           bool partials) {
     if (!qgemv_gs_eligible(T, K, M, bits, group, xf32, ldx)) return hipErrorInvalidValue;
     const GsPlan pl = gs_plan(T, K, M);
     const uint16_t* Xb = (const uint16_t*)X;
 #define TTQ_GS2(G)                                                                                            \
-    return yf32 ? launch_gs2<G, true>(pl, Xb, T, K, ldx, s, codes, scale, zero, M, Y, ldy, ws, st, tm) \
-                : launch_gs2<G, false>(pl, Xb, T, K, ldx, s, codes, scale, zero, M, Y, ldy, ws, st, tm)
+    return yf32 ? launch_gs2<G, true>(pl, Xb, T, K, ldx, s, codes, scale, zero, M, Y, ldy, ws, st, tm, partials) \
+                : launch_gs2<G, false>(pl, Xb, T, K, ldx, s, codes, scale, zero, M, Y, ldy, ws, st, tm, partials)
     switch (group) {
         case 32: TTQ_GS2(32);
         case 64: TTQ_GS2(64);

@@ -718,11 +718,23 @@ ttq_status ttq_qgemm_adapters(const void* X, int xt, int64_t T, int64_t K, int64
     if (ttq_status e = check_ws(ws, ws_bytes, L.total)) return e;
     char* w = (char*)ws;
     float* C = (float*)(w + L.c);
-    if (ttq_status e = ttq_qgemm(X, xt, T, K, ldx, s, codes, scale_f16, zero_f16, M, bits, group, C, TTQ_F32, M,
-                                 w + L.q, ws_qgemm(T, K, M), stream))
+    const bool xf32 = xt == TTQ_F32;
+    ttq::ProjectionIn ci{C, true, M};
+    if (ttq::qgemv_gs_eligible(T, K, M, bits, group, xf32, ldx)) {
+        // The K slices' partial sums are added where the adapters are.
+        if (ttq_status e = device_status(
+                ttq::launch_qgemv_gs(X, xf32, T, K, ldx, s, (const uint32_t*)codes, scale_f16, zero_f16, M, bits, group,
+                                     C, true, M, w + L.q, as_stream(stream), {}, true),
+                "ttq_qgemm_adapters launch"))
+            return e;
+        const int parts = ttq::qgemv_gs_slices(T, K, M);
+        if (parts > 1) ci = {w + L.q, true, M, parts, T * M};
+    } else if (ttq_status e = ttq_qgemm(X, xt, T, K, ldx, s, codes, scale_f16, zero_f16, M, bits, group, C, TTQ_F32, M,
+                                        w + L.q, ws_qgemm(T, K, M), stream)) {
         return e;
-    return device_status(ttq::launch_adapters(X, xt == TTQ_F32, T, K, ldx, adapter_table(ad), {C, true, M}, M, Y,
-                                              yt == TTQ_F32, ldy, (float*)(w + L.z), as_stream(stream)),
+    }
+    return device_status(ttq::launch_adapters(X, xf32, T, K, ldx, adapter_table(ad), ci, M, Y, yt == TTQ_F32, ldy,
+                                              (float*)(w + L.z), as_stream(stream)),
                          "ttq_qgemm_adapters launch");
 }
 
