@@ -177,18 +177,27 @@ __global__ __launch_bounds__(kMtWaves * kWave) void k_moe_rows(MoeProduct a) {
     }
 }
 
+constexpr int kSumThreads = 64;
+
 template <bool YF32>
-__global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ P, int slices, const int32_t* __restrict__ ids,
+__global__ __launch_bounds__(kSumThreads) void k_moe_sum(const float* __restrict__ P, int slices, const int32_t* __restrict__ ids,
                                                  int topk, int E, int64_t n, int64_t M, void* __restrict__ Y,
                                                  int64_t ldy) {
-    const int64_t t = blockIdx.y, o = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t t = blockIdx.y, o = (int64_t)blockIdx.x * kSumThreads + threadIdx.x;
     if (o >= M) return;
     float y = 0.f;
     for (int j = 0; j < topk; ++j) {
         const int e = ids[t * topk + j];
         if (e < 0 || e >= E) continue;
-        float v = P[(t * topk + j) * M + o];
-        for (int s = 1; s < slices; ++s) v += P[(s * n + t * topk + j) * M + o];
+        const float* p = P + (t * topk + j) * M + o;
+        float v = 0.f;
+        for (int s0 = 0; s0 < slices; s0 += 8) {  // eight loads together
+            float x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = s0 + u < slices ? p[(s0 + u) * n * M] : 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) v += x[u];
+        }
         y += v;
     }
     if constexpr (YF32) ((float*)Y)[t * ldy + o] = y;
@@ -196,30 +205,31 @@ __global__ __launch_bounds__(256) void k_moe_sum(const float* __restrict__ P, in
 }
 
 hipError_t launch_moe_sum(const ttq_moe_args* a, const float* p, int slices, hipStream_t st) {
-    const dim3 grid((unsigned)((a->M + 255) / 256), (unsigned)a->T);
+    const dim3 grid((unsigned)((a->M + kSumThreads - 1) / kSumThreads), (unsigned)a->T);
     const int64_t n = a->T * a->topk;
-    return a->yt == TTQ_F32 ? launch_kernel(k_moe_sum<true>, grid, dim3(256), 0, st, nullptr, nullptr, p, slices,
+    return a->yt == TTQ_F32 ? launch_kernel(k_moe_sum<true>, grid, dim3(kSumThreads), 0, st, nullptr, nullptr, p, slices,
                                             a->ids, (int)a->topk, (int)a->E, n, a->M, a->Y, a->ldy)
-                            : launch_kernel(k_moe_sum<false>, grid, dim3(256), 0, st, nullptr, nullptr, p, slices,
+                            : launch_kernel(k_moe_sum<false>, grid, dim3(kSumThreads), 0, st, nullptr, nullptr, p, slices,
                                             a->ids, (int)a->topk, (int)a->E, n, a->M, a->Y, a->ldy);
 }
 
 // ------------------------------------------------------------------ host
 
-// Regions of both paths: the operand terms take at most 3 x 2 bytes per
-// padded channel, h in fp32 less than that.
+// Regions of all paths: an operand row takes at most 3 x 2 bytes per padded
+// channel (the bf16 terms of fp32 X), digits and fp32 h less.
 static MoeLayout layout(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E) {
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
-    const int64_t n = T * topk, kp = moe_pad(K), ip = moe_pad(I);
+    const int64_t n = T * topk, kp = moe_dot_pad(K), ip = moe_dot_pad(I);
+    const int sl = moe_slices(n, E, I, M), sd = T == 1 || T == 2 ? moe_dot_slices(n, E, I, M, (int)T) : 1;
     MoeLayout L{};
     L.order = 0;
     L.tiles = L.order + up((size_t)n * 4);
-    L.xt = L.tiles + up((size_t)moe_tiles(n, E, kMtTok) * sizeof(MoeTile));
+    L.xt = L.tiles + up((size_t)moe_tiles(n, E, 1) * sizeof(MoeTile));
     L.xs = L.xt + up((size_t)n * kp * 6);
     L.h = L.xs + up((size_t)n * (kp / 16) * 4);
     L.hs = L.h + up((size_t)n * ip * 6);
     L.p = L.hs + up((size_t)n * (ip / 16) * 4);
-    L.total = L.p + up((size_t)moe_slices(n, E, I, M) * n * M * 4);
+    L.total = L.p + up((size_t)(sl > sd ? sl : sd) * n * M * 4);
     return L;
 }
 
@@ -250,6 +260,7 @@ static hipError_t launch_rows(const MoeProduct& p, int bits, int64_t ntiles, hip
 hipError_t launch_moe(const ttq_moe_args* a, char* ws, hipStream_t st) {
     const int64_t n = a->T * a->topk;
     const MoeLayout L = layout(a->T, a->topk, a->K, a->I, a->M, a->E);
+    if (moe_dot_tile(a) > 0) return launch_moe_dot(a, L, ws, st);
     if (moe_mfma_ok(a)) return launch_moe_mfma(a, L, ws, st);
     int32_t* order = (int32_t*)(ws + L.order);
     MoeTile* tiles = (MoeTile*)(ws + L.tiles);

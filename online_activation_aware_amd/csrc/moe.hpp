@@ -3,6 +3,7 @@
 
 #include "common.hpp"
 #include "launch.hpp"
+#include "lds_dma.hpp"
 
 namespace ttq {
 
@@ -120,9 +121,95 @@ struct MoeMm {
     float* p;                   // second product: [slices][slots][rows]
 };
 
+// Eight channels from k0 of token t, divided by the scales of expert e.
+template <bool XF32>
+__device__ __forceinline__ void moe_load_scaled(float (&x)[8], const MoePrep& a, int64_t t, int64_t e, int64_t k0) {
+    if constexpr (XF32) {
+        const f32x4 u = *(const f32x4*)((const float*)a.X + t * a.ldx + k0);
+        const f32x4 v = *(const f32x4*)((const float*)a.X + t * a.ldx + k0 + 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[j] = u[j];
+            x[4 + j] = v[j];
+        }
+    } else {
+        const u32x4 u = *(const u32x4*)((const uint16_t*)a.X + t * a.ldx + k0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = bf16lo_to_f32(u[j]);
+            x[2 * j + 1] = bf16hi_to_f32(u[j]);
+        }
+    }
+    const float* s = a.s + e * a.s_stride + k0;
+    const f32x4 u = *(const f32x4*)s, v = *(const f32x4*)(s + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[j] /= u[j];
+        x[4 + j] /= v[j];
+    }
+}
+
+// NH fp16 values (4, 8 or 16) at byte offset `off` of a buffer as packed
+// words, in loads of up to 16 bytes; W2: of two bytes (rows of the array that
+// are aligned to nothing more).
+template <int NH, bool W2>
+__device__ __forceinline__ void moe_load_halves(uint32_t (&d)[NH / 2], rsrc_t r, uint32_t off) {
+    if constexpr (W2) {
+#pragma unroll
+        for (int v = 0; v < NH / 2; ++v)
+            d[v] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(off + 4 * v), 0, 0) |
+                   ((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(off + 4 * v + 2), 0, 0) << 16);
+    } else if constexpr (NH >= 8) {
+#pragma unroll
+        for (int h = 0; h < NH / 8; ++h) {
+            const u32x4 a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(off + 16 * h), 0, 0));
+#pragma unroll
+            for (int v = 0; v < 4; ++v) d[4 * h + v] = a[v];
+        }
+    } else {
+        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
+        d[0] = a[0];
+        d[1] = a[1];
+    }
+}
+
+// The rows of X as the first product's operand, kp padded channels.
+inline MoePrep moe_prep_of(const ttq_moe_args* a, int64_t kp) {
+    MoePrep pr{};
+    pr.X = a->X; pr.ldx = a->ldx; pr.K = a->K; pr.kp = kp;
+    pr.s = a->gate_up.s; pr.s_stride = a->gate_up.s_stride;
+    pr.rows = pr.s_stride ? a->T * a->topk : a->T; pr.ids = a->ids; pr.topk = (int)a->topk; pr.E = (int)a->E;
+    return pr;
+}
+
 bool moe_mfma_ok(const ttq_moe_args* a);
 int64_t moe_pad(int64_t K);
 int moe_slices(int64_t n, int64_t E, int64_t I, int64_t M);
 hipError_t launch_moe_mfma(const ttq_moe_args* a, const MoeLayout& L, char* ws, hipStream_t st);
+
+// ---- integer dot products (moe_dot.hip): the same codes, one or two slots a tile
+
+struct MoeDot {
+    const MoeTile* tiles;
+    const int32_t* order;
+    int64_t slots;
+    const uint32_t* xq;         // operand rows: slot / div
+    int64_t K, kp, rows;
+    int div, per_slice, ksplit, act;
+    const uint32_t* codes;
+    const uint16_t* scale;
+    const uint16_t* zero;
+    const float* w;             // first product: h = act(g) u w / s_out
+    const float* s_out;
+    int64_t s_out_stride;
+    uint32_t* hq;               // [slots]
+    int64_t hp;
+    float* p;                   // second product: [slices][slots][rows]
+};
+
+int moe_dot_tile(const ttq_moe_args* a);          // slots per tile; 0: not this path
+int64_t moe_dot_pad(int64_t K);
+int moe_dot_slices(int64_t n, int64_t E, int64_t I, int64_t M, int tile);
+hipError_t launch_moe_dot(const ttq_moe_args* a, const MoeLayout& L, char* ws, hipStream_t st);
 
 }  // namespace ttq

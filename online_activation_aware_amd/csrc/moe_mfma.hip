@@ -96,31 +96,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_moe_prep(MoePlan pl, MoePrep a
         use = use && e >= 0 && e < a.E;
     }
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (use) {
-        if constexpr (XF32) {
-            const f32x4 u = *(const f32x4*)((const float*)a.X + t * a.ldx + k0);
-            const f32x4 v = *(const f32x4*)((const float*)a.X + t * a.ldx + k0 + 4);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[j] = u[j];
-                x[4 + j] = v[j];
-            }
-        } else {
-            const u32x4 u = *(const u32x4*)((const uint16_t*)a.X + t * a.ldx + k0);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[2 * j] = bf16lo_to_f32(u[j]);
-                x[2 * j + 1] = bf16hi_to_f32(u[j]);
-            }
-        }
-        const float* s = a.s + e * a.s_stride + k0;
-        const f32x4 u = *(const f32x4*)s, v = *(const f32x4*)(s + 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[j] /= u[j];
-            x[4 + j] /= v[j];
-        }
-    }
+    if (use) moe_load_scaled<XF32>(x, a, t, e, k0);
     float sum = 0.f;
     if (in) sum = store_terms<NS>(x, a.xt + row * NS * a.kp + k0, a.kp);
     sum += __shfl_xor(sum, 1);
@@ -155,26 +131,6 @@ __device__ __forceinline__ void exchange_quarters(u32x4& w) {
 }
 
 __device__ __forceinline__ float half_of(uint32_t d, bool hi) { return f16_to_f32((uint16_t)(hi ? d >> 16 : d & 0xFFFFu)); }
-
-// NH fp16 values at byte offset `off` of a buffer as packed words; W2: in
-// two-byte loads (rows of the array that are aligned to nothing more).
-template <int NH, bool W2>
-__device__ __forceinline__ void load_steps(uint32_t (&d)[NH / 2], rsrc_t r, uint32_t off) {
-    if constexpr (W2) {
-#pragma unroll
-        for (int v = 0; v < NH / 2; ++v)
-            d[v] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(off + 4 * v), 0, 0) |
-                   ((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(off + 4 * v + 2), 0, 0) << 16);
-    } else if constexpr (NH == 8) {
-        const u32x4 a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
-#pragma unroll
-        for (int v = 0; v < 4; ++v) d[v] = a[v];
-    } else {
-        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
-        d[0] = a[0];
-        d[1] = a[1];
-    }
-}
 
 constexpr int kMmBlock = 4;                       // chunks whose codes a wave has in flight
 constexpr int kMmStepLds = 3 * 1024;              // a wave's steps (fp16) and step (zero + 16) (fp32) of a block
@@ -228,8 +184,8 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     };
     auto load_sz = [&](int i) __attribute__((always_inline)) {
         const uint32_t off = go + (uint32_t)(cb + i) * (NG * 2);
-        load_steps<NH, W2>(sw, rsc, off);
-        load_steps<NH, W2>(zw, rze, off);
+        moe_load_halves<NH, W2>(sw, rsc, off);
+        moe_load_halves<NH, W2>(zw, rze, off);
     };
     const int b0 = D * kx;
     if (b0 < cnt) {                               // uniform, as every condition on cnt below
@@ -441,8 +397,7 @@ int moe_slices(int64_t n, int64_t E, int64_t I, int64_t M) {
 
 template <int NS, bool GU>
 static hipError_t launch_mm(const MoeMm& p, int group, dim3 grid, int waves, hipStream_t st) {
-    // Steps of a block (four chunks) in one or two 16- or 8-byte loads where the rows of the array keep that alignment.
-    const bool w2 = p.K / group * 2 % (group == 128 ? 8 : 16) != 0;
+    const bool w2 = p.K / group % 2 != 0;         // rows of steps aligned to two bytes only
 #define TTQ_MM(G)                                                                                                     \
     return w2 ? launch_kernel(k_moe_mfma<G, NS, true, GU>, grid, dim3(waves * kWave), 0, st, nullptr, nullptr, p)     \
               : launch_kernel(k_moe_mfma<G, NS, false, GU>, grid, dim3(waves * kWave), 0, st, nullptr, nullptr, p)
@@ -460,10 +415,7 @@ static hipError_t launch_ns(const ttq_moe_args* a, const MoeLayout& L, char* ws,
     const int64_t n = a->T * a->topk, kp = moe_pad(a->K), ip = moe_pad(a->I);
     const int64_t nt = moe_tiles(n, a->E, kMmTile);
     MoePlan pl{a->ids, (int)n, (int)a->E, kMmTile, (int)nt, (int32_t*)(ws + L.order), (MoeTile*)(ws + L.tiles)};
-    MoePrep pr{};
-    pr.X = a->X; pr.ldx = a->ldx; pr.K = a->K; pr.kp = kp;
-    pr.s = a->gate_up.s; pr.s_stride = a->gate_up.s_stride;
-    pr.rows = pr.s_stride ? n : a->T; pr.ids = a->ids; pr.topk = (int)a->topk; pr.E = (int)a->E;
+    MoePrep pr = moe_prep_of(a, kp);
     pr.xt = (uint16_t*)(ws + L.xt); pr.xs = (float*)(ws + L.xs);
     const dim3 pg((unsigned)(1 + (pr.rows * (kp / 8) + kPlanThreads - 1) / kPlanThreads));
     if (hipError_t e = a->xt == TTQ_F32

@@ -7,7 +7,12 @@ for bf16 X (2^-16), three for fp32 X (2^-24), or fp32 values; codes, steps and
 zeros are exact.  Group sums are formed as step (sum (c + q) x - (c + z) sum x)
 with c at most 32, so a rounding is relative to step (q + z + 2 c) |x|; a sum
 of n terms in fp32 is off by at most n 2^-23 of the sum of the absolute terms
-(twice the textbook bound)."""
+(twice the textbook bound).  One or two tokens on 4-bit codes in groups of 32
+or more take x / s and h as integers of five (bf16 X) or six (fp32 X) base-16
+digits times a scale per 32 channels: the largest of them is 7 (16^5 - 1) / 15
+= 489335 or 7829367 scales, every one is off by half a scale at most, i.e. by
+the largest of its 32 over 978670 < 2^-19 or 15658734 < 2^-23, and by another
+2^-23 of it for the two roundings before (inverse scale, product)."""
 import numpy as np
 
 import oracle
@@ -68,21 +73,26 @@ def _gate(x, act):
     return 0.5 * x * (1 + np.tanh(np.sqrt(2 / np.pi) * (x + 0.044715 * x ** 3)))
 
 
-def _product(x, ex, num, s, bits, rel):
+def _product(x, ex, num, s, bits, rel, digits):
     """y = W (x / s) and a bound on |library - y| where x is off by ex."""
     q, d, z = num
     c = 2.0 ** bits
     w = (q - z) * d / s
     mag = d * (q + z + 2 * c) / s
     K = w.shape[1]
-    return x @ w.T, (np.abs(x) @ mag.T) * (rel + 2.0 ** -21 + K * U32) + ex @ np.abs(w).T
+    bound = (np.abs(x) @ mag.T) * (rel + 2.0 ** -21 + K * U32) + ex @ np.abs(w).T
+    if digits:
+        top = np.repeat((np.abs(x / s) + ex / s).reshape(len(x), K // 32, 32).max(2), 32, axis=1)
+        bound += (top @ np.abs(w * s).T) * ((2.0 ** -19 if rel == 2.0 ** -16 else 2.0 ** -23) + U32)
+    return x @ w.T, bound
 
 
-def moe(x, ids, wts, gu, s_in, dn, s_down, bits, act, split):
+def moe(x, ids, wts, gu, s_in, dn, s_down, bits, act, split, group):
     """gu, dn: (q, d, z) of [E][2 I][K] and [E][M][I]; s_*: [K] or [E][.].
-    split: the relative error of x / s and h inside the products.  Returns
-    (Y, bound)."""
+    split: the relative error of x / s and h inside the matrix cores' products.
+    Returns (Y, bound)."""
     T = x.shape[0]
+    digits = T <= 2 and bits == 4 and group >= 32
     E, rows2, _ = gu[0].shape
     I, M = rows2 // 2, dn[0].shape[1]
     y = np.zeros((T, M))
@@ -92,7 +102,7 @@ def moe(x, ids, wts, gu, s_in, dn, s_down, bits, act, split):
         t, j = np.nonzero(ids == e)
         if len(t) == 0:
             continue
-        g, bg = _product(x[t], np.zeros_like(x[t]), tuple(v[e] for v in gu), at(s_in, e), bits, split)
+        g, bg = _product(x[t], np.zeros_like(x[t]), tuple(v[e] for v in gu), at(s_in, e), bits, split, digits)
         a = _gate(g[:, :I], act)
         u, bu = g[:, I:], bg[:, I:]
         # |act'| <= 1.2; exp of an argument off by 2^-23 of it, and 8 more roundings
@@ -100,7 +110,7 @@ def moe(x, ids, wts, gu, s_in, dn, s_down, bits, act, split):
         wt = wts[t, j][:, None]
         h = a * u * wt
         bh = ((np.abs(a) + ba) * bu + ba * np.abs(u)) * np.abs(wt) + np.abs(h) * 8 * U32
-        o, bo = _product(h, bh, tuple(v[e] for v in dn), at(s_down, e), bits, split)
+        o, bo = _product(h, bh, tuple(v[e] for v in dn), at(s_down, e), bits, split, digits)
         np.add.at(y, t, o)
         np.add.at(by, t, bo + np.abs(o) * (ids.shape[1] * U32))
     return y, by

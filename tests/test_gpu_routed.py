@@ -84,15 +84,19 @@ def moe_inputs(seed, Tn, E, topk, K, I, M, bits, group, xt, per_in=False, per_do
     return out
 
 
-def moe_ref(d, bits, act, xt):
+def moe_ref(d, bits, act, xt, group):
     (gu, s_in), (dn, s_down) = d["gate_up_ref"], d["down_ref"]
     return ref.moe(d["x"], d["ids"], d["w"].astype(np.float64), gu, s_in, dn, s_down, bits, act,
-                   2.0 ** -16 if xt == "bf16" else 2.0 ** -23)
+                   2.0 ** -16 if xt == "bf16" else 2.0 ** -23, group)
 
 
 MOE = [  # T, E, topk, K, I, M, bits, group, xt, yt, act
     (1, 8, 2, 256, 384, 256, 4, 32, "bf16", "bf16", "silu"),
     (1, 1, 1, 32, 32, 1, 4, 32, "bf16", "f32", "silu"),
+    (1, 4, 3, 544, 1056, 65, 4, 32, "bf16", "f32", "gelu"),
+    (1, 6, 6, 1024, 512, 300, 4, 64, "f32", "f32", "silu"),
+    (2, 3, 4, 640, 384, 129, 4, 128, "bf16", "f32", "silu"),
+    (2, 40, 8, 2048, 64, 64, 4, 32, "f32", "bf16", "gelu"),
     (3, 4, 2, 96, 160, 33, 4, 32, "bf16", "f32", "gelu"),
     (7, 64, 6, 160, 96, 80, 4, 32, "bf16", "f32", "silu"),
     (16, 5, 3, 512, 640, 513, 4, 64, "bf16", "f32", "silu"),
@@ -117,7 +121,7 @@ def test_moe(T, case):
     say(f"moe {case}")
     d = moe_inputs(sum(case[:8]), Tn, E, topk, K, I, M, bits, group, xt, per_in=E % 2 == 0)
     y = T.ttq_moe(d["X"], i32_dev(d["ids"]), f32_dev(d["w"]), d["gate_up"], d["down"], bits, group, act=act, y_dtype=DT[yt])
-    r, b = moe_ref(d, bits, act, xt)
+    r, b = moe_ref(d, bits, act, xt, group)
     ref.check(num(y), r, b, yt == "bf16")
 
 
@@ -139,7 +143,7 @@ def test_moe_slots_without_an_expert_and_strides(T, bits, group, xt, Tn):
     big[:, 32:32 + K] = d["X"]
     Y = torch.full((Tn, M + 5), -77.0, device="cuda")
     T.ttq_moe(big[:, 32:32 + K], i32_dev(ids), f32_dev(w), d["gate_up"], d["down"], bits, group, Y=Y[:, 2:2 + M])
-    r, b = moe_ref(d, bits, "silu", xt)
+    r, b = moe_ref(d, bits, "silu", xt, group)
     y = num(Y)
     ref.check(y[:, 2:2 + M], r, b, False)
     assert np.all(y[Tn // 2, 2:2 + M] == 0)
@@ -163,12 +167,15 @@ def test_moe_rows_do_not_depend_on_the_batch(T, group):
     d = moe_inputs(9, Tn, E, topk, K, I, M, 4, group, "bf16")
     ids, w = i32_dev(d["ids"]), f32_dev(d["w"])
     call = lambda a, b: T.ttq_moe(d["X"][a:b], ids[a:b].contiguous(), w[a:b].contiguous(), d["gate_up"], d["down"], 4, group)  # noqa: E731
-    r, b = moe_ref(d, 4, "silu", "bf16")
+    r, b = moe_ref(d, 4, "silu", "bf16", group)
     whole = call(0, Tn)
     assert torch.equal(whole, call(0, Tn))
     ref.check(num(whole), r, b, False)
     for t in (0, 7, 23):
-        ref.check(num(call(t, t + 1)), r[t:t + 1], b[t:t + 1], False)
+        one = dict(d, x=d["x"][t:t + 1], ids=d["ids"][t:t + 1], w=d["w"][t:t + 1])
+        r1, b1 = moe_ref(one, 4, "silu", "bf16", group)
+        ref.check(num(call(t, t + 1)), r1, b1, False)
+        ref.check(num(call(t, t + 1)), num(whole)[t:t + 1], b1 + b[t:t + 1], False)
 
 
 # ------------------------------------------------------------------ adapters
@@ -346,7 +353,7 @@ def test_a_layer_of_routed_projections(T):
         c = host(q["codes"]).reshape(-1, cols * bits // 32)
         qn = oracle.unpack_codes(c, bits, cols).astype(np.float64).reshape(E, rows, cols)
         return (qn, *(np.repeat(host(q[k]).astype(np.float64), group, 2) for k in ("scale_f16", "zero_f16")))
-    r, b = ref.moe(num(y), host(e), num(w), numbers(gu, 2 * I, K), num(s), numbers(dn, K, I), num(s2), bits, "silu", 2.0 ** -16)
+    r, b = ref.moe(num(y), host(e), num(w), numbers(gu, 2 * I, K), num(s), numbers(dn, K, I), num(s2), bits, "silu", 2.0 ** -16, group)
     ref.check(num(out), r, b, False)
 
 
