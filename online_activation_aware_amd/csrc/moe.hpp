@@ -108,7 +108,7 @@ struct MoeMm {
     const uint16_t* xt;         // operand rows: slot / div
     const float* xs;
     int64_t K, kp, rows;
-    int div, per_slice, ksplit, act;
+    int div, per_slice, ksplit, act, xbytes;
     const uint32_t* codes;
     const uint16_t* scale;
     const uint16_t* zero;

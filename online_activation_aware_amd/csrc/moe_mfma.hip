@@ -36,9 +36,8 @@
 
 namespace ttq {
 
-constexpr int kMmMaxWaves = 8;
+constexpr int kMmMaxWaves = 16;
 constexpr int kMmRows = 32;                       // code rows per wave
-constexpr int kMmLds = 52 * 1024;                 // x~ and its sums: two workgroups of eight waves on a compute unit
 constexpr int kMmChunk = 128;
 
 int64_t moe_pad(int64_t K) { return (K + kMmChunk - 1) / kMmChunk * kMmChunk; }
@@ -135,6 +134,19 @@ __device__ __forceinline__ float half_of(uint32_t d, bool hi) { return f16_to_f3
 constexpr int kMmBlock = 4;                       // chunks whose codes a wave has in flight
 constexpr int kMmStepLds = 3 * 1024;              // a wave's steps (fp16) and step (zero + 16) (fp32) of a block
 
+// LDS of x~: per slot and chunk NS * 256 bytes of terms and 32 of sums, 32 to
+// keep the rows apart modulo the banks.  Where the whole slice does not fit,
+// half of it holds the chunks being multiplied and half the next ones (kMmMaxX
+// bytes, one workgroup of 16 waves on a compute unit); with kMmSmallX bytes
+// (two workgroups of eight), for tiles that are mostly expected to fit, all of
+// it holds the current ones.
+constexpr int mm_unit(int ns) { return ns * 256 + 32; }
+constexpr int kMmRowPad = 32;
+constexpr int kMmMaxX = 104 * 1024, kMmSmallX = 56 * 1024;
+static_assert(kMmMaxX / 2 >= kMmTile * (kMmBlock * mm_unit(3) + kMmRowPad), "a block of every slot's row fits in a half");
+static_assert(kMmSmallX >= kMmTile * (kMmBlock * mm_unit(3) + kMmRowPad), "or in all of the small one");
+static_assert(kMmMaxX + kMmMaxWaves * kMmStepLds <= 160 * 1024, "LDS of a compute unit");
+
 template <int GROUP, int NS, bool W2, bool GU>
 __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     constexpr int NG = kMmChunk / GROUP;          // groups per chunk
@@ -142,16 +154,16 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     constexpr int D = kMmBlock;
     constexpr int NB = NG * D;                    // groups per block: 16, 8 or 4
     constexpr int NH = NB > 8 ? 8 : NB;           // steps a lane loads
-    __shared__ __attribute__((aligned(16))) unsigned char smem[kMmLds];
-    __shared__ __attribute__((aligned(16))) unsigned char steps[kMmMaxWaves][kMmStepLds];
-    __shared__ int srow[kMmTile];
+    constexpr int kBlockLoads = 2 * D + 2 * (W2 ? NH : 1);
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const MoeTile tl = a.tiles[blockIdx.y];
     if (tl.count == 0) return;
-    const int tid = threadIdx.x, nth = blockDim.x;
+    const int tid = threadIdx.x;
     const int lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int nw = blockDim.x / kWave;
     const int nk = a.ksplit, kx = wave % nk;      // this wave's blocks: kx, kx + nk, ...
-    const int rw = wave / nk, nr = nth / kWave / nk;
+    const int rw = wave / nk, nr = nw / nk;
     const int r16 = lane & 15, q = lane >> 4;
     const int64_t K = a.K, R = GU ? 2 * a.rows : a.rows;
     const int64_t wpr = K / 8, gpr = K / GROUP;
@@ -174,69 +186,79 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     const int cb = (int)blockIdx.z * a.per_slice;
     const int cnt = min(nch, cb + a.per_slice) - cb;   // chunks of this slice
 
+    // x~ and its sums of kb chunks at a time.
+    constexpr int kUnit = mm_unit(NS);
+    const int rows = tl.count;
+    const int xrow = a.order[tl.first + min(lane & 15, rows - 1)] / a.div;   // operand row of slot lane % 16
+    int kb = (cnt + D - 1) & ~(D - 1), half = 0;
+    if (rows * (kb * kUnit + kMmRowPad) > a.xbytes) {
+        half = a.xbytes > kMmSmallX ? a.xbytes / 2 & ~15 : 0;
+        kb = ((half ? half : a.xbytes) / rows - kMmRowPad) / kUnit & ~(D - 1);
+    }
+    const int rowb = NS * kb * 256 + 16, srowb = kb * 32 + 16;
+    unsigned char* const xb = smem + nw * kMmStepLds;
+    // Straight from memory into LDS: a wave's instruction takes four chunks of
+    // one term of one row, or a row's sums.
+    auto stage = [&](int i0, unsigned char* to) __attribute__((always_inline)) {
+        const int per = NS * (kb / D) + 1;
+        for (int u = wave; u < rows * per; u += nw) {
+            const int r = u / per, w = u - r * per;
+            const int64_t xr = __builtin_amdgcn_readlane(xrow, r);
+            if (w == per - 1) {
+                const rsrc_t rs = make_rsrc(a.xs + xr * (a.kp / 16), a.kp / 4);
+                for (int h = 0; h * 32 < kb; ++h)
+                    if (lane < 2 * (kb - 32 * h))
+                        dma_to_lds<16>(rs, to + rows * rowb + r * srowb + h * 1024, lane * 16, (cb + i0 + 32 * h) * 32);
+            } else {
+                const int n = w / (kb / D), c4 = w - n * (kb / D);
+                const rsrc_t rx = make_rsrc(a.xt + xr * NS * a.kp, NS * a.kp * 2);
+                dma_to_lds<16>(rx, to + r * rowb + (n * kb + c4 * D) * 256, lane * 16,
+                               (int)(n * a.kp * 2) + (cb + i0 + c4 * D) * 256);
+            }
+        }
+    };
+    stage(0, xb);
+
+    // Codes, steps and zeros of a block; chunks past the slice are asked for
+    // behind the buffer (zeros, no traffic), so that a block is always
+    // kBlockLoads loads and the waits below can count them.
     u32x4 ring[D][2];
     uint32_t sw[NH / 2], zw[NH / 2];
     auto load = [&](int u, int i) __attribute__((always_inline)) {
+        const uint32_t at = i < cnt ? (uint32_t)(cb + i) * 64 : 0x80000000u;
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt)
-            ring[u][rt] = __builtin_bit_cast(
-                u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(co[rt] + (uint32_t)(cb + i) * 64), 0, 2));
+            ring[u][rt] =
+                __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(co[rt] + at), 0, 2));
     };
     auto load_sz = [&](int i) __attribute__((always_inline)) {
-        const uint32_t off = go + (uint32_t)(cb + i) * (NG * 2);
+        const uint32_t off = go + (i < cnt ? (uint32_t)(cb + i) * (NG * 2) : 0x80000000u);
         moe_load_halves<NH, W2>(sw, rsc, off);
         moe_load_halves<NH, W2>(zw, rze, off);
     };
-    const int b0 = D * kx;
-    if (b0 < cnt) {                               // uniform, as every condition on cnt below
-        load_sz(b0);
+    int b = D * kx;                               // first chunk of the block
+    __builtin_amdgcn_sched_barrier(0);
+    load_sz(b);
 #pragma unroll
-        for (int u = 0; u < D; ++u)
-            if (b0 + u < cnt) load(u, b0 + u);
-    }
+    for (int u = 0; u < D; ++u) load(u, b + u);
+    __builtin_amdgcn_sched_barrier(0);
 
-    // Operand rows of the tile's slots; x~ and its sums of kb chunks at a
-    // time in LDS, rows 16 bytes apart modulo the banks.
-    if (tid < kMmTile) srow[tid] = a.order[tl.first + min(tid, tl.count - 1)] / a.div;
-    const int rows = tl.count;
-    constexpr int kUnit = NS * 256 + 16;          // bytes of a chunk of a row: x~ and four sums
-    static_assert(kMmLds >= kMmTile * (D * kUnit + 32), "a block of every slot's row fits");
-    int kb = (kMmLds / rows - 32) / kUnit & ~(D - 1);   // 32: the row ends; at least one block
-    kb = min(kb, (cnt + D - 1) & ~(D - 1));
-    const int rowb = NS * kb * 256 + 16, srowb = kb * 4 + 4;       // bytes; floats
-    float* ssum = (float*)(smem + rows * rowb);
-    __syncthreads();
-    auto stage = [&](int i0) __attribute__((always_inline)) {
-        const int nc = min(kb, cnt - i0);
-        const int per = NS * nc * 16;             // 16-byte pieces a row
-        for (int p = tid; p < rows * per; p += nth) {
-            const int r = p / per, w = p - r * per;
-            const int n = w / (nc * 16), k = w - n * nc * 16;
-            const u32x4 v = *(const u32x4*)(a.xt + ((int64_t)srow[r] * NS + n) * a.kp + (int64_t)(cb + i0) * kMmChunk + k * 8);
-            *(u32x4*)(smem + r * rowb + n * kb * 256 + k * 16) = v;
-        }
-        for (int p = tid; p < rows * nc * 4; p += nth) {
-            const int r = p / (nc * 4), k = p - r * nc * 4;
-            const float* s = a.xs + (int64_t)srow[r] * (a.kp / 16) + (int64_t)(cb + i0) * 8 + 2 * k;
-            ssum[r * srowb + k] = s[0] + s[1];
-        }
-    };
     // Lanes past the tile's slots repeat its first one; their outputs are not
     // used.  In quarter q, MFMA j takes channels 32 j + 8 q ..+7 of the chunk
     // (the codes after the exchange of quarters), with one group per chunk
     // 32 q + 8 j ..+7 (no exchange needed).
     constexpr int kXq = GROUP < 128 ? 16 : 64, kXj = GROUP < 128 ? 64 : 16;
     const int rl = r16 < rows ? r16 : 0;
-    const unsigned char* xl = smem + rl * rowb + kXq * q;
-    const float* sl = ssum + rl * srowb + q;
-    unsigned char* const my = steps[wave];
+    const int xo = rl * rowb + kXq * q, so = rows * rowb + rl * srowb + 8 * q;
+    unsigned char* const my = smem + wave * kMmStepLds;
     uint16_t* const st_l = (uint16_t*)my;         // [32][NB]
     float* const nb_l = (float*)(my + 1024);      // [32][NB]
     const int gq = NG == 4 ? q : NG == 2 ? q >> 1 : 0;   // group of subgroup q within a chunk
 
     f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-    auto multiply = [&](int u, int i) __attribute__((always_inline)) {   // i: chunk within the stage
-        const float si = sl[4 * i];
+    auto multiply = [&](int u, int i, const unsigned char* x0) __attribute__((always_inline)) {   // i: chunk of the stage
+        const float* sp = (const float*)(x0 + so + 32 * i);
+        const float si = sp[0] + sp[1];
         f32x4 p[2];
         uint32_t st[2][(NG + 1) / 2];
         float nb[2];
@@ -253,14 +275,14 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            u32x4 b[2];
+            u32x4 bb[2];
 #pragma unroll
-            for (int rt = 0; rt < 2; ++rt) b[rt] = codes_plus16(ring[u][rt][j]);
+            for (int rt = 0; rt < 2; ++rt) bb[rt] = codes_plus16(ring[u][rt][j]);
 #pragma unroll
             for (int n = NS - 1; n >= 0; --n) {
-                const u32x4 x = *(const u32x4*)(xl + n * kb * 256 + i * 256 + kXj * j);
+                const u32x4 x = *(const u32x4*)(x0 + xo + n * kb * 256 + i * 256 + kXj * j);
 #pragma unroll
-                for (int rt = 0; rt < 2; ++rt) p[rt] = mfma_16x16x32(x, b[rt], p[rt]);
+                for (int rt = 0; rt < 2; ++rt) p[rt] = mfma_16x16x32(x, bb[rt], p[rt]);
             }
             if ((j + 1) % SPG == 0) {
                 const int g = j / SPG;
@@ -276,12 +298,19 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) acc[rt] = __builtin_amdgcn_mfma_f32_16x16x4f32(si, nb[rt], acc[rt], 0, 0, 0);
     };
-    int b = b0;                                   // first chunk of the block
+    // Everything but this block's loads has arrived: x~ has.
+    wait_vmcnt<kBlockLoads>();
+    unsigned char *x0 = xb, *x1 = xb + half;
     for (int i0 = 0; i0 < cnt; i0 += kb) {
-        if (i0 > 0) __syncthreads();              // the previous chunks have been read
-        stage(i0);
-        __syncthreads();
+        sync_lds();                               // every wave's part of x~; the half multiplied last is free
+        if (half == 0 && i0 > 0) {                // one buffer: refilled between two barriers
+            stage(i0, x0);
+            wait_vmcnt<0>();
+            sync_lds();
+        }
         const int e = min(cnt, i0 + kb);
+        if (half != 0 && e < cnt) stage(e, x1);
+        bool newer = false;                       // loads were issued after the stage's
         for (; b < e; b += D * nk) {
             // This block's steps into the wave's part of LDS (its reads of the
             // block before are done: LDS operations of a wave keep their order).
@@ -297,21 +326,29 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
             }
             __builtin_amdgcn_wave_barrier();
             const int bn = b + D * nk;
-            if (bn < cnt) load_sz(bn);
+            load_sz(bn);
 #pragma unroll
             for (int u = 0; u < D; ++u) {
-                if (b + u < e) multiply(u, b + u - i0);
-                if (bn + u < cnt) load(u, bn + u);
+                if (b + u < e) multiply(u, b + u - i0, x0);
+                load(u, bn + u);
                 __builtin_amdgcn_sched_barrier(0);
             }
+            newer = true;
         }
+        if (half != 0 && e < cnt) {               // uniform
+            if (newer) wait_vmcnt<kBlockLoads>();
+            else wait_vmcnt<0>();
+        }
+        unsigned char* t = x0;
+        x0 = x1;
+        x1 = t;
     }
     if (nk > 1) {                                 // uniform: the waves of a row group added in order
-        __syncthreads();                          // x~ has been read
-        f32x4* red = (f32x4*)smem;
+        sync_lds();                               // x~ has been read
+        f32x4* red = (f32x4*)xb;
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) red[(wave * 2 + rt) * kWave + lane] = acc[rt];
-        __syncthreads();
+        sync_lds();
         if (kx == 0)
             for (int w = 1; w < nk; ++w)
 #pragma unroll
@@ -369,18 +406,32 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
 
 // ------------------------------------------------------------------ host
 
-// Waves of a workgroup: row groups of 32 code rows (they share x~ in LDS), up
-// to eight; fewer where the chip would not get two workgroups per compute
-// unit.  Where there are fewer than 4096 waves (four per SIMD), the blocks of
-// a row group's channels go to up to four waves.
+// Waves of a workgroup: row groups of 32 code rows (they share x~ in LDS).
+// Eight, two workgroups on a compute unit, where the operands fit or the
+// experts have at most four slots on average (their tiles mostly fit); else
+// 16 with two buffers (measured, 128 tokens over 8 experts, 32 slots each: 633
+// us against 661 with eight waves and one buffer; 16 tokens over 64 experts,
+// 1.5 slots each: 97 us against 87).  Where there are fewer than 3072 waves,
+// the blocks of a row group's channels go to up to four waves, and where the
+// chip would not get its workgroups, they are smaller.
 struct MmShape {
-    int nr, nk;
+    int nr, nk, xbytes;
+    size_t lds() const { return (size_t)nr * nk * kMmStepLds + xbytes; }
 };
-static MmShape mm_shape(int64_t waves, int64_t tiles, int64_t chunks) {
-    MmShape s{kMmMaxWaves, 1};
+static MmShape mm_shape(int64_t waves, int64_t tiles, int64_t chunks, int64_t n, int64_t E, int ns) {
+    MmShape s{0, 1, 0};
+    const int64_t rows = n < kMmTile ? n : kMmTile, c4 = (chunks + kMmBlock - 1) / kMmBlock * kMmBlock;
+    const int64_t need = rows * (c4 * mm_unit(ns) + kMmRowPad);
+    const bool wide = need > kMmSmallX && n > 4 * E;
+    const int64_t most_x = wide ? kMmMaxX : kMmSmallX;
+    s.xbytes = (int)(need < most_x ? (need + 15) / 16 * 16 : most_x);
+    const int most = wide ? 16 : 8;
+    const int64_t wgs = wide ? 256 : 512;
     while (s.nk < 4 && waves * tiles * s.nk < 3072 && chunks >= 2 * kMmBlock * s.nk) s.nk *= 2;
-    s.nr = kMmMaxWaves / s.nk;
-    while (s.nr > 1 && s.nr * s.nk > 2 && (waves + s.nr - 1) / s.nr * tiles < 512) s.nr /= 2;
+    s.nr = most / s.nk;
+    while (s.nr > 1 && s.nr * s.nk > 2 && (waves + s.nr - 1) / s.nr * tiles < wgs) s.nr /= 2;
+    const int red = s.nr * s.nk * 2 * kWave * 16;   // the waves' tiles, where they are added
+    if (s.nk > 1 && s.xbytes < red) s.xbytes = red;
     return s;
 }
 
@@ -396,11 +447,11 @@ int moe_slices(int64_t n, int64_t E, int64_t I, int64_t M) {
 }
 
 template <int NS, bool GU>
-static hipError_t launch_mm(const MoeMm& p, int group, dim3 grid, int waves, hipStream_t st) {
+static hipError_t launch_mm(const MoeMm& p, int group, dim3 grid, int waves, size_t lds, hipStream_t st) {
     const bool w2 = p.K / group % 2 != 0;         // rows of steps aligned to two bytes only
 #define TTQ_MM(G)                                                                                                     \
-    return w2 ? launch_kernel(k_moe_mfma<G, NS, true, GU>, grid, dim3(waves * kWave), 0, st, nullptr, nullptr, p)     \
-              : launch_kernel(k_moe_mfma<G, NS, false, GU>, grid, dim3(waves * kWave), 0, st, nullptr, nullptr, p)
+    return w2 ? launch_kernel(k_moe_mfma<G, NS, true, GU>, grid, dim3(waves * kWave), lds, st, nullptr, nullptr, p)   \
+              : launch_kernel(k_moe_mfma<G, NS, false, GU>, grid, dim3(waves * kWave), lds, st, nullptr, nullptr, p)
     switch (group) {
         case 32: TTQ_MM(32);
         case 64: TTQ_MM(64);
@@ -430,10 +481,10 @@ static hipError_t launch_ns(const ttq_moe_args* a, const MoeLayout& L, char* ws,
     p.w = a->w; p.s_out = a->down.s; p.s_out_stride = a->down.s_stride; p.act = a->act;
     p.ht = (uint16_t*)(ws + L.h); p.hs = (float*)(ws + L.hs); p.hp = ip;
     const int64_t gw = ip / 16;
-    const MmShape g = mm_shape(gw, nt, p.per_slice);
-    p.ksplit = g.nk;
+    const MmShape g = mm_shape(gw, nt, p.per_slice, n, a->E, NS);
+    p.ksplit = g.nk; p.xbytes = g.xbytes;
     if (hipError_t e = launch_mm<NS, true>(p, a->group, dim3((unsigned)((gw + g.nr - 1) / g.nr), (unsigned)nt),
-                                           g.nr * g.nk, st))
+                                           g.nr * g.nk, g.lds(), st))
         return e;
     MoeMm d{};
     d.tiles = pl.tiles; d.order = pl.order; d.slots = n;
@@ -444,11 +495,11 @@ static hipError_t launch_ns(const ttq_moe_args* a, const MoeLayout& L, char* ws,
     d.per_slice = (chunks + sl - 1) / sl;
     const int nsl = (chunks + d.per_slice - 1) / d.per_slice;
     const int64_t dw = (a->M + kMmRows - 1) / kMmRows;
-    const MmShape v = mm_shape(dw, nt * nsl, d.per_slice);
-    d.ksplit = v.nk;
+    const MmShape v = mm_shape(dw, nt * nsl, d.per_slice, n, a->E, NS);
+    d.ksplit = v.nk; d.xbytes = v.xbytes;
     if (hipError_t e = launch_mm<NS, false>(d, a->group,
                                             dim3((unsigned)((dw + v.nr - 1) / v.nr), (unsigned)nt, (unsigned)nsl),
-                                            v.nr * v.nk, st))
+                                            v.nr * v.nk, v.lds(), st))
         return e;
     return launch_moe_sum(a, d.p, nsl, st);
 }
