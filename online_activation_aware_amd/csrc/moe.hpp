@@ -149,28 +149,39 @@ __device__ __forceinline__ void moe_load_scaled(float (&x)[8], const MoePrep& a,
     }
 }
 
-// NH fp16 values (4, 8 or 16) at byte offset `off` of a buffer as packed
-// words, in loads of up to 16 bytes; W2: of two bytes (rows of the array that
-// are aligned to nothing more).
+// Descriptor of `bytes` bytes of fp16 values from p, its base aligned down to
+// a word; `adj` (0 or 2) goes onto the offsets.
+__device__ __forceinline__ rsrc_t moe_half_rsrc(const uint16_t* p, int64_t bytes, uint32_t& adj) {
+    adj = (uint32_t)((uintptr_t)p & 2);
+    return make_rsrc((const char*)p - adj, (bytes + adj + 3) & ~(int64_t)3);
+}
+// NH fp16 values (4, 8 or 16) at byte offset `off` as packed words, in loads
+// of up to 16 bytes; W2: the offset may lie within a word (rows of an odd
+// number of groups), one word more is loaded and all are shifted.
 template <int NH, bool W2>
 __device__ __forceinline__ void moe_load_halves(uint32_t (&d)[NH / 2], rsrc_t r, uint32_t off) {
-    if constexpr (W2) {
-#pragma unroll
-        for (int v = 0; v < NH / 2; ++v)
-            d[v] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(off + 4 * v), 0, 0) |
-                   ((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)(off + 4 * v + 2), 0, 0) << 16);
-    } else if constexpr (NH >= 8) {
+    const uint32_t at = W2 ? off & ~2u : off;
+    uint32_t w[NH / 2 + 1];
+    w[NH / 2] = 0;
+    if constexpr (NH >= 8) {
 #pragma unroll
         for (int h = 0; h < NH / 8; ++h) {
-            const u32x4 a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(off + 16 * h), 0, 0));
+            const u32x4 a = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)(at + 16 * h), 0, 0));
 #pragma unroll
-            for (int v = 0; v < 4; ++v) d[4 * h + v] = a[v];
+            for (int v = 0; v < 4; ++v) w[4 * h + v] = a[v];
         }
     } else {
-        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
-        d[0] = a[0];
-        d[1] = a[1];
+        const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)at, 0, 0));
+        w[0] = a[0];
+        w[1] = a[1];
     }
+    if constexpr (W2) w[NH / 2] = __builtin_amdgcn_raw_buffer_load_b32(r, (int)(at + 2 * NH), 0, 0);
+#pragma unroll
+    for (int v = 0; v < NH / 2; ++v) d[v] = W2 ? __builtin_amdgcn_alignbit(w[v + 1], w[v], (off & 2) * 8) : w[v];
+}
+// Whether the rows of steps and zeros need W2.
+inline bool moe_w2(const uint16_t* scale, const uint16_t* zero, int64_t groups) {
+    return groups % 2 != 0 || (uintptr_t)scale % 4 != 0 || (uintptr_t)zero % 4 != 0;
 }
 
 // The rows of X as the first product's operand, kp padded channels.

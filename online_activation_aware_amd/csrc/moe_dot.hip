@@ -125,8 +125,9 @@ __global__ __launch_bounds__(kMdMaxWaves * kWave, TT == 1 ? 3 : 2) void k_moe_do
     const int64_t base = min(o0, a.rows - 1);
     const int64_t left = R - base;
     const rsrc_t rc = make_rsrc(a.codes + ((int64_t)tl.expert * R + base) * wpr, left * wpr * 4);
-    const rsrc_t rsc = make_rsrc(a.scale + ((int64_t)tl.expert * R + base) * gpr, left * gpr * 2);
-    const rsrc_t rze = make_rsrc(a.zero + ((int64_t)tl.expert * R + base) * gpr, left * gpr * 2);
+    uint32_t sa, za;
+    const rsrc_t rsc = moe_half_rsrc(a.scale + ((int64_t)tl.expert * R + base) * gpr, left * gpr * 2, sa);
+    const rsrc_t rze = moe_half_rsrc(a.zero + ((int64_t)tl.expert * R + base) * gpr, left * gpr * 2, za);
     const int np = (int)(a.kp / kMdPiece);
     const int pb = (int)blockIdx.z * a.per_slice, pe = min(np, pb + a.per_slice);
     // Byte offsets: code row 4 r + g, field f; steps of row `lane`.
@@ -151,8 +152,8 @@ __global__ __launch_bounds__(kMdMaxWaves * kWave, TT == 1 ? 3 : 2) void k_moe_do
     };
     auto load_steps = [&](int p) __attribute__((always_inline)) {
         const uint32_t off = so + (uint32_t)p * (NG * 2);
-        moe_load_halves<NG, W2>(sw, rsc, off);
-        moe_load_halves<NG, W2>(zw, rze, off);
+        moe_load_halves<NG, W2>(sw, rsc, off + sa);
+        moe_load_halves<NG, W2>(zw, rze, off + za);
     };
     auto load_x = [&](int p) __attribute__((always_inline)) {
         const int64_t per = a.kp / 8;
@@ -328,7 +329,7 @@ int moe_dot_slices(int64_t n, int64_t E, int64_t I, int64_t M, int tile) {
 
 template <int ND, int TT, bool GU>
 static hipError_t launch_dot(const MoeDot& p, int group, dim3 grid, int waves, hipStream_t st) {
-    const bool w2 = p.K / group % 2 != 0;         // rows of steps aligned to two bytes only
+    const bool w2 = moe_w2(p.scale, p.zero, p.K / group);
 #define TTQ_MD(G)                                                                                                   \
     return w2 ? launch_kernel(k_moe_dot<G, ND, TT, true, GU>, grid, dim3(waves * kWave), 0, st, nullptr, nullptr, p) \
               : launch_kernel(k_moe_dot<G, ND, TT, false, GU>, grid, dim3(waves * kWave), 0, st, nullptr, nullptr, p)

@@ -154,7 +154,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     constexpr int D = kMmBlock;
     constexpr int NB = NG * D;                    // groups per block: 16, 8 or 4
     constexpr int NH = NB > 8 ? 8 : NB;           // steps a lane loads
-    constexpr int kBlockLoads = 2 * D + 2 * (W2 ? NH : 1);
+    constexpr int kBlockLoads = 2 * D + 2 * (W2 ? 2 : 1);
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const MoeTile tl = a.tiles[blockIdx.y];
     if (tl.count == 0) return;
@@ -169,8 +169,9 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     const int64_t wpr = K / 8, gpr = K / GROUP;
     const int64_t o0 = ((int64_t)blockIdx.x * nr + rw) * (GU ? kMmRows / 2 : kMmRows);
     const rsrc_t rc = make_rsrc(a.codes + (int64_t)tl.expert * R * wpr, R * wpr * 4);
-    const rsrc_t rsc = make_rsrc(a.scale + (int64_t)tl.expert * R * gpr, R * gpr * 2);
-    const rsrc_t rze = make_rsrc(a.zero + (int64_t)tl.expert * R * gpr, R * gpr * 2);
+    uint32_t sa, za;
+    const rsrc_t rsc = moe_half_rsrc(a.scale + (int64_t)tl.expert * R * gpr, R * gpr * 2, sa);
+    const rsrc_t rze = moe_half_rsrc(a.zero + (int64_t)tl.expert * R * gpr, R * gpr * 2, za);
     // Code row of column r of column tile rt; rows past the end are clamped
     // and their outputs not used.
     auto row_of = [&](int rt, int r) -> int64_t {
@@ -233,8 +234,8 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     };
     auto load_sz = [&](int i) __attribute__((always_inline)) {
         const uint32_t off = go + (i < cnt ? (uint32_t)(cb + i) * (NG * 2) : 0x80000000u);
-        moe_load_halves<NH, W2>(sw, rsc, off);
-        moe_load_halves<NH, W2>(zw, rze, off);
+        moe_load_halves<NH, W2>(sw, rsc, off + sa);
+        moe_load_halves<NH, W2>(zw, rze, off + za);
     };
     int b = D * kx;                               // first chunk of the block
     __builtin_amdgcn_sched_barrier(0);
@@ -448,7 +449,7 @@ int moe_slices(int64_t n, int64_t E, int64_t I, int64_t M) {
 
 template <int NS, bool GU>
 static hipError_t launch_mm(const MoeMm& p, int group, dim3 grid, int waves, size_t lds, hipStream_t st) {
-    const bool w2 = p.K / group % 2 != 0;         // rows of steps aligned to two bytes only
+    const bool w2 = moe_w2(p.scale, p.zero, p.K / group);
 #define TTQ_MM(G)                                                                                                     \
     return w2 ? launch_kernel(k_moe_mfma<G, NS, true, GU>, grid, dim3(waves * kWave), lds, st, nullptr, nullptr, p)   \
               : launch_kernel(k_moe_mfma<G, NS, false, GU>, grid, dim3(waves * kWave), lds, st, nullptr, nullptr, p)
