@@ -87,7 +87,7 @@ struct MoeLayout {
 // partial results of each, p [slices][T topk][M], in that order.
 hipError_t launch_moe_sum(const ttq_moe_args* a, const float* p, int slices, hipStream_t st);
 
-// ---- on the matrix cores (moe_mfma.hip): 4-bit codes, groups of 32 or more
+// ---- on the matrix cores (moe_mfma.hip)
 
 constexpr int kMmTile = 16;                       // slots per tile
 
@@ -108,7 +108,7 @@ struct MoeMm {
     const uint16_t* xt;         // operand rows: slot / div
     const float* xs;
     int64_t K, kp, rows;
-    int div, per_slice, ksplit, act, xbytes;
+    int div, group, per_slice, ksplit, act, xbytes;
     const uint32_t* codes;
     const uint16_t* scale;
     const uint16_t* zero;
@@ -193,12 +193,12 @@ inline MoePrep moe_prep_of(const ttq_moe_args* a, int64_t kp) {
     return pr;
 }
 
-bool moe_mfma_ok(const ttq_moe_args* a);
 int64_t moe_pad(int64_t K);
 int moe_slices(int64_t n, int64_t E, int64_t I, int64_t M);
 hipError_t launch_moe_mfma(const ttq_moe_args* a, const MoeLayout& L, char* ws, hipStream_t st);
 
-// ---- integer dot products (moe_dot.hip): the same codes, one or two slots a tile
+// ---- integer dot products (moe_dot.hip): 4-bit codes, groups of 32 or more,
+// one or two tokens
 
 struct MoeDot {
     const MoeTile* tiles;

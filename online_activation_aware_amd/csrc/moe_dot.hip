@@ -302,7 +302,7 @@ __global__ __launch_bounds__(kMdMaxWaves * kWave, TT == 1 ? 3 : 2) void k_moe_do
 // One slot a tile for one token, two for two; more tokens take the matrix
 // cores.
 int moe_dot_tile(const ttq_moe_args* a) {
-    return moe_mfma_ok(a) && a->T <= 2 ? (int)a->T : 0;
+    return a->bits == 4 && a->group >= 32 && a->T <= 2 ? (int)a->T : 0;
 }
 
 // Row groups and waves on each one's pieces, up to eight waves a workgroup:

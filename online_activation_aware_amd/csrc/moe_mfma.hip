@@ -1,7 +1,6 @@
-// The mixture-of-experts layer on the matrix cores: 4-bit codes in groups of
-// 32, 64 or 128.
+// The mixture-of-experts layer on the matrix cores.
 //
-// As in the few-token projection (qgemv_gs.hip) codes are never expanded to
+// 4-bit codes in groups of 32, 64 or 128 (the sums form): as in the few-token projection (qgemv_gs.hip) codes are never expanded to
 // weights: per 32-channel subgroup the matrix cores form
 //   P[t][o] = sum_j (16 + q_oj) x~_tj,
 // slots as the 16 rows and code rows as the 16 columns of a 16x16x32 MFMA,
@@ -11,6 +10,10 @@
 // operations and a byte permute per pair of codes; with 16 instead of 128 as
 // the offset, the difference of the two terms loses three bits fewer.
 // step (zero + 16) is exact in fp32 (11 by 5 bits).
+//
+// Other bit widths, and groups of 16 (the weights form): a lane expands the 32
+// channels it loads to (code - zero) step, exact in 16 bits and so as two bf16
+// terms; about six instructions a code where the sums form takes two.
 //
 // x~ = x / s (and h for the second product) enters as a sum of NS bf16 terms,
 // hi = bf16(x~), then bf16 of what is left: 16 bits for two terms (bf16 X,
@@ -29,6 +32,7 @@
 // multiplied, and their tiles are added in wave order through LDS.  The
 // second product's channels can be split further over workgroups (slices);
 // the sum over a token's slots adds the slices, too.
+#include "codes.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 #include "lds_dma.hpp"
@@ -41,11 +45,6 @@ constexpr int kMmRows = 32;                       // code rows per wave
 constexpr int kMmChunk = 128;
 
 int64_t moe_pad(int64_t K) { return (K + kMmChunk - 1) / kMmChunk * kMmChunk; }
-
-bool moe_mfma_ok(const ttq_moe_args* a) {
-    const int64_t lim = (int64_t)1 << 31;
-    return a->bits == 4 && a->group >= 32 && 2 * a->I * a->K / 2 < lim && a->M * a->I / 2 < lim;
-}
 
 // ------------------------------------------------------------------ operand layout
 
@@ -147,14 +146,19 @@ static_assert(kMmMaxX / 2 >= kMmTile * (kMmBlock * mm_unit(3) + kMmRowPad), "a b
 static_assert(kMmSmallX >= kMmTile * (kMmBlock * mm_unit(3) + kMmRowPad), "or in all of the small one");
 static_assert(kMmMaxX + kMmMaxWaves * kMmStepLds <= 160 * 1024, "LDS of a compute unit");
 
-template <int GROUP, int NS, bool W2, bool GU>
+// GROUP 16, or other codes than 4-bit ones (GROUP then is 16, or 32 for any
+// larger one): the weights form (see the head of the file); W2 then is false.
+template <int BITS, int GROUP, int NS, bool W2, bool GU>
 __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
+    constexpr bool kSums = BITS == 4 && GROUP >= 32;
     constexpr int NG = kMmChunk / GROUP;          // groups per chunk
-    constexpr int SPG = GROUP / 32;               // subgroups per group
-    constexpr int D = kMmBlock;
+    constexpr int SPG = kSums ? GROUP / 32 : 1;   // subgroups per group
+    constexpr int SG = GROUP < 32 ? 2 : 1;        // groups of a lane's 32 channels
+    constexpr int D = kSums ? kMmBlock : 2;       // chunks of a block
     constexpr int NB = NG * D;                    // groups per block: 16, 8 or 4
-    constexpr int NH = NB > 8 ? 8 : NB;           // steps a lane loads
-    constexpr int kBlockLoads = 2 * D + 2 * (W2 ? 2 : 1);
+    constexpr int NH = kSums ? (NB > 8 ? 8 : NB) : 4;   // steps a lane loads
+    // Loads of a block at least (the compiler may join narrow ones).
+    constexpr int kBlockLoads = kSums ? 2 * D + 2 : 2 * D;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const MoeTile tl = a.tiles[blockIdx.y];
     if (tl.count == 0) return;
@@ -166,7 +170,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     const int rw = wave / nk, nr = nw / nk;
     const int r16 = lane & 15, q = lane >> 4;
     const int64_t K = a.K, R = GU ? 2 * a.rows : a.rows;
-    const int64_t wpr = K / 8, gpr = K / GROUP;
+    const int64_t wpr = K * BITS / 32, gpr = K / (kSums ? GROUP : a.group);
     const int64_t o0 = ((int64_t)blockIdx.x * nr + rw) * (GU ? kMmRows / 2 : kMmRows);
     const rsrc_t rc = make_rsrc(a.codes + (int64_t)tl.expert * R * wpr, R * wpr * 4);
     uint32_t sa, za;
@@ -178,9 +182,11 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
         if constexpr (GU) return min(o0 + r, a.rows - 1) + (rt ? a.rows : 0);
         else return min(o0 + 16 * rt + r, a.rows - 1);
     };
-    const uint32_t co[2] = {(uint32_t)(row_of(0, r16) * wpr * 4 + 16 * q), (uint32_t)(row_of(1, r16) * wpr * 4 + 16 * q)};
+    const uint32_t co[2] = {(uint32_t)(row_of(0, r16) * wpr * 4 + 4 * BITS * q),
+                            (uint32_t)(row_of(1, r16) * wpr * 4 + 4 * BITS * q)};
+    const uint32_t wo[2] = {(uint32_t)(row_of(0, r16) * gpr * 2), (uint32_t)(row_of(1, r16) * gpr * 2)};   // weights form
     // Steps and zeros of a block: lane (row, part) of the 32 rows.
-    constexpr int kParts = NB / NH;
+    constexpr int kParts = kSums ? NB / NH : 1;
     const int grow = lane / kParts & 31, gpart = lane % kParts;
     const uint32_t go = (uint32_t)((row_of(grow >> 4, grow & 15) * gpr + gpart * NH) * 2);
     const int nch = (int)(a.kp / kMmChunk);
@@ -198,7 +204,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     }
     const int rowb = NS * kb * 256 + 16, srowb = kb * 32 + 16;
     unsigned char* const xb = smem + nw * kMmStepLds;
-    // Straight from memory into LDS: a wave's instruction takes four chunks of
+    // Straight from memory into LDS: a wave's instruction takes a block of
     // one term of one row, or a row's sums.
     auto stage = [&](int i0, unsigned char* to) __attribute__((always_inline)) {
         const int per = NS * (kb / D) + 1;
@@ -213,29 +219,60 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
             } else {
                 const int n = w / (kb / D), c4 = w - n * (kb / D);
                 const rsrc_t rx = make_rsrc(a.xt + xr * NS * a.kp, NS * a.kp * 2);
-                dma_to_lds<16>(rx, to + r * rowb + (n * kb + c4 * D) * 256, lane * 16,
-                               (int)(n * a.kp * 2) + (cb + i0 + c4 * D) * 256);
+                if (lane < 16 * D)
+                    dma_to_lds<16>(rx, to + r * rowb + (n * kb + c4 * D) * 256, lane * 16,
+                                   (int)(n * a.kp * 2) + (cb + i0 + c4 * D) * 256);
             }
         }
     };
     stage(0, xb);
 
     // Codes, steps and zeros of a block; chunks past the slice are asked for
-    // behind the buffer (zeros, no traffic), so that a block is always
-    // kBlockLoads loads and the waits below can count them.
-    u32x4 ring[D][2];
+    // behind the buffer (zeros, no traffic), so that a block always has its
+    // loads and the waits below can count them.
+    struct Code {
+        CodeWords<BITS> c;
+        uint16_t st[kSums ? 1 : SG], ze[kSums ? 1 : SG];   // weights form: of the lane's 32 channels
+    };
+    Code ring[D][2];
     uint32_t sw[NH / 2], zw[NH / 2];
     auto load = [&](int u, int i) __attribute__((always_inline)) {
-        const uint32_t at = i < cnt ? (uint32_t)(cb + i) * 64 : 0x80000000u;
+        const uint32_t at = i < cnt ? (uint32_t)(cb + i) * (16 * BITS) : 0x80000000u;
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt)
-            ring[u][rt] =
-                __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, (int)(co[rt] + at), 0, 2));
+        for (int rt = 0; rt < 2; ++rt) {
+            Code& c = ring[u][rt];
+            const int off = (int)(co[rt] + at);
+            if constexpr (BITS >= 4) {
+                const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rc, off, 0, 2));
+#pragma unroll
+                for (int w = 0; w < 4; ++w) c.c.w[w] = v[w];
+                if constexpr (BITS == 5) c.c.w[4] = __builtin_amdgcn_raw_buffer_load_b32(rc, off + 16, 0, 2);
+            } else if constexpr (BITS == 3) {
+                const auto v = __builtin_amdgcn_raw_buffer_load_b96(rc, off, 0, 2);
+#pragma unroll
+                for (int w = 0; w < 3; ++w) c.c.w[w] = v[w];
+            } else {
+                const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rc, off, 0, 2));
+                c.c.w[0] = v[0];
+                c.c.w[1] = v[1];
+            }
+            if constexpr (!kSums) {
+                const int ch = (cb + i) * kMmChunk + 32 * q;   // first channel of this lane
+                const uint32_t g = i < cnt ? wo[rt] + (uint32_t)(SG == 2 ? ch / 16 : ch / a.group) * 2 : 0x80000000u;
+#pragma unroll
+                for (int h = 0; h < SG; ++h) {
+                    c.st[h] = __builtin_amdgcn_raw_buffer_load_b16(rsc, (int)(g + sa + 2 * h), 0, 0);
+                    c.ze[h] = __builtin_amdgcn_raw_buffer_load_b16(rze, (int)(g + za + 2 * h), 0, 0);
+                }
+            }
+        }
     };
     auto load_sz = [&](int i) __attribute__((always_inline)) {
-        const uint32_t off = go + (i < cnt ? (uint32_t)(cb + i) * (NG * 2) : 0x80000000u);
-        moe_load_halves<NH, W2>(sw, rsc, off + sa);
-        moe_load_halves<NH, W2>(zw, rze, off + za);
+        if constexpr (kSums) {
+            const uint32_t off = go + (i < cnt ? (uint32_t)(cb + i) * (NG * 2) : 0x80000000u);
+            moe_load_halves<NH, W2>(sw, rsc, off + sa);
+            moe_load_halves<NH, W2>(zw, rze, off + za);
+        }
     };
     int b = D * kx;                               // first chunk of the block
     __builtin_amdgcn_sched_barrier(0);
@@ -246,9 +283,10 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
 
     // Lanes past the tile's slots repeat its first one; their outputs are not
     // used.  In quarter q, MFMA j takes channels 32 j + 8 q ..+7 of the chunk
-    // (the codes after the exchange of quarters), with one group per chunk
-    // 32 q + 8 j ..+7 (no exchange needed).
-    constexpr int kXq = GROUP < 128 ? 16 : 64, kXj = GROUP < 128 ? 64 : 16;
+    // (the codes after the exchange of quarters), with one group per chunk or
+    // weights 32 q + 8 j ..+7 (no exchange needed).
+    constexpr bool kExchange = kSums && GROUP < 128;
+    constexpr int kXq = kExchange ? 16 : 64, kXj = kExchange ? 64 : 16;
     const int rl = r16 < rows ? r16 : 0;
     const int xo = rl * rowb + kXq * q, so = rows * rowb + rl * srowb + 8 * q;
     unsigned char* const my = smem + wave * kMmStepLds;
@@ -257,15 +295,51 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     const int gq = NG == 4 ? q : NG == 2 ? q >> 1 : 0;   // group of subgroup q within a chunk
 
     f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+    auto multiply_weights = [&](int u, int i, const unsigned char* x0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            u32x4 wt[2][2];                       // the weights' terms, slot order 0 2 4 6 1 3 5 7
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt) {
+                const Code& c = ring[u][rt];
+                const float st = f16_to_f32(c.st[8 * j / 16 % SG]), nz = -f16_to_f32(c.ze[8 * j / 16 % SG]) * st;
+                float w[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = __builtin_fmaf((float)code_at<BITS>(c.c, 8 * j + e), st, nz);
+                wt[rt][0] = pack_terms(w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {     // element e: channels kLo[e] and kLo[e] + 2
+                    constexpr int kLo[4] = {0, 4, 1, 5};
+                    w[kLo[e]] -= bf16lo_to_f32(wt[rt][0][e]);
+                    w[kLo[e] + 2] -= bf16hi_to_f32(wt[rt][0][e]);
+                }
+                wt[rt][1] = pack_terms(w);
+            }
+#pragma unroll
+            for (int n = NS - 1; n >= 0; --n) {
+                const u32x4 x = *(const u32x4*)(x0 + xo + n * kb * 256 + i * 256 + kXj * j);
+#pragma unroll
+                for (int h = 1; h >= 0; --h)
+#pragma unroll
+                    for (int rt = 0; rt < 2; ++rt) acc[rt] = mfma_16x16x32(x, wt[rt][h], acc[rt]);
+            }
+        }
+    };
     auto multiply = [&](int u, int i, const unsigned char* x0) __attribute__((always_inline)) {   // i: chunk of the stage
+        if constexpr (!kSums) {
+            multiply_weights(u, i, x0);
+            return;
+        }
         const float* sp = (const float*)(x0 + so + 32 * i);
         const float si = sp[0] + sp[1];
         f32x4 p[2];
+        u32x4 w4[2];
         uint32_t st[2][(NG + 1) / 2];
         float nb[2];
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) {
-            if constexpr (GROUP < 128) exchange_quarters(ring[u][rt]);
+            w4[rt] = u32x4{ring[u][rt].c.w[0], ring[u][rt].c.w[1], ring[u][rt].c.w[2], ring[u][rt].c.w[BITS > 3 ? 3 : 0]};
+            if constexpr (kExchange) exchange_quarters(w4[rt]);
             p[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
             const int g = (16 * rt + r16) * NB + u * NG;
             if constexpr (NG == 1) st[rt][0] = st_l[g];
@@ -278,7 +352,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
         for (int j = 0; j < 4; ++j) {
             u32x4 bb[2];
 #pragma unroll
-            for (int rt = 0; rt < 2; ++rt) bb[rt] = codes_plus16(ring[u][rt][j]);
+            for (int rt = 0; rt < 2; ++rt) bb[rt] = codes_plus16(w4[rt][j]);
 #pragma unroll
             for (int n = NS - 1; n >= 0; --n) {
                 const u32x4 x = *(const u32x4*)(x0 + xo + n * kb * 256 + i * 256 + kXj * j);
@@ -315,7 +389,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
         for (; b < e; b += D * nk) {
             // This block's steps into the wave's part of LDS (its reads of the
             // block before are done: LDS operations of a wave keep their order).
-            if (lane < 32 * kParts) {
+            if (kSums && lane < 32 * kParts) {
                 float nb[NH];
 #pragma unroll
                 for (int v = 0; v < NH; ++v)
@@ -448,11 +522,25 @@ int moe_slices(int64_t n, int64_t E, int64_t I, int64_t M) {
 }
 
 template <int NS, bool GU>
-static hipError_t launch_mm(const MoeMm& p, int group, dim3 grid, int waves, size_t lds, hipStream_t st) {
+static hipError_t launch_mm(const MoeMm& p, int bits, int group, dim3 grid, int waves, size_t lds, hipStream_t st) {
     const bool w2 = moe_w2(p.scale, p.zero, p.K / group);
+#define TTQ_MW(B, G) \
+    return launch_kernel(k_moe_mfma<B, G, NS, false, GU>, grid, dim3(waves * kWave), lds, st, nullptr, nullptr, p)
+    if (bits == 4 && group == 16) TTQ_MW(4, 16);
+    if (bits != 4) {
+        if (group == 16) {
+            if (bits == 2) TTQ_MW(2, 16);
+            if (bits == 3) TTQ_MW(3, 16);
+            TTQ_MW(5, 16);
+        }
+        if (bits == 2) TTQ_MW(2, 32);
+        if (bits == 3) TTQ_MW(3, 32);
+        TTQ_MW(5, 32);
+    }
+#undef TTQ_MW
 #define TTQ_MM(G)                                                                                                     \
-    return w2 ? launch_kernel(k_moe_mfma<G, NS, true, GU>, grid, dim3(waves * kWave), lds, st, nullptr, nullptr, p)   \
-              : launch_kernel(k_moe_mfma<G, NS, false, GU>, grid, dim3(waves * kWave), lds, st, nullptr, nullptr, p)
+    return w2 ? launch_kernel(k_moe_mfma<4, G, NS, true, GU>, grid, dim3(waves * kWave), lds, st, nullptr, nullptr, p)   \
+              : launch_kernel(k_moe_mfma<4, G, NS, false, GU>, grid, dim3(waves * kWave), lds, st, nullptr, nullptr, p)
     switch (group) {
         case 32: TTQ_MM(32);
         case 64: TTQ_MM(64);
@@ -476,7 +564,7 @@ static hipError_t launch_ns(const ttq_moe_args* a, const MoeLayout& L, char* ws,
         return e;
     MoeMm p{};
     p.tiles = pl.tiles; p.order = pl.order; p.slots = n;
-    p.xt = pr.xt; p.xs = pr.xs; p.K = a->K; p.kp = kp; p.rows = a->I; p.div = pr.s_stride ? 1 : (int)a->topk;
+    p.xt = pr.xt; p.xs = pr.xs; p.K = a->K; p.group = a->group; p.kp = kp; p.rows = a->I; p.div = pr.s_stride ? 1 : (int)a->topk;
     p.codes = (const uint32_t*)a->gate_up.codes; p.scale = a->gate_up.scale_f16; p.zero = a->gate_up.zero_f16;
     p.per_slice = (int)(kp / kMmChunk);
     p.w = a->w; p.s_out = a->down.s; p.s_out_stride = a->down.s_stride; p.act = a->act;
@@ -484,12 +572,12 @@ static hipError_t launch_ns(const ttq_moe_args* a, const MoeLayout& L, char* ws,
     const int64_t gw = ip / 16;
     const MmShape g = mm_shape(gw, nt, p.per_slice, n, a->E, NS);
     p.ksplit = g.nk; p.xbytes = g.xbytes;
-    if (hipError_t e = launch_mm<NS, true>(p, a->group, dim3((unsigned)((gw + g.nr - 1) / g.nr), (unsigned)nt),
+    if (hipError_t e = launch_mm<NS, true>(p, a->bits, a->group, dim3((unsigned)((gw + g.nr - 1) / g.nr), (unsigned)nt),
                                            g.nr * g.nk, g.lds(), st))
         return e;
     MoeMm d{};
     d.tiles = pl.tiles; d.order = pl.order; d.slots = n;
-    d.xt = p.ht; d.xs = p.hs; d.K = a->I; d.kp = ip; d.rows = a->M; d.div = 1;
+    d.xt = p.ht; d.xs = p.hs; d.K = a->I; d.group = a->group; d.kp = ip; d.rows = a->M; d.div = 1;
     d.codes = (const uint32_t*)a->down.codes; d.scale = a->down.scale_f16; d.zero = a->down.zero_f16;
     d.p = (float*)(ws + L.p);
     const int chunks = (int)(ip / kMmChunk), sl = moe_slices(n, a->E, a->I, a->M);
@@ -498,7 +586,7 @@ static hipError_t launch_ns(const ttq_moe_args* a, const MoeLayout& L, char* ws,
     const int64_t dw = (a->M + kMmRows - 1) / kMmRows;
     const MmShape v = mm_shape(dw, nt * nsl, d.per_slice, n, a->E, NS);
     d.ksplit = v.nk; d.xbytes = v.xbytes;
-    if (hipError_t e = launch_mm<NS, false>(d, a->group,
+    if (hipError_t e = launch_mm<NS, false>(d, a->bits, a->group,
                                             dim3((unsigned)((dw + v.nr - 1) / v.nr), (unsigned)nt, (unsigned)nsl),
                                             v.nr * v.nk, v.lds(), st))
         return e;

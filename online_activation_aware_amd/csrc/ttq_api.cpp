@@ -570,6 +570,7 @@ ttq_status ttq_linear_shared(const ttq_linear_args* layers, int n, void* ws, siz
 namespace {
 
 constexpr int64_t kMaxAdapters = 65536;
+constexpr int64_t kMaxExpertBytes = (int64_t)1 << 31;   // of one weight's codes: one buffer descriptor
 constexpr int64_t kMaxAdapterLdx = (int64_t)1 << 24;
 
 ttq_status check_experts(const char* name, const ttq_expert_state& q, int64_t K) {
@@ -586,6 +587,8 @@ ttq_status check_moe_sizes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_
     if (ttq_status e = check_quant_shape(M, K, bits, group)) return e;
     TTQ_REQUIRE(I > 0 && I <= kMaxK && I % 32 == 0 && I % group == 0,
                 "I must be a positive multiple of 32 and of the group size, at most 2^18");
+    if (2 * I * K * bits / 8 >= kMaxExpertBytes || M * I * bits / 8 >= kMaxExpertBytes)
+        return fail(TTQ_ERR_UNSUPPORTED, "an expert's codes take 2 GiB or more");
     if (T > ttq::kMoeMaxT)
         return fail(TTQ_ERR_UNSUPPORTED, "at most %d tokens a call (got %lld): pass a longer prompt in chunks",
                     (int)ttq::kMoeMaxT, (long long)T);

@@ -60,6 +60,7 @@ def test_moe(T):
                 dict(M=-1), dict(T=-1), dict(ws=None), dict(ws=FAKE + 64), dict(n=64)):
         assert call(**bad) == T.TTQ_ERR_INVALID, bad
     assert call(T=1025) == T.TTQ_ERR_UNSUPPORTED
+    assert call(K=1 << 16, ldx=1 << 16, I=1 << 15) == T.TTQ_ERR_UNSUPPORTED   # 2 GiB of gate and up codes
     assert L.ttq_moe(None, FAKE, BIG, None) == T.TTQ_ERR_INVALID
     assert call(T=0, X=None, ids=None, w=None, Y=None, ws=None, n=0) == T.TTQ_OK
     assert call(M=0, Y=None, ws=None, n=0) == T.TTQ_OK
