@@ -176,6 +176,106 @@ __global__ __launch_bounds__(kAzWaves * kWave) void k_adapter_z(const void* __re
     }
 }
 
+// 128 tokens or more, bf16 operands: a workgroup owns 32 tokens and one K
+// slice and passes it 256 channels at a time through LDS, so that memory is
+// read in rows of 512 consecutive bytes (the fragments above take 64 of each
+// row, rows 2 K bytes apart: a power of two for most K) and a row of A serves
+// both token tiles.  The next channels are in registers while one step is
+// multiplied; wave w has channels 32 w ..+31 of each step, the waves' tiles are
+// added in wave order.  One pass per distinct adapter, mostly one.
+constexpr int kArzCh = 256;
+constexpr int kArzRow = kArzCh * 2 + 16;          // LDS bytes of a row, 16 apart modulo the banks
+
+template <int RT>
+__global__ __launch_bounds__(kAzWaves * kWave) void k_adapter_z_runs(const uint16_t* __restrict__ X, int64_t T,
+                                                                     int64_t K, int64_t ldx, AdapterTable ad,
+                                                                     int64_t per, float* __restrict__ Z) {
+    constexpr int kTok = 32;
+    constexpr int NP = (kTok + 16 * RT) * (kArzCh / 8) / (kAzWaves * kWave);   // 16-byte pieces a thread stages
+    constexpr int kTile = (kTok + 16 * RT) * kArzRow, kRed = kAzWaves * 2 * RT * kWave * 16;
+    __shared__ __attribute__((aligned(16))) unsigned char smem[kTile > kRed ? kTile : kRed];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int r16 = lane & 15, q = lane >> 4;
+    const int64_t t0 = (int64_t)blockIdx.x * kTok;
+    const int64_t k0 = (int64_t)blockIdx.y * per, k1 = min(K, k0 + per);
+    const int64_t rows = min((int64_t)kTok, T - t0);
+    const int R = ad.rank;
+    const int id = (lane & 31) < rows ? ad.ids[t0 + (lane & 31)] : -1;   // lanes 0..31 and again 32..63
+    const int rk = adapter_rank(ad, id);
+    const rsrc_t rx = make_rsrc(X + t0 * ldx, ((rows - 1) * ldx + K) * 2);
+    uint32_t left = (uint32_t)__ballot(rk > 0);
+    while (left) {                                // at most 32 rounds: each takes its first token's bit
+        const int f = __builtin_ctz(left);
+        const int a = __builtin_amdgcn_readlane(id, f), ra = __builtin_amdgcn_readlane(rk, f);
+        const bool mine = rk > 0 && id == a;
+        left &= ~(uint32_t)__ballot(mine);
+        const rsrc_t rA = make_rsrc((const uint16_t*)ad.A + (int64_t)a * R * K, (int64_t)ra * K * 2);
+        u32x4 v[NP];
+        auto fetch = [&](int64_t k) __attribute__((always_inline)) {
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                const int p = tid + n * kAzWaves * kWave, r = p / (kArzCh / 8);
+                const int64_t j = k + p % (kArzCh / 8) * 8;   // K % 8 == 0: all in or all out
+                const uint32_t off = j >= k1 ? kOut : (uint32_t)((r < kTok ? r * ldx : (r - kTok) * K) + j) * 2;
+                // A wave's pieces are of X or of A alone.
+                v[n] = __builtin_bit_cast(u32x4, r < kTok ? __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(r < rows ? off : kOut), 0, 0)
+                                                          : __builtin_amdgcn_raw_buffer_load_b128(rA, (int)off, 0, 0));
+            }
+        };
+        f32x4 acc[2][RT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) acc[h][rt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        fetch(k0);
+        for (int64_t k = k0; k < k1; k += kArzCh) {
+            __syncthreads();                      // what was there has been read
+#pragma unroll
+            for (int n = 0; n < NP; ++n) {
+                const int p = tid + n * kAzWaves * kWave;
+                *(u32x4*)(smem + p / (kArzCh / 8) * kArzRow + p % (kArzCh / 8) * 16) = v[n];
+            }
+            if (k + kArzCh < k1) fetch(k + kArzCh);
+            sync_lds();
+            const unsigned char* b = smem + 64 * wave + 16 * q + r16 * kArzRow;
+            u32x4 x[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) x[h] = *(const u32x4*)(b + 16 * h * kArzRow);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const u32x4 w = *(const u32x4*)(b + (kTok + 16 * rt) * kArzRow);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) acc[h][rt] = mfma_16x16x32(w, x[h], acc[h][rt]);
+            }
+        }
+        __syncthreads();
+        f32x4* red = (f32x4*)smem;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) red[((wave * 2 + h) * RT + rt) * kWave + lane] = acc[h][rt];
+        __syncthreads();
+        // Lane of tile (h, rt): z^T[16 rt + 4 q + i][16 h + r16].
+        for (int w = wave; w < 2 * RT; w += kAzWaves) {
+            const int h = w / RT, rt = w % RT;
+            const bool take = __shfl((int)mine, 16 * h + r16) != 0;
+            f32x4 z = red[w * kWave + lane];
+            for (int u = 1; u < kAzWaves; ++u) {
+                const f32x4 y = red[(u * 2 * RT + w) * kWave + lane];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] += y[i];
+            }
+            if (take)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int kk = 16 * rt + 4 * q + i;
+                    if (kk < R) Z[((int64_t)blockIdx.y * T + t0 + 16 * h + r16) * R + kk] = z[i];
+                }
+        }
+    }
+}
+
 // ------------------------------------------------------------------ Y
 
 // Few tokens (or odd sizes): a wave owns 16 tokens and 16 rows of M at a time;
@@ -446,8 +546,8 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_y(const float* __r
 }
 
 // 128 tokens or more, mostly runs of one adapter: a wave owns 64 rows of M,
-// keeps their B in registers and goes through four tiles of 16 tokens, the
-// next tile's z and C in flight; a tile of several adapters, or another one
+// keeps their B in registers and goes through four tiles of 16 tokens, all of
+// whose C it has requested at the start; a tile of several adapters, or another one
 // than the last, loads its B.  Column m of row tile rt is row 16 (m / 4) +
 // 4 rt + m % 4 of the 64, so that a lane ends with 16 consecutive outputs of
 // one token.  R, M and the strides multiples of 8, 16-byte aligned C and Y.
@@ -459,12 +559,15 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* 
                                                                    int64_t ldy) {
     constexpr int BE = BF32 ? 4 : 2;
     constexpr int CW = CF32 ? 4 : 2;              // 16-byte pieces of 16 values
-    const int lane = threadIdx.x & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    constexpr int kTok = 16 * kArTiles;
+    constexpr int kZp = kTok * 8 * ST / (kAyWaves * kWave);   // 16-byte pieces of z a thread sums
+    static_assert(kTok == kWave, "a lane per token");
+    __shared__ __attribute__((aligned(16))) float zl[kTok][32 * ST + 4];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r16 = lane & 15, q = lane >> 4;
-    const int64_t tb = (int64_t)blockIdx.y * (16 * kArTiles);
+    const int64_t tb = (int64_t)blockIdx.y * kTok;
     const int64_t o0 = ((int64_t)blockIdx.x * kAyWaves + wave) * 64;
-    if (o0 >= M) return;
     const int R = ad.rank;
     const int64_t mrows = min((int64_t)64, M - o0);
     // Lane l: token tb + l of the four tiles.
@@ -472,53 +575,73 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* 
     const int rk_l = adapter_rank(ad, id_l);
     const float sc_l = rk_l > 0 && ad.scale != nullptr ? ad.scale[id_l] : 1.f;
 
-    struct Tile {
-        u32x4 c[CW];
-        f32x4 z[ST][2];
-    };
-    const bool oin = o0 + 16 * q < M;             // 16 consecutive rows, in eights
-    auto load = [&](Tile& s, int i) __attribute__((always_inline)) {
-        const int64_t t = tb + 16 * i + r16;
-        if (t >= T) return;
+    // z of the 64 tokens, slices in order, once for the four waves; requested
+    // before everything else, then C of the four tiles and B of the first
+    // adapter.
+    const int per = R / 4;                        // 16-byte pieces of a row of z
+    f32x4 zs[kZp];
 #pragma unroll
-        for (int h = 0; h < ST; ++h)
+    for (int n = 0; n < kZp; ++n) zs[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int64_t have = min((int64_t)kTok, T - tb) * per;
+    for (int p = 0; p < slices; ++p)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int k = 32 * h + 8 * q + 4 * e;
-                if (k < R) s.z[h][e] = *(const f32x4*)(Z + t * R + k);
+        for (int n = 0; n < kZp; ++n) {
+            const int i = tid + n * kAyWaves * kWave;
+            if (i < have) {
+                const f32x4 v = *(const f32x4*)(Z + ((int64_t)p * T + tb) * R + 4 * i);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) zs[n][e] += v[e];
             }
-        for (int p = 1; p < slices; ++p)
-#pragma unroll
-            for (int h = 0; h < ST; ++h)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int k = 32 * h + 8 * q + 4 * e;
-                    if (k < R) {
-                        const f32x4 v = *(const f32x4*)(Z + ((int64_t)p * T + t) * R + k);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) s.z[h][e][j] += v[j];
-                    }
-                }
-        if (ci.C != nullptr) {
-            const char* cp = (const char*)ci.C + (t * ci.ldc + o0 + 16 * q) * (CF32 ? 4 : 2);
-#pragma unroll
-            for (int w = 0; w < CW; ++w)
-                if (o0 + 16 * q + w * (CF32 ? 4 : 8) < M) s.c[w] = *(const u32x4*)(cp + 16 * w);
         }
-    };
-    Tile s0{}, s1{};
-    load(s0, 0);
+    const bool oin = o0 + 16 * q < M;             // 16 consecutive rows, in eights
+    u32x4 c[kArTiles][CW];
+#pragma unroll
+    for (int i = 0; i < kArTiles; ++i) {
+        const int64_t t = tb + 16 * i + r16;
+        const char* cp = (const char*)ci.C + (t * ci.ldc + o0 + 16 * q) * (CF32 ? 4 : 2);
+#pragma unroll
+        for (int w = 0; w < CW; ++w)
+            if (ci.C != nullptr && t < T && o0 + 16 * q + w * (CF32 ? 4 : 8) < M) c[i][w] = *(const u32x4*)(cp + 16 * w);
+    }
     int cur = -1;                                 // the adapter whose B is held
     Eight<BF32> b[4][ST];
-    auto compute = [&](const Tile& s, int i) __attribute__((always_inline)) {
+    auto load_rows = [&](int a, int ra) __attribute__((always_inline)) {
+        cur = a;
+        const rsrc_t rB = make_rsrc((const char*)ad.B + ((int64_t)a * M + o0) * R * BE, mrows * R * BE);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+            for (int h = 0; h < ST; ++h) {
+                const int r = 16 * (r16 >> 2) + 4 * rt + (r16 & 3);
+                b[rt][h] = load_b<BF32, true>(rB, r, 32 * h + 8 * q, ra, R, r < mrows);
+            }
+    };
+    if (const uint64_t any = __ballot(rk_l > 0); any != 0 && o0 < M) {
+        const int f = __builtin_ctzll(any);
+        load_rows(__builtin_amdgcn_readlane(id_l, f), __builtin_amdgcn_readlane(rk_l, f));
+    }
+#pragma unroll
+    for (int n = 0; n < kZp; ++n) {               // times the adapters' scales
+        const int i = tid + n * kAyWaves * kWave, t = i / per, k = (i - t * per) * 4;
+        const float sc = __shfl(sc_l, t & (kWave - 1));
+        if (t < kTok) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) zl[t][k + e] = zs[n][e] * sc;
+        }
+    }
+    sync_lds();
+    if (o0 >= M) return;
+    auto compute = [&](int i) __attribute__((always_inline)) {
         const int id = __shfl(id_l, 16 * i + r16), rk = __shfl(rk_l, 16 * i + r16);
-        const float sc = __shfl(sc_l, 16 * i + r16);
         ZOp<BF32> zo[ST];
 #pragma unroll
         for (int h = 0; h < ST; ++h) {
+            f32x4 v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) v[e] = *(const f32x4*)&zl[16 * i + r16][32 * h + 8 * q + 4 * e];
             float z[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = 32 * h + 8 * q + e < rk ? s.z[h][e / 4][e % 4] * sc : 0.f;
+            for (int e = 0; e < 8; ++e) z[e] = 32 * h + 8 * q + e < rk ? v[e / 4][e % 4] : 0.f;
             zo[h] = z_operand<BF32>(z);
         }
         f32x4 acc[4];
@@ -530,18 +653,7 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* 
             const int a = __builtin_amdgcn_readlane(id, f);
             const bool mine = rk > 0 && id == a;
             left &= ~((uint32_t)__ballot(mine) & 0xFFFFu);
-            if (a != cur) {                       // uniform
-                cur = a;
-                const int ra = __builtin_amdgcn_readlane(rk, f);
-                const rsrc_t rB = make_rsrc((const char*)ad.B + ((int64_t)a * M + o0) * R * BE, mrows * R * BE);
-#pragma unroll
-                for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-                    for (int h = 0; h < ST; ++h) {
-                        const int r = 16 * (r16 >> 2) + 4 * rt + (r16 & 3);
-                        b[rt][h] = load_b<BF32, true>(rB, r, 32 * h + 8 * q, ra, R, r < mrows);
-                    }
-            }
+            if (a != cur) load_rows(a, __builtin_amdgcn_readlane(rk, f));   // uniform
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
                 f32x4 p = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -557,11 +669,11 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* 
         if (ci.C != nullptr)
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
-                f32x4 c;
-                if constexpr (CF32) c = c4_values<true>(s.c[rt]);
-                else c = c4_values<false>(u32x4{s.c[rt / 2][2 * (rt & 1)], s.c[rt / 2][2 * (rt & 1) + 1], 0u, 0u});
+                f32x4 v;
+                if constexpr (CF32) v = c4_values<true>(c[i][rt]);
+                else v = c4_values<false>(u32x4{c[i][rt / 2][2 * (rt & 1)], c[i][rt / 2][2 * (rt & 1) + 1], 0u, 0u});
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[rt][e] += c[e];
+                for (int e = 0; e < 4; ++e) acc[rt][e] += v[e];
             }
         const int64_t o = o0 + 16 * q;
         if constexpr (YF32) {
@@ -579,13 +691,9 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* 
         }
     };
 #pragma unroll
-    for (int i = 0; i < kArTiles; i += 2) {
-        load(s1, i + 1);
+    for (int i = 0; i < kArTiles; ++i) {
+        compute(i);
         __builtin_amdgcn_sched_barrier(0);
-        compute(s0, i);
-        if (i + 2 < kArTiles) load(s0, i + 2);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(s1, i + 1);
     }
 }
 
@@ -595,12 +703,11 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* 
 // at most eight, of at least 512 channels.  A tile of a few requests spreads
 // over the chip by its adapters as well (eight shares), its slices are of at
 // least 1024; 128 tokens or more
-// (runs of few adapters) by their tiles, with two slices at most where those
-// fill it.
+// (runs of few adapters) by their tiles.
 static int z_shares(int64_t T) { return T == 1 || T >= 128 ? 1 : 8; }
 static int64_t z_slices(int64_t T, int64_t K, int64_t* per) {
     const int64_t tiles = (T + 15) / 16;
-    int64_t s = tiles > 0 ? (T < 128 ? 8 : (256 + tiles - 1) / tiles) : 1;
+    int64_t s = tiles > 0 ? (T < 128 ? 8 : (512 + tiles - 1) / tiles) : 1;
     const int64_t least = T > 1 && T < 128 ? 1024 : 512, most = K / least > 0 ? K / least : 1;
     s = s > most ? most : s;
     s = s > 8 ? 8 : s;
@@ -618,6 +725,17 @@ static hipError_t launch_z(const void* X, int64_t T, int64_t K, int64_t ldx, con
                            hipStream_t st) {
     int64_t per;
     const int64_t s = z_slices(T, K, &per);
+    if constexpr (!XF32 && !AF32)
+        if (T >= 128) {
+            const dim3 grid((unsigned)((T + 31) / 32), (unsigned)s);
+#define TTQ_AZR(RT)                                                                                                  \
+    return launch_kernel(k_adapter_z_runs<RT>, grid, dim3(kAzWaves * kWave), 0, st, nullptr, nullptr,                \
+                         (const uint16_t*)X, T, K, ldx, ad, per, Z)
+            if (ad.rank <= 16) TTQ_AZR(1);
+            if (ad.rank <= 32) TTQ_AZR(2);
+            TTQ_AZR(4);
+#undef TTQ_AZR
+        }
     const dim3 grid((unsigned)((T + 15) / 16), (unsigned)s, (unsigned)z_shares(T));
 #define TTQ_AZ(RT)                                                                                                     \
     return launch_kernel(k_adapter_z<XF32, AF32, RT>, grid, dim3(kAzWaves * kWave), 0, st, nullptr, nullptr, X, T, K, \
