@@ -28,7 +28,9 @@ struct LowrankEpilogue {
 template <typename F, typename... Args>
 inline hipError_t launch_kernel(F kern, dim3 grid, dim3 block, size_t lds, hipStream_t st, hipEvent_t e0,
                                 hipEvent_t e1, Args... args) {
-    hipExtLaunchKernelGGL(kern, grid, block, (std::uint32_t)lds, st, e0, e1, 0u, args...);
+    // (The plain launch costs the host 0.4 us less than one that could stamp.)
+    if (e0 == nullptr && e1 == nullptr) kern<<<grid, block, lds, st>>>(args...);
+    else hipExtLaunchKernelGGL(kern, grid, block, (std::uint32_t)lds, st, e0, e1, 0u, args...);
     return hipGetLastError();
 }
 

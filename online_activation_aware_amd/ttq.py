@@ -482,10 +482,20 @@ def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device:
     return t.data_ptr()
 
 
+_CODES = {torch.float32: TTQ_F32, torch.bfloat16: TTQ_BF16}
+
+
+def _code(t: torch.Tensor) -> int:
+    c = _CODES.get(t.dtype)
+    return c if c is not None else _dtype_code(t)
+
+
 def _row_stride(t: torch.Tensor, name: str) -> int:
     """Row stride of a matrix; that of a single row does not matter."""
-    ld = _ld(t, name)
-    return ld if t.shape[0] > 1 else t.shape[1]
+    st = t.stride()
+    if len(st) != 2 or st[1] != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must be 2-D with unit stride in its last dimension")
+    return st[0] if t.shape[0] > 1 else t.shape[1]
 
 
 def _output(Y: Optional[torch.Tensor], shape: tuple, y_dtype, X: torch.Tensor, name: str = "Y") -> torch.Tensor:
@@ -533,7 +543,7 @@ def ttq_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax", renor
         wp = w.data_ptr()
     else:
         wp = _dense(w, "w", torch.float32, (T, topk), dev)
-    _check(lib().ttq_moe_route(logits.data_ptr(), _dtype_code(logits), T, E, ld, topk, TTQ_SCORES[score],
+    _check(lib().ttq_moe_route(logits.data_ptr(), _code(logits), T, E, ld, topk, TTQ_SCORES[score],
                                int(bool(renormalize)), ip, wp, stream))
     return ids, w
 
@@ -551,11 +561,11 @@ def moe_workspace(T: int, topk: int, K: int, I: int, M: int, E: int, bits: int, 
 def _expert_state(name: str, q: dict, E: int, rows: int, K: int, bits: int, group: int, dev) -> ExpertState:
     s = q["s"]
     per = isinstance(s, torch.Tensor) and s.dim() == 2
-    return ExpertState(
-        s=_dense(s, f"{name} s", torch.float32, (E, K) if per else (K,), dev), s_stride=K if per else 0,
-        codes=_dense(q["codes"], f"{name} codes", torch.int32, (E, rows, K * bits // 32), dev),
-        scale_f16=_dense(q["scale_f16"], f"{name} scale_f16", torch.float16, (E, rows, K // group), dev),
-        zero_f16=_dense(q["zero_f16"], f"{name} zero_f16", torch.float16, (E, rows, K // group), dev))
+    return ExpertState(       # in the order of its fields
+        _dense(s, name + " s", torch.float32, (E, K) if per else (K,), dev), K if per else 0,
+        _dense(q["codes"], name + " codes", torch.int32, (E, rows, K * bits // 32), dev),
+        _dense(q["scale_f16"], name + " scale_f16", torch.float16, (E, rows, K // group), dev),
+        _dense(q["zero_f16"], name + " zero_f16", torch.float16, (E, rows, K // group), dev))
 
 
 @_on_tensor_device
@@ -582,11 +592,12 @@ def ttq_moe(X: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up: dict, 
     Y = _output(Y, (T, M), y_dtype, X)
     wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_moe_workspace_bytes(T, topk, K, I, M, E, bits, group),
                           X)
-    a = MoeArgs(X=X.data_ptr(), xt=_dtype_code(X), T=T, K=K, ldx=ldx,
-                ids=_dense(ids, "ids", torch.int32, (T, topk), dev), w=_dense(w, "w", torch.float32, (T, topk), dev),
-                topk=topk, E=E, I=I, M=M, gate_up=_expert_state("gate_up", gate_up, E, rows2, K, bits, group, dev),
-                down=_expert_state("down", down, E, M, I, bits, group, dev), bits=bits, group=group,
-                act=TTQ_ACTS[act], Y=Y.data_ptr(), yt=_dtype_code(Y), ldy=_row_stride(Y, "Y"))
+    a = MoeArgs(              # in the order of its fields
+        X.data_ptr(), _code(X), T, K, ldx, _dense(ids, "ids", torch.int32, (T, topk), dev),
+        _dense(w, "w", torch.float32, (T, topk), dev), topk, E, I, M,
+        _expert_state("gate_up", gate_up, E, rows2, K, bits, group, dev),
+        _expert_state("down", down, E, M, I, bits, group, dev), bits, group, TTQ_ACTS[act], Y.data_ptr(), _code(Y),
+        _row_stride(Y, "Y"))
     _check(lib().ttq_moe(ctypes.byref(a), wp, wn, stream))
     return Y
 
@@ -604,13 +615,13 @@ def _adapters(A, B, ids, ranks, scale, T: int, K: int, M: Optional[int], dev) ->
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError("A must be [n][rank][K] and B [n][M][rank]")
     n, rank, _ = A.shape
-    dt = _dtype_code(A)
-    return AdaptersArgs(
-        A=_dense(A, "A", A.dtype, (n, rank, K), dev),
-        B=_dense(B, "B", A.dtype, (n, B.shape[1] if M is None else M, rank), dev), dt=dt, n=n, rank=rank,
-        ranks=None if ranks is None else _dense(ranks, "ranks", torch.int32, (n,), dev),
-        scale=None if scale is None else _dense(scale, "scale", torch.float32, (n,), dev),
-        ids=_dense(ids, "ids", torch.int32, (T,), dev))
+    dt = _code(A)
+    return AdaptersArgs(      # in the order of its fields
+        _dense(A, "A", A.dtype, (n, rank, K), dev),
+        _dense(B, "B", A.dtype, (n, B.shape[1] if M is None else M, rank), dev), dt, n, rank,
+        None if ranks is None else _dense(ranks, "ranks", torch.int32, (n,), dev),
+        None if scale is None else _dense(scale, "scale", torch.float32, (n,), dev),
+        _dense(ids, "ids", torch.int32, (T,), dev))
 
 
 @_on_tensor_device
@@ -636,8 +647,8 @@ def ttq_adapters_add(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: tor
             raise TypeError("C must have Y's dtype")
         cp, ldc = C.data_ptr(), _row_stride(C, "C")
     wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_adapters_workspace_bytes(T, K, M, ad.rank), X)
-    _check(lib().ttq_adapters_add(X.data_ptr(), _dtype_code(X), T, K, ldx, ctypes.byref(ad), M, cp, ldc, Y.data_ptr(),
-                                  _dtype_code(Y), _row_stride(Y, "Y"), wp, wn, stream))
+    _check(lib().ttq_adapters_add(X.data_ptr(), _code(X), T, K, ldx, ctypes.byref(ad), M, cp, ldc, Y.data_ptr(),
+                                  _code(Y), _row_stride(Y, "Y"), wp, wn, stream))
     return Y
 
 
@@ -668,11 +679,11 @@ def ttq_qgemm_adapters(X: torch.Tensor, s: torch.Tensor, codes: torch.Tensor, sc
     wp, wn, ws = _scratch(
         ws, 0 if ws is not None else lib().ttq_qgemm_adapters_workspace_bytes(T, K, M, bits, group, ad.rank), X)
     _check(lib().ttq_qgemm_adapters(
-        X.data_ptr(), _dtype_code(X), T, K, ldx, _dense(s, "s", torch.float32, (K,), dev),
+        X.data_ptr(), _code(X), T, K, ldx, _dense(s, "s", torch.float32, (K,), dev),
         _dense(codes, "codes", torch.int32, (M, K * bits // 32), dev),
         _dense(scale_f16, "scale_f16", torch.float16, (M, K // group), dev),
         _dense(zero_f16, "zero_f16", torch.float16, (M, K // group), dev), M, bits, group, ctypes.byref(ad),
-        Y.data_ptr(), _dtype_code(Y), _row_stride(Y, "Y"), wp, wn, stream))
+        Y.data_ptr(), _code(Y), _row_stride(Y, "Y"), wp, wn, stream))
     return Y
 
 
