@@ -519,7 +519,11 @@ int moe_slices(int64_t n, int64_t E, int64_t I, int64_t M) {
     const int64_t tiles = moe_tiles(n, E, kMmTile), waves = (M + kMmRows - 1) / kMmRows * tiles;
     if (waves == 0) return 1;                     // an empty call
     const int64_t chunks = moe_pad(I) / kMmChunk, most = chunks / 8 > 0 ? chunks / 8 : 1;
-    int64_t s = (2048 + waves - 1) / waves;
+    // The wide workgroups (one of 16 waves on a compute unit, for experts of
+    // more than four slots) come in several rounds: 128 tokens over 8 experts,
+    // 14336 -> 4096, 556 us with one slice (160 workgroups), 441 us with three.
+    const int64_t want = n > 4 * E ? 6144 : 2048;
+    int64_t s = (want + waves - 1) / waves;
     if (s > most) s = most;
     return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
 }
