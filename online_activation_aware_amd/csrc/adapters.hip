@@ -388,7 +388,7 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_y(const float* __r
                                                                 int64_t ldy, int blocks, int share, int cvec,
                                                                 int yvec) {
     constexpr int BE = BF32 ? 4 : 2;
-    constexpr int U = 4;
+    constexpr int U = 8;
     constexpr int kZRow = 32 * ST + 4;
     constexpr int kZn = 32 * ST * 16 / (kAyWaves * kWave);   // z values a thread sums
     __shared__ __attribute__((aligned(16))) float zl[16][kZRow];
@@ -543,6 +543,64 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_y(const float* __r
         __builtin_amdgcn_sched_barrier(0);
         compute(i1, i + 1);
     }
+}
+
+// One token: a single launch.  Every workgroup (128 rows of M, four threads a
+// row) forms z itself, a wave a rank at a time; A passes through the L2 once
+// per workgroup, which for small A costs less than a second launch (4096 ->
+// 4096, rank 16: 5.0 us, 9.4 us in two).
+constexpr int kA1Rows = 128, kA1Threads = 512;
+constexpr int64_t kA1Bytes = (int64_t)16 << 20;   // of A over all workgroups
+
+template <bool XF32, bool AF32, bool CF32, bool YF32>
+__global__ __launch_bounds__(kA1Threads) void k_adapter_one(const void* __restrict__ X, int64_t K, AdapterTable ad,
+                                                            ProjectionIn ci, int64_t M, void* Y) {
+    __shared__ float z[64];
+    constexpr int XE = XF32 ? 4 : 2, AE = AF32 ? 4 : 2;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int a = __builtin_amdgcn_readfirstlane(ad.ids[0]);
+    const int ra = __builtin_amdgcn_readfirstlane(adapter_rank(ad, a));
+    const int R = ad.rank;
+    const int64_t o = (int64_t)blockIdx.x * kA1Rows + tid / 4;
+    const rsrc_t rx = make_rsrc(X, K * XE);
+    constexpr int U = 4;                          // pieces of 8 channels in flight
+    for (int k = wave; k < ra; k += kA1Threads / kWave) {
+        const rsrc_t rA = make_rsrc((const char*)ad.A + ((int64_t)a * R + k) * K * AE, K * AE);
+        float s = 0.f;
+        for (int64_t j0 = 8 * lane; j0 < K; j0 += 8 * U * kWave) {
+            Eight<XF32> x[U];
+            Eight<AF32> w[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {         // behind K: zeros
+                x[u] = load_eight<XF32>(rx, (uint32_t)((j0 + 8 * u * kWave) * XE));
+                w[u] = load_eight<AF32>(rA, (uint32_t)((j0 + 8 * u * kWave) * AE));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = __builtin_fmaf(eight_at<AF32>(w[u], e), eight_at<XF32>(x[u], e), s);
+        }
+#pragma unroll
+        for (int m = 1; m < kWave; m <<= 1) s += __shfl_xor(s, m);
+        if (lane == 0) z[k] = s;
+    }
+    __syncthreads();
+    if (o >= M) return;                           // whole quads
+    float y = 0.f;
+    for (int k = tid & 3; k < ra; k += 4) {
+        const int64_t i = ((int64_t)a * M + o) * R + k;
+        y = __builtin_fmaf(AF32 ? ((const float*)ad.B)[i] : bf16_to_f32(((const uint16_t*)ad.B)[i]), z[k], y);
+    }
+    y += __shfl_xor(y, 1);
+    y += __shfl_xor(y, 2);
+    if ((tid & 3) != 0) return;
+    if (ra > 0 && ad.scale != nullptr) y *= ad.scale[a];
+    float c = 0.f;
+    if (ci.C != nullptr) c = CF32 ? ((const float*)ci.C)[o] : bf16_to_f32(((const uint16_t*)ci.C)[o]);
+    if (ra > 0) c += y;
+    if constexpr (YF32) ((float*)Y)[o] = c;
+    else ((uint16_t*)Y)[o] = (uint16_t)f32_to_bf16(c);
 }
 
 // 128 tokens or more, mostly runs of one adapter: a wave owns 64 rows of M,
@@ -701,10 +759,10 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* 
 
 // K slices of z, whose partials every workgroup of the second launch adds:
 // at most eight, of at least 512 channels.  A tile of a few requests spreads
-// over the chip by its adapters as well (eight shares), its slices are of at
-// least 1024; 128 tokens or more
+// over the chip by its adapters as well (sixteen shares), its slices are of at
+// least 1024 (48 requests: 22.8 us; eight shares 23.9, slices of 512 24.5); 128 tokens or more
 // (runs of few adapters) by their tiles.
-static int z_shares(int64_t T) { return T == 1 || T >= 128 ? 1 : 8; }
+static int z_shares(int64_t T) { return T == 1 || T >= 128 ? 1 : 16; }
 static int64_t z_slices(int64_t T, int64_t K, int64_t* per) {
     const int64_t tiles = (T + 15) / 16;
     int64_t s = tiles > 0 ? (T < 128 ? 8 : (512 + tiles - 1) / tiles) : 1;
@@ -788,9 +846,30 @@ static hipError_t launch_y(const float* Z, int64_t T, int64_t K, const AdapterTa
 #undef TTQ_AY2
 }
 
+template <bool CF32, bool YF32>
+static hipError_t launch_one(const void* X, bool xf32, int64_t K, const AdapterTable& ad, const ProjectionIn& ci, int64_t M,
+                             void* Y, hipStream_t st) {
+    const dim3 grid((unsigned)((M + kA1Rows - 1) / kA1Rows)), block(kA1Threads);
+#define TTQ_A1(XF, AF) \
+    return launch_kernel(k_adapter_one<XF, AF, CF32, YF32>, grid, block, 0, st, nullptr, nullptr, X, K, ad, ci, M, Y)
+    if (xf32) {
+        if (ad.f32) TTQ_A1(true, true);
+        TTQ_A1(true, false);
+    }
+    if (ad.f32) TTQ_A1(false, true);
+    TTQ_A1(false, false);
+#undef TTQ_A1
+}
+
 hipError_t launch_adapters(const void* X, bool xf32, int64_t T, int64_t K, int64_t ldx, const AdapterTable& ad,
                            const ProjectionIn& ci, int64_t M, void* Y, bool yf32, int64_t ldy, float* Z,
                            hipStream_t st) {
+    if (T == 1 && ci.parts == 1 && (M + kA1Rows - 1) / kA1Rows * ad.rank * K * (ad.f32 ? 4 : 2) <= kA1Bytes) {
+        if (ci.f32) return yf32 ? launch_one<true, true>(X, xf32, K, ad, ci, M, Y, st)
+                                : launch_one<true, false>(X, xf32, K, ad, ci, M, Y, st);
+        return yf32 ? launch_one<false, true>(X, xf32, K, ad, ci, M, Y, st)
+                    : launch_one<false, false>(X, xf32, K, ad, ci, M, Y, st);
+    }
     hipError_t e;
     if (xf32) e = ad.f32 ? launch_z<true, true>(X, T, K, ldx, ad, Z, st) : launch_z<true, false>(X, T, K, ldx, ad, Z, st);
     else e = ad.f32 ? launch_z<false, true>(X, T, K, ldx, ad, Z, st) : launch_z<false, false>(X, T, K, ldx, ad, Z, st);

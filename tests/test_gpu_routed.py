@@ -193,6 +193,9 @@ def adapter_inputs(seed, Tn, K, M, n, rank, at, mode):
 ADAPTERS = [  # T, K, M, n, rank, xt, at, yt, ids
     (1, 4096, 512, 3, 16, "bf16", "bf16", "bf16", "one"),
     (1, 8, 1, 1, 1, "bf16", "bf16", "f32", "one"),
+    (1, 4096, 14344, 2, 64, "bf16", "bf16", "f32", "one"),
+    (1, 520, 131, 3, 13, "f32", "bf16", "f32", "one"),
+    (1, 2056, 300, 3, 64, "bf16", "f32", "bf16", "one"),
     (5, 40, 33, 2, 3, "bf16", "bf16", "f32", "mixed"),
     (16, 256, 100, 7, 8, "bf16", "bf16", "f32", "mixed"),
     (33, 776, 130, 40, 32, "bf16", "bf16", "f32", "mixed"),
