@@ -25,6 +25,7 @@ struct MoePlan {
 };
 
 constexpr int kPlanThreads = 512;
+constexpr int kSimds = 4 * 256;                   // of the chip
 
 // One workgroup of kPlanThreads: the slots grouped by expert into `order`
 // and the tiles, unused ones with count 0.  The place of a slot within its

@@ -306,13 +306,13 @@ int moe_dot_tile(const ttq_moe_args* a) {
 }
 
 // Row groups and waves on each one's pieces, up to eight waves a workgroup:
-// as many waves as pieces allow until the chip has 4096 (four per SIMD).
+// as many waves as pieces allow until the chip has three per SIMD.
 struct MdShape {
     int nr, nk;
 };
 static MdShape md_shape(int64_t groups, int64_t pieces) {
     MdShape s{1, 1};
-    while (s.nk < kMdMaxWaves && s.nk * 2 <= pieces && groups * s.nk < 3072) s.nk *= 2;
+    while (s.nk < kMdMaxWaves && s.nk * 2 <= pieces && groups * s.nk < 3 * kSimds) s.nk *= 2;
     while (s.nr * s.nk < 4 && groups / s.nr > 1024) s.nr *= 2;
     return s;
 }

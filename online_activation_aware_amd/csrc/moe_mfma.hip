@@ -1,7 +1,8 @@
 // The mixture-of-experts layer on the matrix cores.
 //
-// 4-bit codes in groups of 32, 64 or 128 (the sums form): as in the few-token projection (qgemv_gs.hip) codes are never expanded to
-// weights: per 32-channel subgroup the matrix cores form
+// 4-bit codes in groups of 32, 64 or 128 (the sums form): as in the few-token
+// projection (qgemv_gs.hip) codes are never expanded to weights: per 32-channel
+// subgroup the matrix cores form
 //   P[t][o] = sum_j (16 + q_oj) x~_tj,
 // slots as the 16 rows and code rows as the 16 columns of a 16x16x32 MFMA,
 // and a group adds step P - step (zero + 16) S_t, S_t = sum_j x~_tj, the
@@ -20,18 +21,22 @@
 // whose own 8 bits one more rounding would nearly double in error), 24 for
 // three (fp32 X).  The matrix cores have the room: a step is bound by the
 // codes' way from HBM and the integer work of expanding them.  The terms and
-// the 32-channel sums are laid out once per row (k_moe_prep; the first
+// the 16-channel sums are laid out once per row (k_moe_prep; the first
 // product's epilogue for h), each 8 channels in the order 0 2 4 6 1 3 5 7
 // that the expansion produces, so that a lane loads an operand with one
 // 16-byte load.
 //
-// A workgroup owns 64 code rows (four column tiles; the first product: 32
-// gate rows and their 32 up rows) and up to 16 slots of one expert; its waves
-// take pairs of 128-channel chunks (256 channels: whole 128-byte lines of
-// codes per row) in turn, the next chunk's loads in flight while one is
-// multiplied, and their tiles are added in wave order through LDS.  The
-// second product's channels can be split further over workgroups (slices);
-// the sum over a token's slots adds the slices, too.
+// A wave owns 32 code rows (the first product: 16 gate rows and their 16 up
+// rows) and up to 16 slots of one expert; the waves of a workgroup share the
+// slots' x~ in LDS, brought there by direct loads, and go through the channels
+// in blocks of four chunks of 128, the next block's codes in flight in
+// registers while one is multiplied.  With few row groups the blocks of one go
+// to several waves, whose tiles are added in wave order through LDS; the second
+// product's channels can be split further over workgroups (slices), which the
+// sum over a token's slots adds.
+//
+// What bounds it (64 experts, 2 of them per token, 4096 -> 2 x 1408 -> 4096,
+// ... see mm_shape): FIGS
 #include "codes.hpp"
 #include "common.hpp"
 #include "launch.hpp"
@@ -489,8 +494,8 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
 // experts have at most four slots on average (their tiles mostly fit); else
 // 16 with two buffers (measured, 128 tokens over 8 experts, 32 slots each: 633
 // us against 661 with eight waves and one buffer; 16 tokens over 64 experts,
-// 1.5 slots each: 97 us against 87).  Where there are fewer than 3072 waves,
-// the blocks of a row group's channels go to up to four waves, and where the
+// 1.5 slots each: 97 us against 87).  Where there are fewer than three
+// waves per SIMD, the blocks of a row group's channels go to up to four waves, and where the
 // chip would not get its workgroups, they are smaller.
 struct MmShape {
     int nr, nk, xbytes;
@@ -505,7 +510,7 @@ static MmShape mm_shape(int64_t waves, int64_t tiles, int64_t chunks, int64_t n,
     s.xbytes = (int)(need < most_x ? (need + 15) / 16 * 16 : most_x);
     const int most = wide ? 16 : 8;
     const int64_t wgs = wide ? 256 : 512;
-    while (s.nk < 4 && waves * tiles * s.nk < 3072 && chunks >= 2 * kMmBlock * s.nk) s.nk *= 2;
+    while (s.nk < 4 && waves * tiles * s.nk < 3 * kSimds && chunks >= 2 * kMmBlock * s.nk) s.nk *= 2;
     s.nr = most / s.nk;
     while (s.nr > 1 && s.nr * s.nk > 2 && (waves + s.nr - 1) / s.nr * tiles < wgs) s.nr /= 2;
     const int red = s.nr * s.nk * 2 * kWave * 16;   // the waves' tiles, where they are added
