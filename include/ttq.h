@@ -395,14 +395,16 @@ typedef struct ttq_expert_state {
  *   All sums are kept in fp32; Y is rounded once.  x / s and h enter the
  *   products with 16 bits for bf16 X and 24 for fp32 X (one or two tokens on
  *   4-bit codes in groups of 32 or more: to 2^-19 or 2^-23 of the largest of
- *   their 32 channels), codes, steps and zeros exactly.  Results of a token do not depend on the other
- *   tokens of the call beyond fp32 rounding, and are reproducible run to run.
+ *   their 32 channels), codes, steps and zeros exactly.  Results of a token do
+ *   not depend on the other tokens of the call beyond fp32 rounding, and are
+ *   reproducible run to run; an infinite or NaN x / s or h makes its token's
+ *   outputs NaN and no other's.
  *   K and I multiples of 32 and of group, at most 2^18; E <= 1024;
  *   1 <= topk <= 32; T > 1024, or an expert's gate_up or down codes of 2 GiB
  *   or more, return TTQ_ERR_UNSUPPORTED.  T == 0 or M == 0 is an empty call.
- *   ws: ttq_moe_workspace_bytes(T, topk, K, I, M, E, bits,
- *   group) bytes, 256-byte aligned; calls that may run at the same time need
- *   workspaces of their own.
+ *   ws: ttq_moe_workspace_bytes(T, topk, K, I, M, E, bits, group) bytes,
+ *   256-byte aligned; calls that may run at the same time need workspaces of
+ *   their own.
  */
 typedef struct ttq_moe_args {
     const void* X;  int xt;  int64_t T;  int64_t K;  int64_t ldx;

@@ -43,6 +43,24 @@ struct Digits {
 // u = X + 88..8 has the digits plus 8 as nibbles; nibble d of it as a signed digit.
 __device__ __forceinline__ uint32_t digit_of(uint32_t u, int d) { return ((u >> (4 * d)) & 15u) ^ 8u; }
 
+// |x| as bits, whose largest is a NaN's if there is one (fmax would drop it).
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu; }
+// x as an integer of ND digits where the largest of its 32 is mx: by up * inv,
+// `up` so that kMax / mx stays finite.  Of no meaning (but defined) where mx is
+// no finite number: the scale then carries it.
+template <int ND>
+struct ToDigits {
+    float up, inv;
+    __device__ __forceinline__ explicit ToDigits(float mx) {
+        up = mx < 0x1p-64f ? 0x1p64f : 1.f;
+        inv = mx > 0.f ? (float)Digits<ND>::kMax / (mx * up) : 0.f;
+    }
+    __device__ __forceinline__ int operator()(float x) const {
+        constexpr float m = (float)Digits<ND>::kMax;
+        return (int)rintf(fminf(fmaxf(x * up * inv, -m), m));
+    }
+};
+
 // x~ of a row: digits [ND][kp / 8] words, then per 32 channels the scale and
 // the sum of the integers, [2][kp / 32] floats.
 template <int ND>
@@ -70,17 +88,18 @@ __global__ __launch_bounds__(kPlanThreads) void k_moe_dot_prep(MoePlan pl, MoePr
     }
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (use) moe_load_scaled<XF32>(x, a, t, e, k0);
-    float mx = 0.f;
+    uint32_t mb = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(x[j]));
-    mx = fmaxf(mx, __shfl_xor(mx, 1));
-    mx = fmaxf(mx, __shfl_xor(mx, 2));
-    const float inv = mx > 0.f ? (float)Digits<ND>::kMax / mx : 0.f;
+    for (int j = 0; j < 8; ++j) mb = max(mb, abs_bits(x[j]));
+    mb = max(mb, (uint32_t)__shfl_xor((int)mb, 1));
+    mb = max(mb, (uint32_t)__shfl_xor((int)mb, 2));
+    const float mx = __builtin_bit_cast(float, mb);
+    const ToDigits<ND> digits(mx);
     uint32_t w[ND] = {};
     int sum = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int v = min(max((int)rintf(x[j] * inv), -Digits<ND>::kMax), Digits<ND>::kMax);
+        const int v = digits(x[j]);
         sum += v;
 #pragma unroll
         for (int d = 0; d < ND; ++d) w[d] |= digit_of((uint32_t)v + Digits<ND>::kBias, d) << (4 * j);
@@ -186,6 +205,13 @@ __global__ __launch_bounds__(kMdMaxWaves * kWave, TT == 1 ? 3 : 2) void k_moe_do
         // Steps and zeros of row `lane` to LDS (its reads of the piece before
         // are done: LDS operations of a wave keep their order).
         __builtin_amdgcn_wave_barrier();
+        if ((p + 1) * NG > gpr)                   // behind the row: the next row's, which may be anything
+#pragma unroll
+            for (int v = 0; v < NG / 2; ++v) {
+                const uint32_t m = p * NG + 2 * v + 1 < gpr ? 0xFFFFFFFFu : p * NG + 2 * v < gpr ? 0xFFFFu : 0u;
+                sw[v] &= m;
+                zw[v] &= m;
+            }
 #pragma unroll
         for (int v = 0; v < NG / 2; ++v) {
             my[lane * kSzRow + 2 * v] = __builtin_amdgcn_perm(zw[v], sw[v], 0x05040100u);
@@ -213,7 +239,7 @@ __global__ __launch_bounds__(kMdMaxWaves * kWave, TT == 1 ? 3 : 2) void k_moe_do
                     for (int w = 0; w < 4; ++w) dd = __builtin_amdgcn_sdot8((int)xd[t][d][w], (int)c[w], dd, false);
                     v = (int)((uint32_t)v << 4) + dd;
                 }
-                acc[r][t] = __builtin_fmaf(st * xs[t], __builtin_fmaf(z8, xsum[t], (float)v), acc[r][t]);
+                acc[r][t] = __builtin_fmaf(st, xs[t] * __builtin_fmaf(z8, xsum[t], (float)v), acc[r][t]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -271,11 +297,11 @@ __global__ __launch_bounds__(kMdMaxWaves * kWave, TT == 1 ? 3 : 2) void k_moe_do
             float h = 0.f;
             if (o < a.rows)
                 h = moe_act(gate, a.act) * up * (a.w[slot[t]] / a.s_out[tl.expert * a.s_out_stride + o]);
-            float mx = fabsf(h);
+            uint32_t mb = abs_bits(h);
 #pragma unroll
-            for (int m = 1; m < kWave; m <<= 1) mx = fmaxf(mx, __shfl_xor(mx, m));
-            const float inv = mx > 0.f ? (float)Digits<ND>::kMax / mx : 0.f;
-            const int v = min(max((int)rintf(h * inv), -Digits<ND>::kMax), Digits<ND>::kMax);
+            for (int m = 1; m < kWave; m <<= 1) mb = max(mb, (uint32_t)__shfl_xor((int)mb, m));
+            const float mx = __builtin_bit_cast(float, mb);
+            const int v = ToDigits<ND>(mx)(h);
             int sum = f < 8 ? v : 0;
 #pragma unroll
             for (int m = 1; m < kWave; m <<= 1) sum += __shfl_xor(sum, m);

@@ -35,8 +35,15 @@
 // product's channels can be split further over workgroups (slices), which the
 // sum over a token's slots adds.
 //
-// What bounds it (64 experts, 2 of them per token, 4096 -> 2 x 1408 -> 4096,
-// ... see mm_shape): FIGS
+// What bounds it.  128 tokens, two each of 8 experts, 4096 -> 2 x 14336 -> 4096,
+// groups of 64: 441 us, 1.8 TB/s of codes (each read once from memory) and 410
+// TFLOP/s counting both terms: vector instructions half of the busy cycles
+// (expanding, once per tile of 16 slots), matrix instructions 30%, and waves
+// enough to overlap them only with 128 registers each (eight waves instead of
+// 16 on a compute unit: 515 us; tiles of 32 slots, which halve the expanding
+// but take two operands' registers: 471 us at best).  16 tokens, six each of 64
+// experts, 2048 -> 2 x 1056 -> 2048: 75 us, 1.5 slots per tile of 16, where a
+// launch per product, its first loads and its end cost as much as the stream.
 #include "codes.hpp"
 #include "common.hpp"
 #include "launch.hpp"
@@ -266,7 +273,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
             }
             if constexpr (!kSums) {
                 const int ch = (cb + i) * kMmChunk + 32 * q;   // first channel of this lane
-                const uint32_t g = i < cnt ? wo[rt] + (uint32_t)(SG == 2 ? ch / 16 : ch / a.group) * 2 : 0x80000000u;
+                const uint32_t g = i < cnt && ch < K ? wo[rt] + (uint32_t)(SG == 2 ? ch / 16 : ch / a.group) * 2 : 0x80000000u;
 #pragma unroll
                 for (int h = 0; h < SG; ++h) {
                     c.st[h] = __builtin_amdgcn_raw_buffer_load_b16(rsc, (int)(g + sa + 2 * h), 0, 0);
@@ -402,6 +409,14 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
 #pragma unroll
                 for (int v = 0; v < NH; ++v)
                     nb[v] = -(half_of(sw[v / 2], v & 1) * (half_of(zw[v / 2], v & 1) + 16.f));
+                const int left = (int)gpr - (cb + b) * NG - gpart * NH;   // groups of the row from here
+                if (left < NH)                    // behind the row: the next row's, which may be anything
+#pragma unroll
+                    for (int v = 0; v < NH; ++v)
+                        if (v >= left) {
+                            nb[v] = 0.f;
+                            sw[v / 2] &= v & 1 ? 0xFFFFu : 0u;
+                        }
 #pragma unroll
                 for (int v = 0; v < NH / 2; ++v) ((uint32_t*)(st_l + grow * NB + gpart * NH))[v] = sw[v];
 #pragma unroll
@@ -494,9 +509,10 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
 // experts have at most four slots on average (their tiles mostly fit); else
 // 16 with two buffers (measured, 128 tokens over 8 experts, 32 slots each: 633
 // us against 661 with eight waves and one buffer; 16 tokens over 64 experts,
-// 1.5 slots each: 97 us against 87).  Where there are fewer than three
-// waves per SIMD, the blocks of a row group's channels go to up to four waves, and where the
-// chip would not get its workgroups, they are smaller.
+// 1.5 slots each: 97 us against 87; both before the steps that followed).
+// Where there are fewer than three waves per SIMD, the blocks of a row group's
+// channels go to up to four waves, and where the chip would not get its
+// workgroups, they are smaller.
 struct MmShape {
     int nr, nk, xbytes;
     size_t lds() const { return (size_t)nr * nk * kMmStepLds + xbytes; }

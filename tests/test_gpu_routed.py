@@ -1,6 +1,8 @@
 """Projections whose weights each token chooses: the expert router, the
 mixture-of-experts layer on quantized experts, adapters of many requests, and
 a shared projection with adapters, element by element against fp64."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -112,6 +114,15 @@ MOE = [  # T, E, topk, K, I, M, bits, group, xt, yt, act
     (33, 3, 2, 256, 128, 64, 5, 128, "bf16", "f32", "gelu"),
     (6, 3, 3, 320, 192, 70, 3, 64, "bf16", "bf16", "silu"),
     (19, 6, 2, 384, 256, 100, 4, 64, "f32", "bf16", "silu"),
+    # more than 16 slots an expert: 33 (one behind a tile of 32), several rounds of channels, odd numbers of groups
+    (33, 1, 1, 1024, 288, 40, 4, 32, "bf16", "f32", "silu"),
+    (70, 2, 2, 2048, 1408, 72, 4, 32, "bf16", "bf16", "silu"),
+    (40, 2, 1, 1312, 352, 136, 4, 32, "f32", "f32", "gelu"),
+    (50, 2, 2, 1024, 768, 64, 4, 128, "f32", "f32", "silu"),
+    (90, 3, 2, 1536, 640, 300, 4, 64, "bf16", "f32", "silu"),
+    (60, 2, 2, 1024, 512, 40, 3, 16, "f32", "f32", "gelu"),
+    (60, 2, 2, 800, 544, 40, 2, 32, "bf16", "bf16", "silu"),
+    (60, 2, 2, 640, 1024, 40, 5, 64, "bf16", "f32", "silu"),
 ]
 
 
@@ -148,6 +159,49 @@ def test_moe_slots_without_an_expert_and_strides(T, bits, group, xt, Tn):
     ref.check(y[:, 2:2 + M], r, b, False)
     assert np.all(y[Tn // 2, 2:2 + M] == 0)
     assert np.all(y[:, :2] == -77) and np.all(y[:, 2 + M:] == -77)
+
+
+@pytest.mark.parametrize("Tn,bits,group", [(1, 4, 32), (2, 4, 64), (12, 4, 32), (12, 4, 128), (12, 3, 32), (12, 4, 16)])
+def test_moe_steps_of_other_rows_do_not_matter(T, Tn, bits, group):
+    """A row whose steps and zeros are no numbers leaves the others as they are (rows end inside a chunk)."""
+    say(f"moe steps b{bits} g{group} T={Tn}")
+    I, M = 5 * max(group, 32), 9
+    d = moe_inputs(Tn + group, Tn, 2, 2, 256, I, M, bits, group, "bf16")
+    args = d["X"], i32_dev(d["ids"]), f32_dev(d["w"]), d["gate_up"]
+    want = num(T.ttq_moe(*args, d["down"], bits, group))
+    down = dict(d["down"], scale_f16=d["down"]["scale_f16"].clone(), zero_f16=d["down"]["zero_f16"].clone())
+    down["scale_f16"][:, 4] = math.inf
+    down["zero_f16"][:, 4] = math.nan
+    y = num(T.ttq_moe(*args, down, bits, group))
+    rows = np.arange(M) != 4
+    np.testing.assert_array_equal(y[:, rows], want[:, rows])
+    assert np.all(np.isnan(y[:, 4]))
+
+
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("Tn", [1, 2, 12])
+def test_moe_nan_stays_in_its_token(T, Tn, xt):
+    say(f"moe nan {xt} T={Tn}")
+    d = moe_inputs(Tn, Tn, 2, 2, 256, 160, 40, 4, 32, xt)
+    args = i32_dev(d["ids"]), f32_dev(d["w"]), d["gate_up"], d["down"], 4, 32
+    want = num(T.ttq_moe(d["X"], *args))
+    X = d["X"].clone()
+    X[0, 77] = math.nan
+    y = num(T.ttq_moe(X, *args))
+    assert np.all(np.isnan(y[0]))
+    np.testing.assert_array_equal(y[1:], want[1:])
+
+
+@pytest.mark.parametrize("Tn", [1, 2])
+def test_moe_tiny_weights(T, Tn):
+    """Weights of 2^-110 scale the result (the range of h's integers: their scale is 2^-129 here, off by at
+    most 2^-150, a 2^-21st of it)."""
+    say(f"moe tiny weights T={Tn}")
+    d = moe_inputs(3, Tn, 2, 2, 256, 160, 40, 4, 32, "bf16")
+    d["w"] = (d["w"] * 2.0 ** -110).astype(np.float32)
+    y = T.ttq_moe(d["X"], i32_dev(d["ids"]), f32_dev(d["w"]), d["gate_up"], d["down"], 4, 32)
+    r, b = moe_ref(d, 4, "silu", "bf16", 32)
+    ref.check(num(y) * 2.0 ** 110, r * 2.0 ** 110, b * 2.0 ** 110, False)
 
 
 def test_moe_all_slots_empty(T):
