@@ -145,8 +145,8 @@ __device__ __forceinline__ float half_of(uint32_t d, bool hi) { return f16_to_f3
 constexpr int kMmBlock = 4;                       // chunks whose codes a wave has in flight
 constexpr int kMmStepLds = 3 * 1024;              // a wave's steps (fp16) and step (zero + 16) (fp32) of a block
 
-// LDS of x~: per slot and chunk NS * 256 bytes of terms and 32 of sums, 32 to
-// keep the rows apart modulo the banks.  Where the whole slice does not fit,
+// LDS of x~: per slot and chunk NS * 256 bytes of terms and 32 of sums, and 32
+// a row.  Where the whole slice does not fit,
 // half of it holds the chunks being multiplied and half the next ones (kMmMaxX
 // bytes, one workgroup of 16 waves on a compute unit); with kMmSmallX bytes
 // (two workgroups of eight), for tiles that are mostly expected to fit, all of
@@ -166,6 +166,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     constexpr int NG = kMmChunk / GROUP;          // groups per chunk
     constexpr int SPG = kSums ? GROUP / 32 : 1;   // subgroups per group
     constexpr int SG = GROUP < 32 ? 2 : 1;        // groups of a lane's 32 channels
+    constexpr bool kExchange = kSums && GROUP < 128;
     constexpr int D = kSums ? kMmBlock : 2;       // chunks of a block
     constexpr int NB = NG * D;                    // groups per block: 16, 8 or 4
     constexpr int NH = kSums ? (NB > 8 ? 8 : NB) : 4;   // steps a lane loads
@@ -211,15 +212,20 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     const int xrow = a.order[tl.first + min(lane & 15, rows - 1)] / a.div;   // operand row of slot lane % 16
     int kb = (cnt + D - 1) & ~(D - 1), half = 0;
     if (rows * (kb * kUnit + kMmRowPad) > a.xbytes) {
-        half = a.xbytes > kMmSmallX ? a.xbytes / 2 & ~15 : 0;
+        half = a.xbytes > kMmSmallX ? a.xbytes / 2 & ~255 : 0;
         kb = ((half ? half : a.xbytes) / rows - kMmRowPad) / kUnit & ~(D - 1);
     }
-    const int rowb = NS * kb * 256 + 16, srowb = kb * 32 + 16;
+    const int rowb = NS * kb * 256, srowb = kb * 32 + 16;
     unsigned char* const xb = smem + nw * kMmStepLds;
-    // Straight from memory into LDS: a wave's instruction takes a block of
-    // one term of one row, or a row's sums.
+    // Straight from memory into LDS: a wave's instruction takes four pairs of
+    // chunk and term (256 bytes each, terms next to each other) of one row, or
+    // a row's sums.  Row r has its 16-byte pieces at their place exclusive-or'ed
+    // with f(r), so that the 16 rows of a fragment lie in different banks, also
+    // where the hardware pairs rows of one quarter with others of the next (f:
+    // r, or with the quarters 64 bytes apart its bit pairs swapped).
+    auto swizzle = [](int r) __attribute__((always_inline)) { return kExchange ? r : (r & 3) << 2 | r >> 2; };
     auto stage = [&](int i0, unsigned char* to) __attribute__((always_inline)) {
-        const int per = NS * (kb / D) + 1;
+        const int units = NS * kb, per = (units + 3) / 4 + 1;
         for (int u = wave; u < rows * per; u += nw) {
             const int r = u / per, w = u - r * per;
             const int64_t xr = __builtin_amdgcn_readlane(xrow, r);
@@ -229,11 +235,11 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
                     if (lane < 2 * (kb - 32 * h))
                         dma_to_lds<16>(rs, to + rows * rowb + r * srowb + h * 1024, lane * 16, (cb + i0 + 32 * h) * 32);
             } else {
-                const int n = w / (kb / D), c4 = w - n * (kb / D);
                 const rsrc_t rx = make_rsrc(a.xt + xr * NS * a.kp, NS * a.kp * 2);
-                if (lane < 16 * D)
-                    dma_to_lds<16>(rx, to + r * rowb + (n * kb + c4 * D) * 256, lane * 16,
-                                   (int)(n * a.kp * 2) + (cb + i0 + c4 * D) * 256);
+                const int v = 4 * w + q, c = v / NS, n = v - c * NS;
+                if (v < units)
+                    dma_to_lds<16>(rx, to + r * rowb + w * 1024,
+                                   (int)(n * a.kp * 2) + c * 256 + ((r16 ^ swizzle(r)) * 16), (cb + i0) * 256);
             }
         }
     };
@@ -300,17 +306,18 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     // used.  In quarter q, MFMA j takes channels 32 j + 8 q ..+7 of the chunk
     // (the codes after the exchange of quarters), with one group per chunk or
     // weights 32 q + 8 j ..+7 (no exchange needed).
-    constexpr bool kExchange = kSums && GROUP < 128;
-    constexpr int kXq = kExchange ? 16 : 64, kXj = kExchange ? 64 : 16;
     const int rl = r16 < rows ? r16 : 0;
-    const int xo = rl * rowb + kXq * q, so = rows * rowb + rl * srowb + 8 * q;
+    uint32_t xo[4];                               // bytes from the buffer's start, of MFMA j's piece
+#pragma unroll
+    for (int j = 0; j < 4; ++j) xo[j] = rl * rowb + (((kExchange ? 4 * j + q : 4 * q + j) ^ swizzle(rl)) * 16);
+    const uint32_t so = rows * rowb + rl * srowb + 8 * q;
     unsigned char* const my = smem + wave * kMmStepLds;
     uint16_t* const st_l = (uint16_t*)my;         // [32][NB]
     float* const nb_l = (float*)(my + 1024);      // [32][NB]
     const int gq = NG == 4 ? q : NG == 2 ? q >> 1 : 0;   // group of subgroup q within a chunk
 
     f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-    auto multiply_weights = [&](int u, int i, const unsigned char* x0) __attribute__((always_inline)) {
+    auto multiply_weights = [&](int u, const uint32_t (&xa)[4]) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             u32x4 wt[2][2];                       // the weights' terms, slot order 0 2 4 6 1 3 5 7
@@ -332,7 +339,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
             }
 #pragma unroll
             for (int n = NS - 1; n >= 0; --n) {
-                const u32x4 x = *(const u32x4*)(x0 + xo + n * kb * 256 + i * 256 + kXj * j);
+                const u32x4 x = *(const u32x4*)(smem + xa[j] + (u * NS + n) * 256);
 #pragma unroll
                 for (int h = 1; h >= 0; --h)
 #pragma unroll
@@ -340,12 +347,13 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
             }
         }
     };
-    auto multiply = [&](int u, int i, const unsigned char* x0) __attribute__((always_inline)) {   // i: chunk of the stage
+    // xa, sa: the block's operand and sums in LDS.
+    auto multiply = [&](int u, const uint32_t (&xa)[4], uint32_t sa) __attribute__((always_inline)) {
         if constexpr (!kSums) {
-            multiply_weights(u, i, x0);
+            multiply_weights(u, xa);
             return;
         }
-        const float* sp = (const float*)(x0 + so + 32 * i);
+        const float* sp = (const float*)(smem + sa + 32 * u);
         const float si = sp[0] + sp[1];
         f32x4 p[2];
         u32x4 w4[2];
@@ -370,7 +378,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
             for (int rt = 0; rt < 2; ++rt) bb[rt] = codes_plus16(w4[rt][j]);
 #pragma unroll
             for (int n = NS - 1; n >= 0; --n) {
-                const u32x4 x = *(const u32x4*)(x0 + xo + n * kb * 256 + i * 256 + kXj * j);
+                const u32x4 x = *(const u32x4*)(smem + xa[j] + (u * NS + n) * 256);
 #pragma unroll
                 for (int rt = 0; rt < 2; ++rt) p[rt] = mfma_16x16x32(x, bb[rt], p[rt]);
             }
@@ -425,9 +433,14 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
             __builtin_amdgcn_wave_barrier();
             const int bn = b + D * nk;
             load_sz(bn);
+            uint32_t xa[4];
+            const uint32_t x00 = (uint32_t)(x0 - smem);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xa[j] = xo[j] + (x00 + (b - i0) * (NS * 256));
+            const uint32_t xsum = so + (x00 + (b - i0) * 32);
 #pragma unroll
             for (int u = 0; u < D; ++u) {
-                if (b + u < e) multiply(u, b + u - i0, x0);
+                if (b + u < e) multiply(u, xa, xsum);
                 load(u, bn + u);
                 __builtin_amdgcn_sched_barrier(0);
             }
