@@ -637,20 +637,20 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* 
     // before everything else, then C of the four tiles and B of the first
     // adapter.
     const int per = R / 4;                        // 16-byte pieces of a row of z
-    f32x4 zs[kZp];
-#pragma unroll
-    for (int n = 0; n < kZp; ++n) zs[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    constexpr int kZs = 4;                        // slices whose loads are in flight together
+    f32x4 zv[kZs][kZp];
     const int64_t have = min((int64_t)kTok, T - tb) * per;
-    for (int p = 0; p < slices; ++p)
+    auto load_z = [&](int p0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int n = 0; n < kZp; ++n) {
-            const int i = tid + n * kAyWaves * kWave;
-            if (i < have) {
-                const f32x4 v = *(const f32x4*)(Z + ((int64_t)p * T + tb) * R + 4 * i);
+        for (int p = 0; p < kZs; ++p) {
+            const rsrc_t rz = make_rsrc(Z + ((int64_t)(p0 + p) * T + tb) * R, p0 + p < slices ? have * 16 : 0);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) zs[n][e] += v[e];
-            }
+            for (int n = 0; n < kZp; ++n)         // behind the tokens or slices: zeros
+                zv[p][n] = __builtin_bit_cast(
+                    f32x4, __builtin_amdgcn_raw_buffer_load_b128(rz, (tid + n * kAyWaves * kWave) * 16, 0, 0));
         }
+    };
+    load_z(0);
     const bool oin = o0 + 16 * q < M;             // 16 consecutive rows, in eights
     u32x4 c[kArTiles][CW];
 #pragma unroll
@@ -677,6 +677,20 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* 
     if (const uint64_t any = __ballot(rk_l > 0); any != 0 && o0 < M) {
         const int f = __builtin_ctzll(any);
         load_rows(__builtin_amdgcn_readlane(id_l, f), __builtin_amdgcn_readlane(rk_l, f));
+    }
+    f32x4 zs[kZp];
+#pragma unroll
+    for (int n = 0; n < kZp; ++n) zs[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int p0 = 0;;) {
+#pragma unroll
+        for (int p = 0; p < kZs; ++p)
+#pragma unroll
+            for (int n = 0; n < kZp; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) zs[n][e] += zv[p][n][e];
+        p0 += kZs;
+        if (p0 >= slices) break;
+        load_z(p0);
     }
 #pragma unroll
     for (int n = 0; n < kZp; ++n) {               // times the adapters' scales
