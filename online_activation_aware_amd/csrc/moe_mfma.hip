@@ -36,13 +36,13 @@
 // sum over a token's slots adds.
 //
 // What bounds it.  128 tokens, two each of 8 experts, 4096 -> 2 x 14336 -> 4096,
-// groups of 64: 441 us, 1.8 TB/s of codes (each read once from memory) and 410
+// groups of 64: 443 us, 1.8 TB/s of codes (each read once from memory) and 410
 // TFLOP/s counting both terms: vector instructions half of the busy cycles
 // (expanding, once per tile of 16 slots), matrix instructions 30%, and waves
 // enough to overlap them only with 128 registers each (eight waves instead of
 // 16 on a compute unit: 515 us; tiles of 32 slots, which halve the expanding
 // but take two operands' registers: 471 us at best).  16 tokens, six each of 64
-// experts, 2048 -> 2 x 1056 -> 2048: 75 us, 1.5 slots per tile of 16, where a
+// experts, 2048 -> 2 x 1056 -> 2048: 78 us, 1.5 slots per tile of 16, where a
 // launch per product, its first loads and its end cost as much as the stream.
 #include "codes.hpp"
 #include "common.hpp"

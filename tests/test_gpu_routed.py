@@ -260,6 +260,9 @@ ADAPTERS = [  # T, K, M, n, rank, xt, at, yt, ids
     (70, 264, 65, 3, 20, "f32", "bf16", "f32", "mixed"),
     (20, 768, 768, 6, 16, "f32", "f32", "f32", "mixed"),
     (200, 128, 48, 2, 40, "f32", "f32", "bf16", "runs"),
+    (150, 4096, 64, 3, 64, "bf16", "bf16", "bf16", "runs"),
+    (140, 3584, 136, 3, 32, "bf16", "f32", "f32", "runs"),
+    (200, 2560, 72, 2, 56, "bf16", "bf16", "f32", "runs"),
     (3, 16384, 40, 2, 4, "bf16", "bf16", "f32", "mixed"),
 ]
 
