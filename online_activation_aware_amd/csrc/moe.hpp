@@ -42,7 +42,7 @@ __device__ __forceinline__ void moe_plan(const MoePlan& a) {
     }
     __syncthreads();
     if (tid < kWave) {
-        int p0 = 0, q0 = 0;                       // slots and tiles of the experts before this round's
+        int p0 = 0, q0 = 0;                       // slots and tiles of the experts before these 64
         for (int b = 0; b < a.E; b += kWave) {
             const int e = b + tid;
             const int c = e < a.E ? cnt[e] : 0, nt = (c + a.tile - 1) / a.tile;
