@@ -47,7 +47,7 @@ __device__ __forceinline__ uint32_t digit_of(uint32_t u, int d) { return ((u >> 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu; }
 // x as an integer of ND digits where the largest of its 32 is mx: by up * inv,
 // `up` so that kMax / mx stays finite.  Of no meaning (but defined) where mx is
-// no finite number: the scale then carries it.
+// no finite number: the scale is NaN then.
 template <int ND>
 struct ToDigits {
     float up, inv;
@@ -60,6 +60,13 @@ struct ToDigits {
         return (int)rintf(fminf(fmaxf(x * up * inv, -m), m));
     }
 };
+
+// The scale of 32 channels.  An infinite one would give signed infinities
+// (and the digits of an infinity have no sign), so it is NaN as well.
+template <int ND>
+__device__ __forceinline__ float digit_scale(float mx) {
+    return mx < __builtin_inff() ? mx / (float)Digits<ND>::kMax : __builtin_nanf("");
+}
 
 // x~ of a row: digits [ND][kp / 8] words, then per 32 channels the scale and
 // the sum of the integers, [2][kp / 32] floats.
@@ -112,7 +119,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_moe_dot_prep(MoePlan pl, MoePr
         for (int d = 0; d < ND; ++d) o[d * per + k8] = w[d];
         if ((k8 & 3) == 0) {
             float* f = (float*)(o + ND * per);
-            f[k8 / 4] = mx / (float)Digits<ND>::kMax;
+            f[k8 / 4] = digit_scale<ND>(mx);
             f[per / 4 + k8 / 4] = (float)sum;
         }
     }
@@ -316,7 +323,7 @@ __global__ __launch_bounds__(kMdMaxWaves * kWave, TT == 1 ? 3 : 2) void k_moe_do
             }
             if (lane == 0) {
                 float* s = (float*)(q + ND * per);
-                s[o0 / 32] = mx / (float)Digits<ND>::kMax;
+                s[o0 / 32] = digit_scale<ND>(mx);
                 s[per / 4 + o0 / 32] = (float)sum;
             }
         }
