@@ -75,8 +75,10 @@ __device__ __forceinline__ void moe_plan(const MoePlan& a) {
 
 __device__ __forceinline__ float moe_act(float x, int act) {
     if (act == TTQ_ACT_SILU) return x / (1.f + expf(-x));
+    // x (1 + tanh u) / 2 without a difference of near numbers (1 + tanh u has
+    // no correct digit left below x = -5).
     const float u = 0.7978845608028654f * (x + 0.044715f * x * x * x);
-    return x * (1.f - 1.f / (1.f + expf(2.f * u)));      // x (1 + tanh u) / 2
+    return x / (1.f + expf(-2.f * u));
 }
 
 // Workspace regions (bytes from its start).

@@ -1,7 +1,9 @@
 """Projections whose weights each token chooses at the ends of their ranges."""
 import numpy as np
 import pytest
+import torch
 
+import oracle
 from gpu_util import f32_dev, i32_dev, say
 from test_gpu_routed import enc, moe_inputs, num
 
@@ -64,3 +66,43 @@ def test_moe_overflowing_h(T, Tn, sign, xt, bits, group):
     y = num(T.ttq_moe(X, *args, dict(d["down"], s=s), bits, group))
     assert np.all(np.isnan(y[0]))
     np.testing.assert_array_equal(y[1:], want[1:])
+
+
+# ------------------------------------------------------------------ values next to zero
+
+@pytest.mark.parametrize("g", [2.0, 0.5, -1.0, -3.0, -4.0, -5.5])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("Tn", [1, 5])
+def test_moe_activation_keeps_its_precision(T, Tn, xt, act, g):
+    """Every gate is g, every up value 1 and the second product passes h on: y is the activation of g itself."""
+    say(f"moe act {act} {xt} g={g} T={Tn}")
+    K = I = M = 32
+    q = np.full((2 * I, K), 8)
+    q[:, 0] = 9                                    # (9 - 8) step times x[0] = 1
+    step = np.repeat([abs(g), 1.0], I)[:, None].astype(np.float16)
+    if g < 0:
+        q[:I, 0] = 7
+    qd = np.full((M, I), 8) + np.eye(I, dtype=int)
+
+    def state(q, step):
+        return dict(s=torch.ones(32, device="cuda"), codes=i32_dev(oracle.pack_codes(q, 4))[None],
+                    scale_f16=torch.from_numpy(step).cuda()[None], zero_f16=torch.full((1, len(q), 1), 8.0, dtype=torch.float16, device="cuda"))
+    x = np.zeros((Tn, K))
+    x[:, 0] = 1
+    y = num(T.ttq_moe(enc(x, xt)[0], torch.zeros((Tn, 1), dtype=torch.int32, device="cuda"), torch.ones((Tn, 1), device="cuda"),
+                      state(q, step), state(qd, np.ones((M, 1), np.float16)), 4, 32, act=act))
+    u = np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3)
+    want = g / (1 + np.exp(-g)) if act == "silu" else g / (1 + np.exp(-2 * u))
+    # g off by 8 roundings moves the value by its slope over it, at most 1 + |g| (silu), 1 + 2 u' |g| (gelu); the exponential's
+    # argument by 4 roundings of itself; 16 more roundings; h as digits (half a scale and 3 roundings) or terms
+    slope = 1 + abs(g) * (1 if act == "silu" else 2 * np.sqrt(2 / np.pi) * (1 + 3 * 0.044715 * g * g))
+    rel = 2.0 ** -24 * (8 * slope + 4 * abs(2 * u) + 16)
+    if Tn == 1:
+        rel += 2.0 ** -19 if xt == "bf16" else 2.0 ** -23
+    else:
+        # the second product is a difference, y = P - 24 S, of P = sum (16 + q) h = 31 * 24 h + 25 h = 769 h and S = 32 h.  P in four
+        # steps of at most P/4, P/2, 3 P/4 and P in size: 2.5 roundings of 2^-23 P; S in 31 additions of 2^-24: 15.5; the zero
+        # term and the running sum 3: 21 * 769 * 2^-23 < 2^-9
+        rel += 2.0 ** -9
+    assert np.all(np.abs(y - want) <= rel * abs(want)), (y[0, 0], want, rel)
