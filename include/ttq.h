@@ -361,9 +361,11 @@ typedef enum {
  *   dense.  ids[t][j] is the expert of the j-th largest logit of token t,
  *   equal logits in the order of their index; w[t][j] is its score (in fp32:
  *   softmax over all E logits, or sigmoid), divided by the sum of the topk
- *   scores if renormalize != 0.  A logit that is -inf or NaN is never chosen
- *   and has score 0: where fewer than topk others are left, the remaining
- *   slots get id -1 and weight 0 (all of them for a row without any).  +inf
+ *   scores if renormalize != 0.  Renormalized sigmoid scores keep their ratios
+ *   below fp32's range; if the row's largest logit is below -745 they are 0.
+ *   A logit that is -inf or NaN is never chosen and has score 0: where fewer
+ *   than topk others are left, the remaining slots get id -1 and weight 0
+ *   (all of them for a row without any).  +inf
  *   logits share the softmax equally.
  *   1 <= E <= 1024, 1 <= topk <= min(E, 32).  logits, ids and w aligned to
  *   their element size.  T == 0 is an empty call.  No workspace.

@@ -3,7 +3,9 @@
 //
 //   ids[t][j]: the experts of the j-th largest logit, ties to the lowest
 //   index; softmax: w = exp(l_j - m) / sum_e exp(l_e - m), m the row's
-//   maximum; sigmoid: w = 1 / (1 + exp(-l_j)); renormalised: w / sum_j w.
+//   maximum; sigmoid: w = 1 / (1 + exp(-l_j)); renormalised: w / sum_j w.  A
+//   sigmoid of l < 0 is exp(l) / (1 + exp(l)); to be renormalised, of exp(l - m),
+//   so that the ratios of scores below fp32's range are kept.
 //
 // One wave per token: lane l holds the logits l, l + 64, ... as 32-bit keys
 // that order like the floats (NaN and -inf as the key 0, which is never
@@ -106,10 +108,14 @@ __global__ __launch_bounds__(kRouteWaves * kWave) void k_moe_route(const void* _
         for (int i = 0; i < NV; ++i) part += key[i] ? exp_below(key_value(key[i]), m) : 0.f;
         sum = wave_sum(part);
     }
+    // Below -745 the scores are none in 64 bits either (rows masked by a lowest
+    // finite value): they stay 0.
+    const float base = renorm && m < 0.f && m >= -745.f ? m : 0.f;
     float w = 0.f;
     if (mine) {
         const float v = key_value(mine);
-        w = score == TTQ_SCORE_SOFTMAX ? exp_below(v, m) / sum : 1.f / (1.f + expf(-v));
+        if (score == TTQ_SCORE_SOFTMAX) w = exp_below(v, m) / sum;
+        else w = v < 0.f ? expf(v - base) / (1.f + expf(v)) : 1.f / (1.f + expf(-v));
     }
     if (renorm) {
         const float tot = wave_sum(w);

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import oracle
-from gpu_util import f32_dev, i32_dev, say
+from gpu_util import f32_dev, host, i32_dev, say
 from test_gpu_routed import enc, moe_inputs, num
 
 pytestmark = pytest.mark.gpu
@@ -106,3 +106,28 @@ def test_moe_activation_keeps_its_precision(T, Tn, xt, act, g):
         # term and the running sum 3: 21 * 769 * 2^-23 < 2^-9
         rel += 2.0 ** -9
     assert np.all(np.abs(y - want) <= rel * abs(want)), (y[0, 0], want, rel)
+
+
+@pytest.mark.parametrize("lt", ["f32", "bf16"])
+def test_route_small_sigmoid_scores(T, lt):
+    """Scores below fp32's range: renormalized, their ratios are weights as any others."""
+    say(f"route small sigmoids {lt}")
+    rows = [[-80, -81, -82.5, -90, -95], [-89, -90, -91, -89.5, -300], [-95, -95, -96, -97, -95], [-200, -201, -199, -200, -205],
+            [-744, -743, -744, -742, -741], [0.5, -100, -200, -1, 3], [-3e38, -1e38, -2e38, -3e38, -1e38]]
+    L, x = enc(rows, lt)
+    for topk in (1, 3):
+        ids, w = T.ttq_moe_route(L, topk, score="sigmoid", renormalize=True)
+        order = np.argsort(-x, axis=1, kind="stable")[:, :topk]
+        np.testing.assert_array_equal(host(ids), order)
+        v = np.take_along_axis(x, order, 1)
+        r = np.exp(np.minimum(v, 0) - np.minimum(v[:, :1], 0)) / (1 + np.exp(-np.abs(v)))
+        r[v[:, 0] < -745] = 0                      # no score left, in 64 bits either
+        r /= np.maximum(r.sum(1, keepdims=True), 1e-300)
+        # the exponential of a difference up to 100, in fp32, and 8 roundings, of the score and of the sum
+        assert np.all(np.abs(num(w) - r) <= 2.0 ** -24 * 2 * (100 + 8 + topk) * r + 1e-37), (num(w), r)
+    ids, w = T.ttq_moe_route(L, 5, score="sigmoid")
+    v = np.take_along_axis(x, host(ids), 1)
+    with np.errstate(over="ignore"):
+        r = 1 / (1 + np.exp(-v))
+    # 2^-149 is the least fp32 number: half a step of it besides the relative error
+    assert np.all(np.abs(num(w) - r) <= (np.abs(v).clip(max=104) + 10) * 2.0 ** -23 * r + 2.0 ** -149)
