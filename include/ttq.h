@@ -443,8 +443,9 @@ typedef struct ttq_adapters {
  *   Y[t] = C[t] + scale_a B_a (A_a X[t]),  a = ids[t]; without an adapter
  *   Y[t] = C[t].  In fp32, rounded once to Y.
  *   X: [T][K] (xt).  C: [T][M] of Y's dtype, stride ldc, or NULL for zeros;
- *   it may be Y itself (ldc == ldy), else it must not overlap Y.  Any order
- *   of ids is accepted; runs of tokens of one adapter (prompts) cost least.
+ *   it may be Y itself (ldc == ldy), else it must not overlap Y; Y may lie on
+ *   X.  Any order of ids is accepted; runs of tokens of one adapter (prompts)
+ *   cost least.
  *   K a multiple of 8, at most 2^18; ldx above 2^24 returns
  *   TTQ_ERR_UNSUPPORTED.  T == 0 or M == 0 is an empty call.
  *   ws: ttq_adapters_workspace_bytes(T, K, M, rank) bytes, 256-byte aligned.

@@ -880,7 +880,12 @@ static hipError_t launch_one(const void* X, bool xf32, int64_t K, const AdapterT
 hipError_t launch_adapters(const void* X, bool xf32, int64_t T, int64_t K, int64_t ldx, const AdapterTable& ad,
                            const ProjectionIn& ci, int64_t M, void* Y, bool yf32, int64_t ldy, float* Z,
                            hipStream_t st) {
-    if (T == 1 && ci.parts == 1 && (M + kA1Rows - 1) / kA1Rows * ad.rank * K * (ad.f32 ? 4 : 2) <= kA1Bytes) {
+    // (Not where Y lies on X: its first workgroups would write over what the
+    // last still read.)
+    const char *x0 = (const char*)X, *y0 = (const char*)Y;
+    const bool apart = x0 + K * (xf32 ? 4 : 2) <= y0 || y0 + M * (yf32 ? 4 : 2) <= x0;
+    if (T == 1 && ci.parts == 1 && apart &&
+        (M + kA1Rows - 1) / kA1Rows * ad.rank * K * (ad.f32 ? 4 : 2) <= kA1Bytes) {
         if (ci.f32) return yf32 ? launch_one<true, true>(X, xf32, K, ad, ci, M, Y, st)
                                 : launch_one<true, false>(X, xf32, K, ad, ci, M, Y, st);
         return yf32 ? launch_one<false, true>(X, xf32, K, ad, ci, M, Y, st)

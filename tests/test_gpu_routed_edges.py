@@ -131,3 +131,29 @@ def test_route_small_sigmoid_scores(T, lt):
         r = 1 / (1 + np.exp(-v))
     # 2^-149 is the least fp32 number: half a step of it besides the relative error
     assert np.all(np.abs(num(w) - r) <= (np.abs(v).clip(max=104) + 10) * 2.0 ** -23 * r + 2.0 ** -149)
+
+
+# ------------------------------------------------------------------ shared memory
+
+@pytest.mark.parametrize("Tn", [1, 5, 130])
+@pytest.mark.parametrize("add", [False, True])
+def test_adapters_written_over_x(T, Tn, add):
+    """Y may lie on X, alone or as C too: a residual connection in place."""
+    say(f"adapters over X T={Tn} add={add}")
+    rng = np.random.default_rng(Tn)
+    K, rank, n = 4096, 16, 3
+    A, B = enc(rng.standard_normal((n, rank, K)) / 64, "bf16")[0], enc(rng.standard_normal((n, K, rank)), "bf16")[0]
+    ids = i32_dev(rng.integers(0, n, Tn))
+    for _ in range(4):
+        X = enc(rng.standard_normal((Tn, K)), "bf16")[0]
+        want = T.ttq_adapters_add(X, A, B, ids, C=X if add else None, y_dtype=torch.bfloat16)
+        Z = X.clone()
+        T.ttq_adapters_add(Z, A, B, ids, C=Z if add else None, Y=Z)
+        # one token in place takes two launches, whose sums have another order: each within 64 + 16 fp32 roundings, then bf16
+        got, r = num(Z), num(want)
+        x = num(X)
+        mag = np.zeros_like(r)
+        for t in range(Tn):
+            a = int(ids[t])
+            mag[t] = np.abs(num(B)[a]) @ (np.abs(num(A)[a]) @ np.abs(x[t]))
+        assert np.all(np.abs(got - r) <= 2.0 ** -7 * np.abs(r) + 2 * (K + 2 * rank) * 2.0 ** -23 * mag)
