@@ -457,17 +457,28 @@ def _on_tensor_device(fn):
     """Run a call on its first tensor's device and on ``stream`` (default:
     that device's current stream); what the call allocates belongs to that
     stream."""
+    names = list(inspect.signature(fn).parameters)
+    first, at = names[0], names.index("stream")
+
     @functools.wraps(fn)
-    def call(X, *args, stream=None, **kwargs):
+    def call(*args, stream=None, **kwargs):
+        if len(args) == at + 1:           # the stream in its place
+            args, stream = args[:at], args[at]
+        if args:
+            X = args[0]
+        elif first in kwargs:
+            X = kwargs[first]
+        else:
+            raise TypeError(f"{fn.__name__}() missing its first argument, {first!r}")
         if not isinstance(X, torch.Tensor) or not X.is_cuda:
-            raise TypeError("the first argument must be a device tensor")
+            raise TypeError(f"{first} must be a device tensor")
         index = X.get_device()
         if stream is None and index == torch.cuda.current_device():
-            return fn(X, *args, stream=_current_stream(index), **kwargs)
+            return fn(*args, stream=_current_stream(index), **kwargs)
         with torch.cuda.device(index):
             ts = _torch_stream(stream)
             with torch.cuda.stream(ts):
-                return fn(X, *args, stream=ts.cuda_stream, **kwargs)
+                return fn(*args, stream=ts.cuda_stream, **kwargs)
     return call
 
 

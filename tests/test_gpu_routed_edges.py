@@ -157,3 +157,20 @@ def test_adapters_written_over_x(T, Tn, add):
             a = int(ids[t])
             mag[t] = np.abs(num(B)[a]) @ (np.abs(num(A)[a]) @ np.abs(x[t]))
         assert np.all(np.abs(got - r) <= 2.0 ** -7 * np.abs(r) + 2 * (K + 2 * rank) * 2.0 ** -23 * mag)
+
+
+# ------------------------------------------------------------------ calling
+
+def test_calls_by_name_and_with_a_stream_in_place(T):
+    say("calls by name")
+    d = moe_inputs(4, 3, 2, 2, 64, 64, 32, 4, 32, "bf16")
+    L = torch.randn((3, 4), device="cuda")
+    ids, w = T.ttq_moe_route(L, 2)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    for i2, w2 in (T.ttq_moe_route(logits=L, topk=2), T.ttq_moe_route(L, 2, "softmax", False, None, None, st),
+                   T.ttq_moe_route(L, 2, stream=st.cuda_stream)):
+        torch.cuda.synchronize()
+        assert torch.equal(ids, i2) and torch.equal(w, w2)
+    args = dict(X=d["X"], ids=i32_dev(d["ids"]), w=f32_dev(d["w"]), gate_up=d["gate_up"], down=d["down"], bits=4, group=32)
+    assert torch.equal(T.ttq_moe(**args), T.ttq_moe(*args.values()))
