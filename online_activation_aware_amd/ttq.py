@@ -544,13 +544,14 @@ def ttq_moe_route(logits: torch.Tensor, topk: int, score: str = "softmax", renor
     ld = _row_stride(logits, "logits")
     T, E = logits.shape
     dev = logits.get_device()
+    k = topk if 0 <= topk <= E else 0     # others are refused below, with nothing allocated for them
     if ids is None:
-        ids = logits.new_empty((T, max(topk, 0)), dtype=torch.int32)
+        ids = logits.new_empty((T, k), dtype=torch.int32)
         ip = ids.data_ptr()
     else:
         ip = _dense(ids, "ids", torch.int32, (T, topk), dev)
     if w is None:
-        w = logits.new_empty((T, max(topk, 0)), dtype=torch.float32)
+        w = logits.new_empty((T, k), dtype=torch.float32)
         wp = w.data_ptr()
     else:
         wp = _dense(w, "w", torch.float32, (T, topk), dev)

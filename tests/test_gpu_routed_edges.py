@@ -174,3 +174,14 @@ def test_calls_by_name_and_with_a_stream_in_place(T):
         assert torch.equal(ids, i2) and torch.equal(w, w2)
     args = dict(X=d["X"], ids=i32_dev(d["ids"]), w=f32_dev(d["w"]), gate_up=d["gate_up"], down=d["down"], bits=4, group=32)
     assert torch.equal(T.ttq_moe(**args), T.ttq_moe(*args.values()))
+
+
+def test_refused_sizes_allocate_nothing(T):
+    say("refused sizes")
+    L = torch.zeros((4, 8), device="cuda")
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    for topk in (0, 9, -1, 1 << 20):
+        with pytest.raises(T.TTQError):
+            T.ttq_moe_route(L, topk)
+    assert torch.cuda.max_memory_allocated() - before < 1 << 16
