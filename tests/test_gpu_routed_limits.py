@@ -1,0 +1,130 @@
+"""Projections whose weights each token chooses against fp64, within the
+variance of their rounding errors (routed_limits): outputs that miss a slot, a
+slice of channels or a term of an operand are rejected, see
+test_routed_limits.py."""
+import numpy as np
+import pytest
+import torch
+
+import routed_limits as lim
+from gpu_util import f32_dev, i32_dev, say, to_dev
+from online_activation_aware_amd import synth
+from test_gpu_routed import SHARED, num
+from test_routed_limits import LAYERS
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def T():
+    from online_activation_aware_amd import ttq
+    ttq.lib()
+    return ttq
+
+
+def dev(a, dt):
+    return to_dev(synth.encode(np.asarray(a, np.float64), dt), dt)
+
+
+def state_dev(q):
+    return dict(s=f32_dev(q["s"]), codes=i32_dev(q["codes"]), scale_f16=torch.from_numpy(q["step"]).cuda(),
+                zero_f16=torch.from_numpy(q["zero"]).cuda())
+
+
+def moe_call(T, d, case, a=0, b=None):
+    bits, group, xt, act = case[6:10]
+    b = len(d["ids"]) if b is None else b
+    gu, dn = d.setdefault("dev", [state_dev(d["gate_up"]), state_dev(d["down"])])
+    return num(T.ttq_moe(dev(d["x"][a:b], xt), i32_dev(d["ids"][a:b]), f32_dev(d["w"][a:b]), gu, dn, bits, group, act=act))
+
+
+# ------------------------------------------------------------------ experts
+
+@pytest.mark.parametrize("case", LAYERS, ids=lambda c: "-".join(map(str, c)))
+def test_expert_layers(T, case):
+    say(f"layer {case}")
+    d = lim.moe_case(case)
+    y, var = lim.moe_model(d, case)
+    got = moe_call(T, d, case)
+    lim.check(got, y, var)
+    np.testing.assert_array_equal(moe_call(T, d, case), got)
+
+
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("bits,group", [(4, 32), (3, 16)])
+def test_a_token_in_calls_of_other_sizes(T, bits, group, xt):
+    """Calls that hold x / s and h alike (one and two tokens; three and more) give a token the same outputs up to
+    the order of fp32 sums, others up to their operands' errors."""
+    say(f"layer in parts b{bits} g{group} {xt}")
+    case = (24, 4, 2, 384, 2304, 96, bits, group, xt, "silu", "any")
+    d = lim.moe_case(case)
+    whole = moe_call(T, d, case)
+    y, sums = lim.moe_model(d, case, own=False)
+    full = lim.moe_model(d, case)[1]
+
+    def part(a, b):
+        rows = dict(d, **{k: d[k][a:b] for k in ("x", "ids", "w")})
+        own, v = (lim.moe_model(rows, (b - a, *case[1:]), own=o)[1] for o in (True, False))
+        return moe_call(T, d, case, a, b), own, v
+    digits = bits == 4 and group >= 32
+    for a, b in ((0, 3), (4, 12), (7, 24)):
+        got, _, v = part(a, b)
+        lim.check(got, whole[a:b], v + sums[a:b])
+    for a in (0, 9, 22):
+        one, own, v = part(a, a + 1)
+        two, _, v2 = part(a, a + 2)
+        lim.check(one, two[:1], v + v2[:1])
+        lim.check(one, whole[a:a + 1], own + full[a:a + 1] if digits else v + sums[a:a + 1])
+
+
+# ------------------------------------------------------------------ adapters
+
+@pytest.mark.parametrize("yt", ["f32", "bf16"])
+@pytest.mark.parametrize("case", lim.MIXED, ids=lambda c: "-".join(map(str, c)))
+def test_adapters_in_any_order(T, case, yt):
+    say(f"adapters mixed {case} {yt}")
+    Tn, K, M, n, rank, xt, at = case
+    d = lim.adapter_case(sum(case[:5]), *case)
+    none = d["ids"] < 0
+    assert none.any() and len(set(d["ids"][:32])) > 5
+    y, var = lim.adapters(d["x"], d["a"], d["b"], d["ids"], d["ranks"], d["scale"], "f32" in (xt, at))
+    A, B = dev(d["a"], at), dev(d["b"], at)
+    for i, r in enumerate(d["ranks"]):             # what lies behind a rank is not used
+        A[i, r:] = float("nan")
+        B[i, :, r:] = float("nan")
+    X, args = dev(d["x"], xt), (A, B, i32_dev(d["ids"]))
+    kw = dict(ranks=i32_dev(d["ranks"]), scale=f32_dev(d["scale"]))
+    got = num(T.ttq_adapters_add(X, *args, **kw))
+    lim.check(got, y, var + (lim.U * y) ** 2)
+    assert np.all(got[none] == 0)
+    C = dev(d["rng"].standard_normal((Tn, M)), yt)
+    c = num(C)
+    out = T.ttq_adapters_add(X, *args, C=C, **kw)
+    half = 2.0 ** -8 if yt == "bf16" else lim.U
+    lim.check(num(out), c + y, var + (half * (c + y)) ** 2)
+    np.testing.assert_array_equal(num(out)[none], c[none])
+    assert torch.equal(T.ttq_adapters_add(X, *args, C=C, Y=C, **kw), out)
+
+
+# ------------------------------------------------------------------ a shared projection with adapters
+
+@pytest.mark.parametrize("case", SHARED + [(140, 512, 136, 4, 32, 60, 16, "bf16", "f32", "mixed"),
+                                           (190, 1024, 65, 3, 32, 30, 24, "bf16", "f32", "mixed")],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_shared_projections(T, case):
+    """Against fp64, and against the two calls it stands for up to the order of fp32 sums."""
+    say(f"shared {case}")
+    Tn, K, M, bits, group, n, rank, xt, _, _ = case
+    d, nums, s = lim.shared_case(case)
+    y, var = lim.shared(d["x"], nums, s, xt)
+    a, va = lim.adapters(d["x"], d["a"], d["b"], d["ids"], d["ranks"], d["scale"], xt == "f32")
+    q = state_dev(d["state"])
+    X, state = dev(d["x"], xt), (q["s"], q["codes"], q["scale_f16"], q["zero_f16"], M, bits, group)
+    ad = dict(A=dev(d["a"], xt), B=dev(d["b"], xt), ids=i32_dev(d["ids"]), ranks=i32_dev(d["ranks"]), scale=f32_dev(d["scale"]))
+    got = num(T.ttq_qgemm_adapters(X, *state, **ad))
+    lim.check(got, y + a, var + va)
+    ws = T.workspace(Tn, K, M, bits, group)
+    two = num(T.ttq_adapters_add(X, C=T.ttq_qgemm(X, *state, ws=ws), **ad))
+    qn, dl, z = nums
+    R = d["x"] ** 2 @ (((qn - z) * dl / s) ** 2).T
+    lim.check(got, two, lim.U ** 2 * (16 * R + 4 * y ** 2 + 4 * a ** 2))
