@@ -622,7 +622,10 @@ static hipError_t launch_ns(const ttq_moe_args* a, const MoeLayout& L, char* ws,
     d.codes = (const uint32_t*)a->down.codes; d.scale = a->down.scale_f16; d.zero = a->down.zero_f16;
     d.p = (float*)(ws + L.p);
     const int chunks = (int)(ip / kMmChunk), sl = moe_slices(n, a->E, a->I, a->M);
-    d.per_slice = (chunks + sl - 1) / sl;
+    // An even number of chunks: a slice's first step lies at a word's start also
+    // where a chunk is one group (a load at half a word would lose the steps of
+    // the last row's end, cut off there by the buffer's word-wise bound).
+    d.per_slice = ((chunks + sl - 1) / sl + 1) & ~1;
     const int nsl = (chunks + d.per_slice - 1) / d.per_slice;
     const int64_t dw = (a->M + kMmRows - 1) / kMmRows;
     const MmShape v = mm_shape(dw, nt * nsl, d.per_slice, n, a->E, NS);

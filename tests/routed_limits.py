@@ -103,6 +103,7 @@ EXPERTS = [
     # all tokens on one expert of many: the rows of x~ do not fit and are brought in again
     (16, 8, 1, 2080, 96, 40, 4, 32, "bf16", "silu", "one"),
     (16, 8, 1, 2080, 96, 40, 4, 32, "f32", "gelu", "one"),
+    (30, 8, 1, 1152, 2304, 33, 4, 128, "bf16", "silu", "one"),
     (16, 8, 1, 2048, 64, 40, 3, 64, "f32", "silu", "one"),
     # more than 64 experts (the plan's scan in blocks of 64), up to 1024, and up to 32 a token
     (12, 130, 4, 64, 64, 40, 4, 32, "bf16", "silu", "any"),

@@ -51,7 +51,7 @@ def test_expert_layers(T, case):
 
 
 @pytest.mark.parametrize("xt", ["bf16", "f32"])
-@pytest.mark.parametrize("bits,group", [(4, 32), (3, 16)])
+@pytest.mark.parametrize("bits,group", [(4, 32), (4, 128), (3, 16)])
 def test_a_token_in_calls_of_other_sizes(T, bits, group, xt):
     """Calls that hold x / s and h alike (one and two tokens; three and more) give a token the same outputs up to
     the order of fp32 sums, others up to their operands' errors."""
