@@ -397,8 +397,9 @@ typedef struct ttq_expert_state {
  *   All sums are kept in fp32; Y is rounded once.  x / s and h enter the
  *   products with 16 bits for bf16 X and 24 for fp32 X (one or two tokens on
  *   4-bit codes in groups of 32 or more: to 2^-19 or 2^-23 of the largest of
- *   their 32 channels), codes, steps and zeros exactly.  Results of a token do
- *   not depend on the other tokens of the call beyond fp32 rounding, and are
+ *   their 32 channels), codes, steps and zeros exactly.  A token's results
+ *   depend on the other tokens of the call only through that choice (one or
+ *   two tokens, or more) and the order of the fp32 sums.  They are
  *   reproducible run to run; an infinite or NaN x / s or h makes its token's
  *   outputs NaN and no other's.
  *   K and I multiples of 32 and of group, at most 2^18; E <= 1024;
