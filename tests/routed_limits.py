@@ -5,7 +5,8 @@ Each rounding is taken as uniform within its half step h and independent of
 the others: variance h^2 / 3.  Half steps, relative to the value: bf16 2^-8,
 fp32 2^-24; an addition inside a matrix instruction is counted with 2^-23, as
 if it truncated.  Errors are carried through the products and the activation
-to first order.  The model counts, for y_o = sum_j w_oj x~_j, w = (q - z) d:
+to first order (a slot's errors as independent of the token's other slots: an
+expert named twice repeats them, which is not modelled).  The model counts, for y_o = sum_j w_oj x~_j, w = (q - z) d:
 
 - the operand: NS bf16 terms, half step 2^-(8 NS) |x~|; or digits, a scale
   per 32 channels of their largest over 489335 (five) or 7829367 (six digits),

@@ -128,3 +128,36 @@ def test_shared_projections(T, case):
     qn, dl, z = nums
     R = d["x"] ** 2 @ (((qn - z) * dl / s) ** 2).T
     lim.check(got, two, lim.U ** 2 * (16 * R + 4 * y ** 2 + 4 * a ** 2))
+
+
+# ------------------------------------------------------------------ memory around a call
+
+@pytest.mark.parametrize("case", [(1, 3, 2, 544, 1056, 65, 4, 32, "bf16", "silu", "any"), (2, 4, 2, 640, 384, 129, 4, 128, "f32", "gelu", "any"),
+                                  (5, 3, 2, 96, 160, 33, 4, 32, "bf16", "gelu", "any"), (20, 2, 2, 640, 2432, 33, 4, 128, "bf16", "silu", "any"),
+                                  (18, 5, 2, 512, 640, 70, 4, 64, "f32", "silu", "any"), (9, 3, 2, 96, 96, 34, 3, 16, "bf16", "silu", "any")],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_expert_layer_steps_at_half_words_and_a_used_workspace(T, case):
+    """Steps and zeros whose arrays start within a word (each, or one of them), a workspace full of NaN, and nothing
+    written behind it or beside Y."""
+    say(f"layer memory {case}")
+    Tn, E, topk, K, I, M, bits, group, xt, act, _ = case
+    d = lim.moe_case(case)
+    rng = np.random.default_rng(1)
+    d["ids"] = np.argsort(rng.random((Tn, E)), axis=1)[:, :topk].astype(np.int32)
+    y, var = lim.moe_model(d, case)
+    need = T.ttq_moe_workspace_bytes(Tn, topk, K, I, M, E, bits, group)
+    for by in ((1, 1), (1, 0), (0, 1)):
+        def place(q):
+            st = state_dev(q)
+            for k, n in zip(("scale_f16", "zero_f16"), by):
+                buf = torch.full((st[k].numel() + 2,), float("nan"), dtype=torch.float16, device="cuda")
+                st[k] = buf[n:n + st[k].numel()].view(st[k].shape).copy_(st[k])
+            return st
+        ws = torch.full((need + 512,), 255, dtype=torch.uint8, device="cuda")
+        Y = torch.full((Tn + 2, M + 3), -7.0, device="cuda")
+        T.ttq_moe(dev(d["x"], xt), i32_dev(d["ids"]), f32_dev(d["w"]), place(d["gate_up"]), place(d["down"]), bits, group, act=act,
+                  Y=Y[1:-1, 1:1 + M], ws=ws[:need])
+        got = num(Y)
+        lim.check(got[1:-1, 1:1 + M], y, var)
+        assert np.all(got[[0, -1]] == -7) and np.all(got[:, 0] == -7) and np.all(got[:, 1 + M:] == -7)
+        assert torch.all(ws[need:] == 255)
