@@ -877,6 +877,7 @@ static hipError_t launch_one(const void* X, bool xf32, int64_t K, const AdapterT
 #undef TTQ_A1
 }
 
+// C has Y's dtype or fp32.
 hipError_t launch_adapters(const void* X, bool xf32, int64_t T, int64_t K, int64_t ldx, const AdapterTable& ad,
                            const ProjectionIn& ci, int64_t M, void* Y, bool yf32, int64_t ldy, float* Z,
                            hipStream_t st) {
@@ -886,10 +887,9 @@ hipError_t launch_adapters(const void* X, bool xf32, int64_t T, int64_t K, int64
     const bool apart = x0 + K * (xf32 ? 4 : 2) <= y0 || y0 + M * (yf32 ? 4 : 2) <= x0;
     if (T == 1 && ci.parts == 1 && apart &&
         (M + kA1Rows - 1) / kA1Rows * ad.rank * K * (ad.f32 ? 4 : 2) <= kA1Bytes) {
-        if (ci.f32) return yf32 ? launch_one<true, true>(X, xf32, K, ad, ci, M, Y, st)
-                                : launch_one<true, false>(X, xf32, K, ad, ci, M, Y, st);
-        return yf32 ? launch_one<false, true>(X, xf32, K, ad, ci, M, Y, st)
-                    : launch_one<false, false>(X, xf32, K, ad, ci, M, Y, st);
+        if (yf32) return launch_one<true, true>(X, xf32, K, ad, ci, M, Y, st);
+        return ci.f32 ? launch_one<true, false>(X, xf32, K, ad, ci, M, Y, st)
+                      : launch_one<false, false>(X, xf32, K, ad, ci, M, Y, st);
     }
     hipError_t e;
     if (xf32) e = ad.f32 ? launch_z<true, true>(X, T, K, ldx, ad, Z, st) : launch_z<true, false>(X, T, K, ldx, ad, Z, st);
@@ -898,11 +898,8 @@ hipError_t launch_adapters(const void* X, bool xf32, int64_t T, int64_t K, int64
 #define TTQ_AY(CF, YF)                                                                 \
     return ad.f32 ? launch_y<CF, true, YF>(Z, T, K, ad, ci, M, Y, ldy, st)             \
                   : launch_y<CF, false, YF>(Z, T, K, ad, ci, M, Y, ldy, st)
-    if (ci.f32) {
-        if (yf32) TTQ_AY(true, true);
-        TTQ_AY(true, false);
-    }
-    if (yf32) TTQ_AY(false, true);
+    if (yf32) TTQ_AY(true, true);
+    if (ci.f32) TTQ_AY(true, false);
     TTQ_AY(false, false);
 #undef TTQ_AY
 }

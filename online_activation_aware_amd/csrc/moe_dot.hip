@@ -35,6 +35,8 @@ constexpr int kMdRing = 8;                        // code loads in flight
 
 int64_t moe_dot_pad(int64_t K) { return (K + kMdPiece - 1) / kMdPiece * kMdPiece; }
 
+constexpr int md_digits(bool xf32) { return xf32 ? 6 : 5; }
+
 template <int ND>
 struct Digits {
     static constexpr int kMax = 7 * ((1 << (4 * ND)) - 1) / 15;   // the largest number of ND digits <= 7
@@ -76,8 +78,9 @@ __device__ __forceinline__ int64_t digit_row_words(int64_t kp) { return ND * (kp
 // ------------------------------------------------------------------ operand
 
 // Block 0 plans; the others lay out X / s per slot: a thread has 8 channels.
-template <int ND, bool XF32>
+template <bool XF32>
 __global__ __launch_bounds__(kPlanThreads) void k_moe_dot_prep(MoePlan pl, MoePrep a, uint32_t* __restrict__ out) {
+    constexpr int ND = md_digits(XF32);
     if (blockIdx.x == 0) {
         moe_plan(pl);
         return;
@@ -375,18 +378,16 @@ static hipError_t launch_dot(const MoeDot& p, int group, dim3 grid, int waves, h
     return hipErrorInvalidValue;
 }
 
-template <int ND, int TT>
-static hipError_t launch_nd(const ttq_moe_args* a, const MoeLayout& L, char* ws, hipStream_t st) {
+template <bool XF32, int TT>
+static hipError_t launch_layer(const ttq_moe_args* a, const MoeLayout& L, char* ws, hipStream_t st) {
+    constexpr int ND = md_digits(XF32);
     const int64_t n = a->T * a->topk, kp = moe_dot_pad(a->K), ip = moe_dot_pad(a->I);
     const int64_t nt = moe_tiles(n, a->E, TT);
     MoePlan pl{a->ids, (int)n, (int)a->E, TT, (int)nt, (int32_t*)(ws + L.order), (MoeTile*)(ws + L.tiles)};
     MoePrep pr = moe_prep_of(a, kp);
     uint32_t* xq = (uint32_t*)(ws + L.xt);
     const dim3 pg((unsigned)(1 + (pr.rows * (kp / 8) + kPlanThreads - 1) / kPlanThreads));
-    if (hipError_t e = a->xt == TTQ_F32 ? launch_kernel(k_moe_dot_prep<ND, true>, pg, dim3(kPlanThreads), 0, st, nullptr,
-                                                        nullptr, pl, pr, xq)
-                                        : launch_kernel(k_moe_dot_prep<ND, false>, pg, dim3(kPlanThreads), 0, st, nullptr,
-                                                        nullptr, pl, pr, xq))
+    if (hipError_t e = launch_kernel(k_moe_dot_prep<XF32>, pg, dim3(kPlanThreads), 0, st, nullptr, nullptr, pl, pr, xq))
         return e;
     MoeDot p{};
     p.tiles = pl.tiles; p.order = pl.order; p.slots = n;
@@ -420,8 +421,9 @@ static hipError_t launch_nd(const ttq_moe_args* a, const MoeLayout& L, char* ws,
 }
 
 hipError_t launch_moe_dot(const ttq_moe_args* a, const MoeLayout& L, char* ws, hipStream_t st) {
-    if (a->T == 1) return a->xt == TTQ_F32 ? launch_nd<6, 1>(a, L, ws, st) : launch_nd<5, 1>(a, L, ws, st);
-    return a->xt == TTQ_F32 ? launch_nd<6, 2>(a, L, ws, st) : launch_nd<5, 2>(a, L, ws, st);
+    if (a->T == 1)
+        return a->xt == TTQ_F32 ? launch_layer<true, 1>(a, L, ws, st) : launch_layer<false, 1>(a, L, ws, st);
+    return a->xt == TTQ_F32 ? launch_layer<true, 2>(a, L, ws, st) : launch_layer<false, 2>(a, L, ws, st);
 }
 
 }  // namespace ttq

@@ -60,6 +60,8 @@ int64_t moe_pad(int64_t K) { return (K + kMmChunk - 1) / kMmChunk * kMmChunk; }
 
 // ------------------------------------------------------------------ operand layout
 
+constexpr int mm_terms(bool xf32) { return xf32 ? 3 : 2; }
+
 __device__ __forceinline__ u32x4 pack_terms(const float (&x)[8]) {
     // slot order 0 2 4 6 1 3 5 7
     return u32x4{pack_bf16x2(x[0], x[2]), pack_bf16x2(x[4], x[6]), pack_bf16x2(x[1], x[3]), pack_bf16x2(x[5], x[7])};
@@ -87,8 +89,9 @@ __device__ __forceinline__ float store_terms(float (&x)[8], uint16_t* d, int64_t
 // Block 0 plans (moe.hpp); the others lay out rows of X / s: row r is token
 // r (one s for all experts) or slot r (s of the slot's expert; nothing for a
 // slot without one).
-template <int NS, bool XF32>
+template <bool XF32>
 __global__ __launch_bounds__(kPlanThreads) void k_moe_prep(MoePlan pl, MoePrep a) {
+    constexpr int NS = mm_terms(XF32);
     if (blockIdx.x == 0) {
         moe_plan(pl);
         return;
@@ -591,17 +594,16 @@ static hipError_t launch_mm(const MoeMm& p, int bits, int group, dim3 grid, int 
     return hipErrorInvalidValue;
 }
 
-template <int NS>
-static hipError_t launch_ns(const ttq_moe_args* a, const MoeLayout& L, char* ws, hipStream_t st) {
+template <bool XF32>
+static hipError_t launch_layer(const ttq_moe_args* a, const MoeLayout& L, char* ws, hipStream_t st) {
+    constexpr int NS = mm_terms(XF32);
     const int64_t n = a->T * a->topk, kp = moe_pad(a->K), ip = moe_pad(a->I);
     const int64_t nt = moe_tiles(n, a->E, kMmTile);
     MoePlan pl{a->ids, (int)n, (int)a->E, kMmTile, (int)nt, (int32_t*)(ws + L.order), (MoeTile*)(ws + L.tiles)};
     MoePrep pr = moe_prep_of(a, kp);
     pr.xt = (uint16_t*)(ws + L.xt); pr.xs = (float*)(ws + L.xs);
     const dim3 pg((unsigned)(1 + (pr.rows * (kp / 8) + kPlanThreads - 1) / kPlanThreads));
-    if (hipError_t e = a->xt == TTQ_F32
-                           ? launch_kernel(k_moe_prep<NS, true>, pg, dim3(kPlanThreads), 0, st, nullptr, nullptr, pl, pr)
-                           : launch_kernel(k_moe_prep<NS, false>, pg, dim3(kPlanThreads), 0, st, nullptr, nullptr, pl, pr))
+    if (hipError_t e = launch_kernel(k_moe_prep<XF32>, pg, dim3(kPlanThreads), 0, st, nullptr, nullptr, pl, pr))
         return e;
     MoeMm p{};
     p.tiles = pl.tiles; p.order = pl.order; p.slots = n;
@@ -638,7 +640,7 @@ static hipError_t launch_ns(const ttq_moe_args* a, const MoeLayout& L, char* ws,
 }
 
 hipError_t launch_moe_mfma(const ttq_moe_args* a, const MoeLayout& L, char* ws, hipStream_t st) {
-    return a->xt == TTQ_F32 ? launch_ns<3>(a, L, ws, st) : launch_ns<2>(a, L, ws, st);
+    return a->xt == TTQ_F32 ? launch_layer<true>(a, L, ws, st) : launch_layer<false>(a, L, ws, st);
 }
 
 }  // namespace ttq
