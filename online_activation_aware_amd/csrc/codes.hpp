@@ -84,4 +84,14 @@ __device__ __forceinline__ void field_codes(const CodeWords<BITS>& c, float (&q)
     }
 }
 
+// 4x4 exchange between the lane quarters (16-lane rows) and the four words of
+// a lane: word j of quarter q becomes word q of quarter j.
+__device__ __forceinline__ void swap_quarters(u32x4& w) {
+    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    w = u32x4{c[0], c[1], d[0], d[1]};
+}
+
 }  // namespace ttq

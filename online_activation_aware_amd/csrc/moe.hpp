@@ -182,6 +182,8 @@ __device__ __forceinline__ void moe_load_halves(uint32_t (&d)[NH / 2], rsrc_t r,
 #pragma unroll
     for (int v = 0; v < NH / 2; ++v) d[v] = W2 ? __builtin_amdgcn_alignbit(w[v + 1], w[v], (off & 2) * 8) : w[v];
 }
+// One of a word's two fp16 values.
+__device__ __forceinline__ float half_at(uint32_t d, bool hi) { return f16_to_f32((uint16_t)(hi ? d >> 16 : d & 0xFFFFu)); }
 // Whether the rows of steps and zeros need W2.
 inline bool moe_w2(const uint16_t* scale, const uint16_t* zero, int64_t groups) {
     return groups % 2 != 0 || (uintptr_t)scale % 4 != 0 || (uintptr_t)zero % 4 != 0;

@@ -130,8 +130,6 @@ __global__ __launch_bounds__(kPlanThreads) void k_moe_dot_prep(MoePlan pl, MoePr
 
 // ------------------------------------------------------------------ products
 
-__device__ __forceinline__ float half_at(uint32_t d, bool hi) { return f16_to_f32((uint16_t)(hi ? d >> 16 : d & 0xFFFFu)); }
-
 template <int GROUP, int ND, int TT, bool W2, bool GU>
 __global__ __launch_bounds__(kMdMaxWaves * kWave, TT == 1 ? 3 : 2) void k_moe_dot(MoeDot a) {
     constexpr int NG = kMdPiece / GROUP;          // groups of a piece and row: 16, 8 or 4

@@ -133,18 +133,6 @@ __device__ __forceinline__ u32x4 codes_plus16(uint32_t w) {
                  __builtin_amdgcn_perm(k41, hi, 0x04010400u), __builtin_amdgcn_perm(k41, hi, 0x04030402u)};
 }
 
-// 4x4 exchange between the lane quarters and the four words of a lane: word
-// j of quarter q becomes word q of quarter j.
-__device__ __forceinline__ void exchange_quarters(u32x4& w) {
-    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-    w = u32x4{c[0], c[1], d[0], d[1]};
-}
-
-__device__ __forceinline__ float half_of(uint32_t d, bool hi) { return f16_to_f32((uint16_t)(hi ? d >> 16 : d & 0xFFFFu)); }
-
 constexpr int kMmBlock = 4;                       // chunks whose codes a wave has in flight
 constexpr int kMmStepLds = 3 * 1024;              // a wave's steps (fp16) and step (zero + 16) (fp32) of a block
 
@@ -365,7 +353,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) {
             w4[rt] = u32x4{ring[u][rt].c.w[0], ring[u][rt].c.w[1], ring[u][rt].c.w[2], ring[u][rt].c.w[BITS > 3 ? 3 : 0]};
-            if constexpr (kExchange) exchange_quarters(w4[rt]);
+            if constexpr (kExchange) swap_quarters(w4[rt]);
             p[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
             const int g = (16 * rt + r16) * NB + u * NG;
             if constexpr (NG == 1) st[rt][0] = st_l[g];
@@ -389,7 +377,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
                 const int g = j / SPG;
 #pragma unroll
                 for (int rt = 0; rt < 2; ++rt) {
-                    const float s = half_of(st[rt][g / 2], g & 1);
+                    const float s = half_at(st[rt][g / 2], g & 1);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[rt][e] = __builtin_fmaf(s, p[rt][e], acc[rt][e]);
                     p[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -419,7 +407,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
                 float nb[NH];
 #pragma unroll
                 for (int v = 0; v < NH; ++v)
-                    nb[v] = -(half_of(sw[v / 2], v & 1) * (half_of(zw[v / 2], v & 1) + 16.f));
+                    nb[v] = -(half_at(sw[v / 2], v & 1) * (half_at(zw[v / 2], v & 1) + 16.f));
                 const int left = (int)gpr - (cb + b) * NG - gpart * NH;   // groups of the row from here
                 if (left < NH)                    // behind the row: the next row's, which may be anything
 #pragma unroll

@@ -31,6 +31,7 @@
 // inside one launch would need a counter in known state or a device-scope
 // fence per workgroup, which writes back and invalidates the L2 of its
 // XCD).  Both orders are fixed, so results do not depend on timing.
+#include "codes.hpp"
 #include "common.hpp"
 #include "launch.hpp"
 #include "lds_dma.hpp"
@@ -88,19 +89,6 @@ __device__ __forceinline__ u32x4 codes_as_bf16(uint32_t w) {
     r[2] = __builtin_amdgcn_perm(k43, hi, 0x04010400u);   // codes 1, 3
     r[3] = __builtin_amdgcn_perm(k43, hi, 0x04030402u);   // codes 5, 7
     return r;
-}
-
-// 4x4 exchange between the lane quarters (16-lane rows) and the four words
-// of a lane: word j of quarter q becomes word q of quarter j.
-__device__ __forceinline__ void swap_quarters(u32x4& w) {
-    const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-    const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-    w[0] = c[0];
-    w[1] = c[1];
-    w[2] = d[0];
-    w[3] = d[1];
 }
 
 __device__ __forceinline__ float h2f_lo(uint32_t d) { return f16_to_f32((uint16_t)(d & 0xFFFFu)); }
