@@ -12,6 +12,15 @@
 // the offset, the difference of the two terms loses three bits fewer.
 // step (zero + 16) is exact in fp32 (11 by 5 bits).
 //
+// With fp32 X that difference is what rounds most: P is five times as large as
+// what it is for, and the outputs were off by 3e-6 to 5e-6 of themselves (2e-7
+// to 1e-6 in fp32 arithmetic).  There P is summed over q - c, c the zero as an
+// integer, exact in bf16 too; only what is left of a zero, step (c - zero) S_t,
+// is added.  Three operations a code instead of two: off by 2e-7 to 3.4e-7; 3 to
+// 32 tokens of two of 8 experts, 2048 -> 4096, 42 -> 50, 46 -> 55, 61 -> 75 us; 128
+// tokens, 4096 -> 8192, 334 -> 417 us (the weights form below: 6e-7 to 1.4e-6, 61,
+// 76, 91 and 639 us).
+//
 // Other bit widths, and groups of 16 (the weights form): a lane expands the 32
 // channels it loads to (code - zero) step, exact in 16 bits and so as two bf16
 // terms; about six instructions a code where the sums form takes two.
@@ -133,8 +142,23 @@ __device__ __forceinline__ u32x4 codes_plus16(uint32_t w) {
                  __builtin_amdgcn_perm(k41, hi, 0x04010400u), __builtin_amdgcn_perm(k41, hi, 0x04030402u)};
 }
 
+// The bf16 numbers q - z of the eight codes of a word, z an integer of at most
+// kMaxShift, slot order as above.
+constexpr float kMaxShift = 128.f;
+__device__ __forceinline__ u32x4 codes_minus(uint32_t w, float z) {
+    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+    return u32x4{pack_bf16x2(cvt_ubyte<0>(lo) - z, cvt_ubyte<1>(lo) - z), pack_bf16x2(cvt_ubyte<2>(lo) - z, cvt_ubyte<3>(lo) - z),
+                 pack_bf16x2(cvt_ubyte<0>(hi) - z, cvt_ubyte<1>(hi) - z), pack_bf16x2(cvt_ubyte<2>(hi) - z, cvt_ubyte<3>(hi) - z)};
+}
+// The integer that is taken from the codes of a group with this zero (a NaN:
+// any; what is left of the zero then is NaN).
+__device__ __forceinline__ float shift_of(float zero) { return fminf(fmaxf(rintf(zero), -kMaxShift), kMaxShift); }
+
 constexpr int kMmBlock = 4;                       // chunks whose codes a wave has in flight
-constexpr int kMmStepLds = 3 * 1024;              // a wave's steps (fp16) and step (zero + 16) (fp32) of a block
+// A wave's steps (fp16) and step (zero + 16) (fp32) of a block; or steps with
+// what is taken from the codes (pairs of fp16) and what is left of the zeros
+// (fp16).
+constexpr int kMmStepLds = 3 * 1024;
 
 // LDS of x~: per slot and chunk NS * 256 bytes of terms and 32 of sums, and 32
 // a row.  Where the whole slice does not fit,
@@ -154,6 +178,7 @@ static_assert(kMmMaxX + kMmMaxWaves * kMmStepLds <= 160 * 1024, "LDS of a comput
 template <int BITS, int GROUP, int NS, bool W2, bool GU>
 __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     constexpr bool kSums = BITS == 4 && GROUP >= 32;
+    constexpr bool kShift = NS == 3;              // sums of q - zero, not 16 + q
     constexpr int NG = kMmChunk / GROUP;          // groups per chunk
     constexpr int SPG = kSums ? GROUP / 32 : 1;   // subgroups per group
     constexpr int SG = GROUP < 32 ? 2 : 1;        // groups of a lane's 32 channels
@@ -305,6 +330,8 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
     unsigned char* const my = smem + wave * kMmStepLds;
     uint16_t* const st_l = (uint16_t*)my;         // [32][NB]
     float* const nb_l = (float*)(my + 1024);      // [32][NB]
+    uint32_t* const sz_l = (uint32_t*)my;         // kShift: [32][NB]
+    uint16_t* const rest_l = (uint16_t*)(my + 2048);
     const int gq = NG == 4 ? q : NG == 2 ? q >> 1 : 0;   // group of subgroup q within a chunk
 
     f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
@@ -348,25 +375,35 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
         const float si = sp[0] + sp[1];
         f32x4 p[2];
         u32x4 w4[2];
-        uint32_t st[2][(NG + 1) / 2];
-        float nb[2];
+        uint32_t st[2][(NG + 1) / 2];             // steps
+        float nb[2];                              // the zero terms' factors: -step (zero + 16), or what is left of it
+        uint32_t sz[2][kShift ? NG : 1];
 #pragma unroll
         for (int rt = 0; rt < 2; ++rt) {
             w4[rt] = u32x4{ring[u][rt].c.w[0], ring[u][rt].c.w[1], ring[u][rt].c.w[2], ring[u][rt].c.w[BITS > 3 ? 3 : 0]};
             if constexpr (kExchange) swap_quarters(w4[rt]);
             p[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
             const int g = (16 * rt + r16) * NB + u * NG;
-            if constexpr (NG == 1) st[rt][0] = st_l[g];
-            else
+            if constexpr (kShift) {
 #pragma unroll
-                for (int v = 0; v < NG / 2; ++v) st[rt][v] = ((const uint32_t*)(st_l + g))[v];
-            nb[rt] = nb_l[g + gq];
+                for (int v = 0; v < NG; ++v) sz[rt][v] = sz_l[g + v];
+                nb[rt] = half_at(sz_l[g + gq], false) * f16_to_f32(rest_l[g + gq]);
+            } else {
+                if constexpr (NG == 1) st[rt][0] = st_l[g];
+                else
+#pragma unroll
+                    for (int v = 0; v < NG / 2; ++v) st[rt][v] = ((const uint32_t*)(st_l + g))[v];
+                nb[rt] = nb_l[g + gq];
+            }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             u32x4 bb[2];
 #pragma unroll
-            for (int rt = 0; rt < 2; ++rt) bb[rt] = codes_plus16(w4[rt][j]);
+            for (int rt = 0; rt < 2; ++rt) {
+                if constexpr (kShift) bb[rt] = codes_minus(w4[rt][j], half_at(sz[rt][j / SPG], true));
+                else bb[rt] = codes_plus16(w4[rt][j]);
+            }
 #pragma unroll
             for (int n = NS - 1; n >= 0; --n) {
                 const u32x4 x = *(const u32x4*)(smem + xa[j] + (u * NS + n) * 256);
@@ -377,7 +414,9 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
                 const int g = j / SPG;
 #pragma unroll
                 for (int rt = 0; rt < 2; ++rt) {
-                    const float s = half_at(st[rt][g / 2], g & 1);
+                    float s;
+                    if constexpr (kShift) s = half_at(sz[rt][g], false);
+                    else s = half_at(st[rt][g / 2], g & 1);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[rt][e] = __builtin_fmaf(s, p[rt][e], acc[rt][e]);
                     p[rt] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -404,22 +443,29 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
             // This block's steps into the wave's part of LDS (its reads of the
             // block before are done: LDS operations of a wave keep their order).
             if (kSums && lane < 32 * kParts) {
-                float nb[NH];
-#pragma unroll
-                for (int v = 0; v < NH; ++v)
-                    nb[v] = -(half_at(sw[v / 2], v & 1) * (half_at(zw[v / 2], v & 1) + 16.f));
                 const int left = (int)gpr - (cb + b) * NG - gpart * NH;   // groups of the row from here
                 if (left < NH)                    // behind the row: the next row's, which may be anything
 #pragma unroll
                     for (int v = 0; v < NH; ++v)
                         if (v >= left) {
-                            nb[v] = 0.f;
                             sw[v / 2] &= v & 1 ? 0xFFFFu : 0u;
+                            zw[v / 2] &= v & 1 ? 0xFFFFu : 0u;
                         }
+                if constexpr (kShift) {
 #pragma unroll
-                for (int v = 0; v < NH / 2; ++v) ((uint32_t*)(st_l + grow * NB + gpart * NH))[v] = sw[v];
+                    for (int v = 0; v < NH; ++v) {
+                        const float z = half_at(zw[v / 2], v & 1), c = shift_of(z);
+                        const uint32_t st = v & 1 ? sw[v / 2] >> 16 : sw[v / 2] & 0xFFFFu;
+                        sz_l[grow * NB + gpart * NH + v] = st | (uint32_t)f32_to_f16_rne(c) << 16;
+                        rest_l[grow * NB + gpart * NH + v] = f32_to_f16_rne(c - z);   // exact
+                    }
+                } else {
 #pragma unroll
-                for (int v = 0; v < NH; ++v) nb_l[grow * NB + gpart * NH + v] = nb[v];
+                    for (int v = 0; v < NH / 2; ++v) ((uint32_t*)(st_l + grow * NB + gpart * NH))[v] = sw[v];
+#pragma unroll
+                    for (int v = 0; v < NH; ++v)
+                        nb_l[grow * NB + gpart * NH + v] = -(half_at(sw[v / 2], v & 1) * (half_at(zw[v / 2], v & 1) + 16.f));
+                }
             }
             __builtin_amdgcn_wave_barrier();
             const int bn = b + D * nk;

@@ -2,19 +2,22 @@
 the checks that outputs follow them.
 
 Each rounding is taken as uniform within its half step h and independent of
-the others: variance h^2 / 3.  Half steps, relative to the value: bf16 2^-8,
+the others: variance h^2 / 3 (so for weights of either sign, as random ones
+are).  Half steps, relative to the value: bf16 2^-8,
 fp32 2^-24; an addition inside a matrix instruction is counted with 2^-23, as
 if it truncated.  Errors are carried through the products and the activation
 to first order (a slot's errors as independent of the token's other slots: an
-expert named twice repeats them, which is not modelled).  The model counts, for y_o = sum_j w_oj x~_j, w = (q - z) d:
+expert named twice repeats them, which is not modelled).  The model counts,
+for y_o = sum_j w_oj x~_j, w = (q - z) d:
 
 - the operand: NS bf16 terms, half step 2^-(8 NS) |x~|; or digits, a scale
   per 32 channels of their largest over 489335 (five) or 7829367 (six digits),
   half step scale / 2, and three fp32 roundings of the largest;
-- 4-bit codes in groups of 32 or more, matrix cores: sums P of (16 + q) x~ per
-  32 channels in four steps of a matrix instruction, groups of more channels
-  growing linearly, their addition (times d) to the running sum, which holds
-  up to 128 channels of them, and the zero terms;
+- 4-bit codes in groups of 32 or more, matrix cores: sums P of (16 + q) x~
+  (fp32 X: of q minus the zero's integer) per 32 channels in four steps of a
+  matrix instruction, groups of more channels growing linearly, their addition
+  (times d) to the running sum, which holds up to 128 channels of them, and
+  the zero terms;
 - digits: the integer sum as fp32 (q - 8 times x~), the zero term, the product;
 - other codes: 2 NS products per 32 channels into the running sum;
 - the running sum, as large as the terms' root sum of squares R.
@@ -80,7 +83,11 @@ class Form:
             var += U ** 2 / 3 * (x2 @ ((q - 8) * d).T ** 2 + (3 + pieces) * R)
         elif self.sums:
             per, ng = self.group / 32, 128 / self.group
-            P, Z = x2 @ (((16 + q) * d) ** 2).T, x2 @ (((16 + z) * d) ** 2).T
+            if self.terms == 2:
+                P, Z = x2 @ (((16 + q) * d) ** 2).T, x2 @ (((16 + z) * d) ** 2).T
+            else:
+                c = np.rint(z).clip(-128, 128)
+                P, Z = x2 @ (((q - c) * d) ** 2).T, x2 @ (((c - z) * d) ** 2).T
             var += M1 ** 2 / 3 * (4 * (per + 1) / 2 * P + 4 * Z) + U ** 2 / 3 * (ng + 1) / 2 * P
             var += R * (U ** 2 / 3 * (K / self.group + 20) + M1 ** 2 / 3 * (K / 32)) / 2
         else:

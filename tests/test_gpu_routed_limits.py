@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import routed_limits as lim
+import routed_ref as ref
 from gpu_util import f32_dev, i32_dev, say, to_dev
 from online_activation_aware_amd import synth
 from test_gpu_routed import SHARED, num
@@ -161,3 +162,27 @@ def test_expert_layer_steps_at_half_words_and_a_used_workspace(T, case):
         lim.check(got[1:-1, 1:1 + M], y, var)
         assert np.all(got[[0, -1]] == -7) and np.all(got[:, 0] == -7) and np.all(got[:, 1 + M:] == -7)
         assert torch.all(ws[need:] == 255)
+
+
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("bits,group", [(4, 32), (4, 64), (4, 128), (3, 16), (2, 32)])
+@pytest.mark.parametrize("Tn", [1, 2, 5, 40])
+def test_zeros_of_any_value(T, Tn, bits, group, xt):
+    """Zeros between the codes, below and far above them are taken as they are."""
+    say(f"layer zeros b{bits} g{group} {xt} T={Tn}")
+    case = (Tn, 3, 2, 384, 256, 70, bits, group, xt, "silu", "any")
+    d = lim.moe_case(case)
+    rng = np.random.default_rng(Tn)
+    d["ids"] = np.argsort(rng.random((Tn, 3)), axis=1)[:, :2].astype(np.int32)
+    for q in (d["gate_up"], d["down"]):
+        z = (rng.integers(-4, 20, q["zero"].shape) + rng.integers(0, 8, q["zero"].shape) / 8).astype(np.float16)
+        z[rng.random(z.shape) < 0.02] = 200.125
+        q["zero"] = z
+        q["num"] = (*q["num"][:2], np.repeat(z.astype(np.float64), group, 2))
+    d["x"] = np.round(d["x"] * 8) / 1024
+    # Weights of one sign: the roundings of a group's sum of x / s are common to all of a token's outputs, not independent
+    # as in the variances, so the limit is the sum of the largest roundings.
+    gu, dn = d["gate_up"], d["down"]
+    y, b = ref.moe(d["x"], d["ids"], d["w"].astype(np.float64), gu["num"], gu["s"].astype(np.float64), dn["num"], dn["s"].astype(np.float64),
+                   bits, "silu", 2.0 ** -16 if xt == "bf16" else 2.0 ** -23, group)
+    ref.check(moe_call(T, d, case), y, b, False)
