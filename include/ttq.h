@@ -462,8 +462,10 @@ size_t ttq_adapters_workspace_bytes(int64_t T, int64_t K, int64_t M, int rank);
  * ttq_qgemm_adapters — a quantized projection shared by the tokens' requests,
  * plus their adapters.  [TTQ §method b5, b7].
  *   Y[t] = W_hat (X[t] / s) + scale_a B_a (A_a X[t]),  a = ids[t]:
- *   ttq_qgemm followed by ttq_adapters_add, with Y rounded once.  The
- *   arguments are those of the two calls, and K is a multiple of 32.
+ *   ttq_qgemm followed by ttq_adapters_add, with Y rounded once, and for fp32 X
+ *   with 24 bits of x / s and fp32 sums (ttq_qgemm on more than four tokens: 16
+ *   bits of x and of the weight).  The arguments are those of the two calls,
+ *   and K is a multiple of 32.
  *   ws: ttq_qgemm_adapters_workspace_bytes(...) bytes, 256-byte aligned.
  */
 ttq_status ttq_qgemm_adapters(const void* X, int xt, int64_t T, int64_t K, int64_t ldx, const float* s,

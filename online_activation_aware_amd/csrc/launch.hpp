@@ -155,6 +155,14 @@ constexpr int64_t kMoeMaxT = 1024;
 size_t moe_ws_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E);
 hipError_t launch_moe(const ttq_moe_args* a, char* ws, hipStream_t st);
 
+// Projection of fp32 X with x / s to 24 bits (moe_mfma.hip): its partial sums
+// [parts][T][M], to be added in order, at the start of ws.
+int proj_f32_parts(int64_t T, int64_t K, int64_t M);
+size_t proj_f32_ws_bytes(int64_t T, int64_t K, int64_t M);
+hipError_t launch_proj_f32(const float* X, int64_t T, int64_t K, int64_t ldx, const float* s, const uint32_t* codes,
+                           const uint16_t* scale, const uint16_t* zero, int64_t M, int bits, int group, char* ws,
+                           hipStream_t st);
+
 // Adapters of many requests (adapters.hip).
 struct AdapterTable {
     const void* A;

@@ -27,13 +27,20 @@ struct MoePlan {
 constexpr int kPlanThreads = 512;
 constexpr int kSimds = 4 * 256;                   // of the chip
 
-// One workgroup of kPlanThreads: the slots grouped by expert into `order`
+// One workgroup of kPlanThreads: the slots grouped by expert (without ids: all
+// of expert 0, in their order) into `order`
 // and the tiles, unused ones with count 0.  The place of a slot within its
 // expert depends on the timing of LDS atomics, and no result depends on it: a
 // slot's products are those of its own row wherever that row stands.
 __device__ __forceinline__ void moe_plan(const MoePlan& a) {
     __shared__ int cnt[kMoeMaxExperts], pos[kMoeMaxExperts];
     const int tid = threadIdx.x;
+    if (a.ids == nullptr) {
+        for (int i = tid; i < a.n; i += kPlanThreads) a.order[i] = i;
+        for (int j = tid; j < a.ntiles; j += kPlanThreads)
+            a.tiles[j] = MoeTile{0, j * a.tile, min(a.tile, a.n - j * a.tile)};
+        return;
+    }
     for (int e = tid; e < a.E; e += kPlanThreads) cnt[e] = 0;
     __syncthreads();
     for (int i = tid; i < a.n; i += kPlanThreads) {
@@ -121,7 +128,8 @@ struct MoeMm {
     uint16_t* ht;               // [slots][terms][hp]
     float* hs;
     int64_t hp;
-    float* p;                   // second product: [slices][slots][rows]
+    float* p;                   // second product: [slices][slots][ldp], from its row's place
+    int64_t ldp;
 };
 
 // Eight channels from k0 of token t, divided by the scales of expert e.

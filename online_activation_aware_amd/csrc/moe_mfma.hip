@@ -517,7 +517,7 @@ __global__ __launch_bounds__(kMmMaxWaves * kWave, 4) void k_moe_mfma(MoeMm a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (4 * q + e < rows)
-                        a.p[((int64_t)blockIdx.z * a.slots + a.order[tl.first + 4 * q + e]) * a.rows + o] = acc[rt][e];
+                        a.p[((int64_t)blockIdx.z * a.slots + a.order[tl.first + 4 * q + e]) * a.ldp + o] = acc[rt][e];
             }
         }
     } else {
@@ -628,6 +628,24 @@ static hipError_t launch_mm(const MoeMm& p, int bits, int group, dim3 grid, int 
     return hipErrorInvalidValue;
 }
 
+// Chunks of a slice where `sl` are wanted.  An even number: a slice's first step
+// lies at a word's start also where a chunk is one group (a load at half a word
+// would lose the steps of the last row's end, cut off there by the buffer's
+// word-wise bound).
+static int mm_per_slice(int64_t chunks, int64_t sl) { return (int)((chunks + sl - 1) / sl + 1) & ~1; }
+
+// d.p = the products of n operand rows and d.rows code rows, in slices of
+// per_slice chunks.
+template <int NS>
+static hipError_t launch_rows(MoeMm d, int bits, int64_t nt, int64_t n, int64_t E, int per_slice, hipStream_t st) {
+    const int64_t chunks = d.kp / kMmChunk, nsl = (chunks + per_slice - 1) / per_slice;
+    const int64_t dw = (d.rows + kMmRows - 1) / kMmRows;
+    const MmShape v = mm_shape(dw, nt * nsl, per_slice, n, E, NS);
+    d.per_slice = per_slice; d.ksplit = v.nk; d.xbytes = v.xbytes;
+    return launch_mm<NS, false>(d, bits, d.group, dim3((unsigned)((dw + v.nr - 1) / v.nr), (unsigned)nt, (unsigned)nsl),
+                                v.nr * v.nk, v.lds(), st);
+}
+
 template <bool XF32>
 static hipError_t launch_layer(const ttq_moe_args* a, const MoeLayout& L, char* ws, hipStream_t st) {
     constexpr int NS = mm_terms(XF32);
@@ -656,25 +674,77 @@ static hipError_t launch_layer(const ttq_moe_args* a, const MoeLayout& L, char* 
     d.tiles = pl.tiles; d.order = pl.order; d.slots = n;
     d.xt = p.ht; d.xs = p.hs; d.K = a->I; d.group = a->group; d.kp = ip; d.rows = a->M; d.div = 1;
     d.codes = (const uint32_t*)a->down.codes; d.scale = a->down.scale_f16; d.zero = a->down.zero_f16;
-    d.p = (float*)(ws + L.p);
-    const int chunks = (int)(ip / kMmChunk), sl = moe_slices(n, a->E, a->I, a->M);
-    // An even number of chunks: a slice's first step lies at a word's start also
-    // where a chunk is one group (a load at half a word would lose the steps of
-    // the last row's end, cut off there by the buffer's word-wise bound).
-    d.per_slice = ((chunks + sl - 1) / sl + 1) & ~1;
-    const int nsl = (chunks + d.per_slice - 1) / d.per_slice;
-    const int64_t dw = (a->M + kMmRows - 1) / kMmRows;
-    const MmShape v = mm_shape(dw, nt * nsl, d.per_slice, n, a->E, NS);
-    d.ksplit = v.nk; d.xbytes = v.xbytes;
-    if (hipError_t e = launch_mm<NS, false>(d, a->bits, a->group,
-                                            dim3((unsigned)((dw + v.nr - 1) / v.nr), (unsigned)nt, (unsigned)nsl),
-                                            v.nr * v.nk, v.lds(), st))
-        return e;
-    return launch_moe_sum(a, d.p, nsl, st);
+    d.p = (float*)(ws + L.p); d.ldp = a->M;
+    const int64_t chunks = ip / kMmChunk;
+    const int per = mm_per_slice(chunks, moe_slices(n, a->E, a->I, a->M));
+    if (hipError_t e = launch_rows<NS>(d, a->bits, nt, n, a->E, per, st)) return e;
+    return launch_moe_sum(a, d.p, (int)((chunks + per - 1) / per), st);
 }
 
 hipError_t launch_moe_mfma(const ttq_moe_args* a, const MoeLayout& L, char* ws, hipStream_t st) {
     return a->xt == TTQ_F32 ? launch_layer<true>(a, L, ws, st) : launch_layer<false>(a, L, ws, st);
+}
+
+// ------------------------------------------------------------------ one weight for all tokens
+
+// A projection of fp32 X with x / s to 24 bits: one expert's product, off by
+// 1.5e-7 to 3.4e-7 of the outputs (two bf16 halves of x and of the weight: 3e-6).
+// In ttq_qgemm_adapters, 4096 -> 4096, 4-bit groups of 32 (in brackets with the
+// halves' kernels): 16 tokens 29 (30) us, 64 47 (60), 300 114 (333), 1024 233 (355);
+// 16 tokens 2048 -> 2048, where one launch more counts, 31 (21).  At most
+// kProjTokens tokens a pass, and of code rows what a buffer descriptor holds.
+constexpr int64_t kProjTokens = 4096;
+
+struct ProjLayout {
+    size_t p, order, tiles, xt, xs, total;
+};
+static ProjLayout proj_layout(int64_t T, int64_t K, int64_t M) {
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    const int64_t n = T < kProjTokens ? T : kProjTokens, kp = moe_pad(K);
+    ProjLayout L{};
+    L.p = 0;
+    L.order = L.p + up((size_t)proj_f32_parts(T, K, M) * T * M * 4);
+    L.tiles = L.order + up((size_t)n * 4);
+    L.xt = L.tiles + up((size_t)moe_tiles(n, 1, kMmTile) * sizeof(MoeTile));
+    L.xs = L.xt + up((size_t)n * mm_terms(true) * kp * 2);
+    L.total = L.xs + up((size_t)n * (kp / 16) * 4);
+    return L;
+}
+static int proj_per_slice(int64_t T, int64_t K, int64_t M) {
+    return mm_per_slice(moe_pad(K) / kMmChunk, moe_slices(T < kProjTokens ? T : kProjTokens, 1, K, M));
+}
+int proj_f32_parts(int64_t T, int64_t K, int64_t M) {
+    const int per = proj_per_slice(T, K, M);
+    return (int)((moe_pad(K) / kMmChunk + per - 1) / per);
+}
+size_t proj_f32_ws_bytes(int64_t T, int64_t K, int64_t M) { return proj_layout(T, K, M).total; }
+
+hipError_t launch_proj_f32(const float* X, int64_t T, int64_t K, int64_t ldx, const float* s, const uint32_t* codes,
+                           const uint16_t* scale, const uint16_t* zero, int64_t M, int bits, int group, char* ws,
+                           hipStream_t st) {
+    constexpr int NS = mm_terms(true);
+    const ProjLayout L = proj_layout(T, K, M);
+    const int64_t kp = moe_pad(K), wpr = K * bits / 32;
+    const int64_t most = (((int64_t)1 << 31) - 1) / (wpr * 4) / kMmRows * kMmRows;   // code rows
+    for (int64_t t0 = 0; t0 < T; t0 += kProjTokens) {
+        const int64_t n = T - t0 < kProjTokens ? T - t0 : kProjTokens, nt = moe_tiles(n, 1, kMmTile);
+        MoePlan pl{nullptr, (int)n, 1, kMmTile, (int)nt, (int32_t*)(ws + L.order), (MoeTile*)(ws + L.tiles)};
+        MoePrep pr{};
+        pr.X = X + t0 * ldx; pr.ldx = ldx; pr.K = K; pr.kp = kp; pr.rows = n; pr.s = s;
+        pr.xt = (uint16_t*)(ws + L.xt); pr.xs = (float*)(ws + L.xs);
+        const dim3 pg((unsigned)(1 + (n * (kp / 8) + kPlanThreads - 1) / kPlanThreads));
+        if (hipError_t e = launch_kernel(k_moe_prep<true>, pg, dim3(kPlanThreads), 0, st, nullptr, nullptr, pl, pr)) return e;
+        for (int64_t r0 = 0; r0 < M; r0 += most) {
+            MoeMm d{};
+            d.tiles = pl.tiles; d.order = pl.order; d.slots = T;
+            d.xt = pr.xt; d.xs = pr.xs; d.K = K; d.group = group; d.kp = kp; d.div = 1;
+            d.rows = M - r0 < most ? M - r0 : most;
+            d.codes = codes + r0 * wpr; d.scale = scale + r0 * (K / group); d.zero = zero + r0 * (K / group);
+            d.p = (float*)(ws + L.p) + t0 * M + r0; d.ldp = M;
+            if (hipError_t e = launch_rows<NS>(d, bits, nt, n, 1, proj_per_slice(T, K, M), st)) return e;
+        }
+    }
+    return hipSuccess;
 }
 
 }  // namespace ttq

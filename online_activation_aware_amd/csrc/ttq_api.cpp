@@ -615,8 +615,12 @@ ttq::AdapterTable adapter_table(const ttq_adapters* ad) {
     return {ad->A, ad->B, ad->dt == TTQ_F32, (int)ad->n, ad->rank, ad->ranks, ad->scale, ad->ids};
 }
 
-// Workspace of ttq_qgemm_adapters: the adapters' sums, the projection in
-// fp32, the projection's own workspace.
+// fp32 X: four tokens at most have a projection in fp32 arithmetic
+// (launch_qgemv); ttq_qgemm's other ones keep 16 bits of x / s, this one 24.
+bool shared_f32(int64_t T, int64_t K) { return T > 4 || K % 128 != 0; }
+
+// Workspace of ttq_qgemm_adapters: the adapters' sums, then the projection in
+// fp32 and its own workspace, or that of the projection of fp32 X.
 struct SharedLayout {
     size_t z, c, q, total;
 };
@@ -626,6 +630,8 @@ SharedLayout shared_layout(int64_t T, int64_t K, int64_t M, int rank) {
     L.c = L.z + round_up(ttq::adapters_ws_bytes(T, K, rank));
     L.q = L.c + round_up((size_t)T * (size_t)M * 4);
     L.total = L.q + ws_qgemm(T, K, M);
+    const size_t f32 = L.c + (shared_f32(T, K) ? ttq::proj_f32_ws_bytes(T, K, M) : 0);
+    if (L.total < f32) L.total = f32;
     return L;
 }
 
@@ -723,7 +729,15 @@ ttq_status ttq_qgemm_adapters(const void* X, int xt, int64_t T, int64_t K, int64
     float* C = (float*)(w + L.c);
     const bool xf32 = xt == TTQ_F32;
     ttq::ProjectionIn ci{C, true, M};
-    if (ttq::qgemv_gs_eligible(T, K, M, bits, group, xf32, ldx)) {
+    if (xf32 && shared_f32(T, K)) {
+        if (ttq_status e = device_status(
+                ttq::launch_proj_f32((const float*)X, T, K, ldx, s, (const uint32_t*)codes, scale_f16, zero_f16, M, bits,
+                                     group, w + L.c, as_stream(stream)),
+                "ttq_qgemm_adapters launch"))
+            return e;
+        ci.parts = ttq::proj_f32_parts(T, K, M);
+        ci.stride = T * M;
+    } else if (ttq::qgemv_gs_eligible(T, K, M, bits, group, xf32, ldx)) {
         // The K slices' partial sums are added where the adapters are.
         if (ttq_status e = device_status(
                 ttq::launch_qgemv_gs(X, xf32, T, K, ldx, s, (const uint32_t*)codes, scale_f16, zero_f16, M, bits, group,

@@ -138,6 +138,20 @@ MIXED = [
 ]
 
 
+# Shared projections beside those of the element-wise tests: T, K, M, bits, group, n, rank, xt, yt, ids
+SHARED = [
+    (140, 512, 136, 4, 32, 60, 16, "bf16", "f32", "mixed"),
+    (190, 1024, 65, 3, 32, 30, 24, "bf16", "f32", "mixed"),
+    (1, 2048, 129, 4, 64, 3, 8, "f32", "f32", "mixed"),
+    (4, 1184, 70, 4, 32, 3, 8, "f32", "f32", "mixed"),
+    (5, 4096, 40, 4, 128, 6, 16, "f32", "f32", "mixed"),
+    (30, 2368, 136, 4, 64, 9, 8, "f32", "f32", "mixed"),
+    (140, 3200, 264, 4, 32, 12, 16, "f32", "f32", "mixed"),
+    (200, 608, 96, 2, 16, 5, 32, "f32", "f32", "runs"),
+    (4200, 128, 64, 4, 32, 5, 8, "f32", "f32", "runs"),
+]
+
+
 def moe_case(case, seed=0):
     """numpy inputs of an expert layer: x (values of its type), ids, w, and
     per weight its codes, steps, zeros, s, and (q, d, z) in fp64."""
@@ -244,16 +258,23 @@ def moe(x, ids, wts, gu, s_in, dn, s_down, bits, name, xt, group, less=0, drop_s
     return y, var + (U * y) ** 2 / 3
 
 
-def shared(x, num, s, xt):
-    """(Y, variance) of the shared projection: x / s or the dequantized weight
-    rounded to bf16, or both split in two for fp32 X (their product's last
-    part left out: 2^-14)."""
+def shared(x, num, s, xt, bits, group):
+    """(Y, variance) of the shared projection: for bf16 X, x / s or the
+    dequantized weight rounded to bf16; for fp32 X the product of an expert, or
+    up to four tokens in fp32 (x times 1 / s, sums per group and lane)."""
     q, d, z = num
+    T, K = x.shape
+    if xt == "f32" and (T > 4 or K % 128):
+        f = Form(3, bits, group, xt)
+        y, var = f.product(x, np.zeros_like(x), num, s)
+        return y, var + (U * y) ** 2 / 3 * 16      # the slices
     w = (q - z) * d / s
     R = x ** 2 @ (w ** 2).T
+    if xt == "f32":                                # fused multiply-adds of q x and sums of x over 32 channels, a lane's groups, 64 lanes
+        lane = x ** 2 @ ((q ** 2 + z ** 2) * (d / s) ** 2).T
+        return x @ w.T, U ** 2 / 3 * (9 * R + 20 * lane + (K / 32 + 64) * R)
     mag = x ** 2 @ (((q + z + 16) * d / s) ** 2).T
-    K = x.shape[1]
-    return x @ w.T, R * (2.0 ** -8 if xt == "bf16" else 2.0 ** -14) ** 2 / 3 + M1 ** 2 / 3 * (16 * mag + 4 * K * R)
+    return x @ w.T, R * 2.0 ** -16 / 3 + M1 ** 2 / 3 * (16 * mag + 4 * K * R)
 
 
 def adapters(x, A, B, ids, ranks=None, scale=None, f32=False, z_terms=None):

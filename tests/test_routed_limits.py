@@ -5,11 +5,13 @@ import numpy as np
 import pytest
 
 import routed_limits as lim
-from test_gpu_routed import MOE, SHARED
+from test_gpu_routed import MOE
+from test_gpu_routed import SHARED as SHARED_CASES
 
 # the element-wise cases with fp32 outputs, in the form (T, E, topk, K, I, M, bits, group, xt, act, ids)
 LAYERS = [(*c[:9], c[10], "any") for c in MOE] + lim.EXPERTS
 LAYERS = list(dict.fromkeys(LAYERS))
+SHARED = SHARED_CASES + lim.SHARED
 
 
 @pytest.mark.parametrize("case", LAYERS, ids=lambda c: "-".join(map(str, c)))
@@ -46,10 +48,14 @@ def test_adapters(case):
 def test_shared_projections(case):
     Tn, K, M, bits, group, n, rank, xt, _, _ = case
     d, num, s = lim.shared_case(case)
-    y, var = lim.shared(d["x"], num, s, xt)
+    y, var = lim.shared(d["x"], num, s, xt, bits, group)
     a, va = lim.adapters(d["x"], d["a"], d["b"], d["ids"], d["ranks"], d["scale"], xt == "f32")
     assert lim.far(y, y + a, var + va)
     assert lim.far(a, y + a, var + va)
     x = d["x"].copy()
     x[:, K - 32:] = 0
-    assert lim.far(lim.shared(x, num, s, xt)[0] + a, y + a, var + va)
+    assert lim.far(lim.shared(x, num, s, xt, bits, group)[0] + a, y + a, var + va)
+    if xt == "f32" and (Tn > 4 or K % 128):        # x cut to two bf16 terms
+        x = lim.bf16(d["x"])
+        x = x + lim.bf16(d["x"] - x)
+        assert lim.far(lim.shared(x, num, s, xt, bits, group)[0] + a, y + a, var + va)
