@@ -21,6 +21,15 @@
 
 namespace ttq {
 
+// From here on the kernels for runs of one adapter: the ids lie on the device,
+// so the number of tokens decides.  Runs of 100 tokens (in brackets an adapter of
+// 64 for every token), bf16, rank 16 and 64, 4096 -> 4096, the kernels for few
+// tokens against these: 128 tokens 11 (18) against 10 (61) us and 15 (30)
+// against 15 (134); 256: 13 (29) / 12 (73), 20 (51) / 18 (138); 512: 26 (49) / 21
+// (70), 42 (91) / 38 (135); 1024: 33 (84) / 20 (72), 54 (160) / 34 (143).  4096 ->
+// 14336, rank 32, 256 adapters: 128 tokens 18 (35) / 11 (97), 256 28 (62) / 14 (103).
+constexpr int64_t kRunsMinT = 512;
+
 constexpr uint32_t kOut = 0x80000000u;            // an offset behind every buffer: loads return zero
 
 // Rows of adapter a in use; 0 where the id names none.
@@ -176,7 +185,7 @@ __global__ __launch_bounds__(kAzWaves * kWave) void k_adapter_z(const void* __re
     }
 }
 
-// 128 tokens or more, bf16 operands: a workgroup owns 32 tokens and one K
+// kRunsMinT tokens or more, bf16 operands: a workgroup owns 32 tokens and one K
 // slice and passes it 256 channels at a time through LDS, so that memory is
 // read in rows of 512 consecutive bytes (the fragments above take 64 of each
 // row, rows 2 K bytes apart: a power of two for most K) and a row of A serves
@@ -603,7 +612,7 @@ __global__ __launch_bounds__(kA1Threads) void k_adapter_one(const void* __restri
     else ((uint16_t*)Y)[o] = (uint16_t)f32_to_bf16(c);
 }
 
-// 128 tokens or more, mostly runs of one adapter: a wave owns 64 rows of M,
+// kRunsMinT tokens or more, mostly runs of one adapter: a wave owns 64 rows of M,
 // keeps their B in registers and goes through four tiles of 16 tokens, all of
 // whose C it has requested at the start; a tile of several adapters, or another one
 // than the last, loads its B.  Column m of row tile rt is row 16 (m / 4) +
@@ -776,13 +785,13 @@ __global__ __launch_bounds__(kAyWaves * kWave) void k_adapter_runs(const float* 
 // K slices of z, whose partials every workgroup of the second launch adds:
 // at most eight, of at least 512 channels.  A tile of a few requests spreads
 // over the chip by its adapters as well (sixteen shares), its slices are of at
-// least 1024 (48 requests: 22.8 us; eight shares 23.9, slices of 512 24.5); 128 tokens or more
-// (runs of few adapters) by their tiles.
-static int z_shares(int64_t T) { return T == 1 || T >= 128 ? 1 : 16; }
+// least 1024 (48 requests: 22.8 us; eight shares 23.9, slices of 512 24.5);
+// kRunsMinT tokens or more (runs of few adapters) by their tiles.
+static int z_shares(int64_t T) { return T == 1 || T >= kRunsMinT ? 1 : 16; }
 static int64_t z_slices(int64_t T, int64_t K, int64_t* per) {
     const int64_t tiles = (T + 15) / 16;
-    int64_t s = tiles > 0 ? (T < 128 ? 8 : (512 + tiles - 1) / tiles) : 1;
-    const int64_t least = T > 1 && T < 128 ? 1024 : 512, most = K / least > 0 ? K / least : 1;
+    int64_t s = tiles > 0 ? (T < kRunsMinT ? 8 : (512 + tiles - 1) / tiles) : 1;
+    const int64_t least = T > 1 && T < kRunsMinT ? 1024 : 512, most = K / least > 0 ? K / least : 1;
     s = s > most ? most : s;
     s = s > 8 ? 8 : s;
     *per = ((K + s - 1) / s + 31) / 32 * 32;
@@ -800,7 +809,7 @@ static hipError_t launch_z(const void* X, int64_t T, int64_t K, int64_t ldx, con
     int64_t per;
     const int64_t s = z_slices(T, K, &per);
     if constexpr (!XF32 && !AF32)
-        if (T >= 128) {
+        if (T >= kRunsMinT) {
             const dim3 grid((unsigned)((T + 31) / 32), (unsigned)s);
 #define TTQ_AZR(RT)                                                                                                  \
     return launch_kernel(k_adapter_z_runs<RT>, grid, dim3(kAzWaves * kWave), 0, st, nullptr, nullptr,                \
@@ -830,7 +839,7 @@ static hipError_t launch_y(const float* Z, int64_t T, int64_t K, const AdapterTa
     auto vec = [](const void* p, int64_t ld, bool f32) { return (uintptr_t)p % (f32 ? 16 : 8) == 0 && ld % 4 == 0; };
     auto vec16 = [](const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; };
     const int cv = ci.C != nullptr && vec(ci.C, ci.ldc, CF32) && ci.stride % 4 == 0, yv = vec(Y, ldy, YF32);
-    if (T >= 128 && ad.rank % 8 == 0 && M % 8 == 0 && vec16(Y, ldy) && ci.parts == 1 &&
+    if (T >= kRunsMinT && ad.rank % 8 == 0 && M % 8 == 0 && vec16(Y, ldy) && ci.parts == 1 &&
         (ci.C == nullptr || vec16(ci.C, ci.ldc))) {
         const dim3 grid((unsigned)((M + 64 * kAyWaves - 1) / (64 * kAyWaves)),
                         (unsigned)((T + 16 * kArTiles - 1) / (16 * kArTiles)));

@@ -126,7 +126,7 @@ EXPERTS = [
     (1024, 70, 4, 64, 32, 32, 3, 32, "f32", "silu", "any"),
 ]
 
-# Adapters of 128 tokens or more in any order, an eighth of the tokens without one: T, K, M, n, rank, xt, at
+# Adapters of many tokens in any order, an eighth of the tokens without one: T, K, M, n, rank, xt, at
 MIXED = [
     (128, 256, 64, 40, 32, "bf16", "bf16"),
     (200, 4096, 72, 64, 64, "bf16", "bf16"),
@@ -135,6 +135,22 @@ MIXED = [
     (129, 520, 131, 20, 13, "bf16", "bf16"),
     (160, 264, 65, 50, 24, "f32", "bf16"),
     (300, 768, 200, 9, 48, "f32", "f32"),
+    (512, 4096, 72, 64, 64, "bf16", "bf16"),
+    (600, 1032, 136, 200, 8, "bf16", "bf16"),
+    (545, 264, 520, 30, 40, "bf16", "bf16"),
+    (530, 2056, 131, 20, 13, "bf16", "bf16"),
+    (520, 512, 264, 30, 16, "bf16", "f32"),
+    (513, 768, 200, 9, 48, "f32", "f32"),
+]
+
+# the same, ids in runs: the last token of every run and tokens without an adapter between them
+RUNS = [
+    (256, 2048, 192, 5, 64, "bf16", "bf16"),
+    (512, 4096, 64, 3, 64, "bf16", "bf16"),
+    (700, 3584, 136, 3, 32, "bf16", "f32"),
+    (513, 2560, 72, 2, 56, "bf16", "bf16"),
+    (515, 128, 48, 2, 40, "f32", "f32"),
+    (1000, 512, 264, 9, 16, "bf16", "bf16"),
 ]
 
 
@@ -175,10 +191,12 @@ def moe_model(d, case, **kw):
                dn["s"].astype(np.float64), bits, name, xt, group, **kw)
 
 
-def adapter_case(seed, Tn, K, M, n, rank, xt, at):
+def adapter_case(seed, Tn, K, M, n, rank, xt, at, runs=False):
     rng = np.random.default_rng(seed)
     cut = lambda a, t: oracle.decode(synth.encode(a, t), t)   # noqa: E731
-    ids = np.where(rng.random(Tn) < 0.125, -1, rng.integers(0, n, Tn)).astype(np.int32)
+    none = rng.random(Tn) < (0.02 if runs else 0.125)
+    ids = rng.integers(0, n, Tn)
+    ids = np.where(none, -1, np.sort(ids) if runs else ids).astype(np.int32)
     return dict(x=cut(rng.standard_normal((Tn, K)), xt), a=cut(rng.standard_normal((n, rank, K)) / np.sqrt(K), at),
                 b=cut(rng.standard_normal((n, M, rank)), at), ids=ids, ranks=rng.integers(0, rank + 1, n).astype(np.int32),
                 scale=(rng.random(n) + 0.5).astype(np.float32), rng=rng)

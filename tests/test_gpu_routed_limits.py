@@ -81,13 +81,13 @@ def test_a_token_in_calls_of_other_sizes(T, bits, group, xt):
 # ------------------------------------------------------------------ adapters
 
 @pytest.mark.parametrize("yt", ["f32", "bf16"])
-@pytest.mark.parametrize("case", lim.MIXED, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("case", lim.MIXED + lim.RUNS, ids=lambda c: "-".join(map(str, c)))
 def test_adapters_in_any_order(T, case, yt):
-    say(f"adapters mixed {case} {yt}")
+    say(f"adapters {case} {yt}")
     Tn, K, M, n, rank, xt, at = case
-    d = lim.adapter_case(sum(case[:5]), *case)
+    d = lim.adapter_case(sum(case[:5]), *case, runs=case in lim.RUNS)
     none = d["ids"] < 0
-    assert none.any() and len(set(d["ids"][:32])) > 5
+    assert none.any() and (len(set(d["ids"][:32])) > 5) == (case in lim.MIXED)
     y, var = lim.adapters(d["x"], d["a"], d["b"], d["ids"], d["ranks"], d["scale"], "f32" in (xt, at))
     A, B = dev(d["a"], at), dev(d["b"], at)
     for i, r in enumerate(d["ranks"]):             # what lies behind a rank is not used
