@@ -53,6 +53,8 @@
 // but take two operands' registers: 471 us at best).  16 tokens, six each of 64
 // experts, 2048 -> 2 x 1056 -> 2048: 78 us, 1.5 slots per tile of 16, where a
 // launch per product, its first loads and its end cost as much as the stream.
+// (With 128 registers no variant goes to memory for more; some keep up to 20
+// scalars in the lanes of a vector register.)
 #include "codes.hpp"
 #include "common.hpp"
 #include "launch.hpp"
