@@ -185,3 +185,43 @@ def test_refused_sizes_allocate_nothing(T):
         with pytest.raises(T.TTQError):
             T.ttq_moe_route(L, topk)
     assert torch.cuda.max_memory_allocated() - before < 1 << 16
+
+
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+def test_two_captured_graphs(T, xt):
+    """An expert layer and a shared projection in a graph each, with workspaces of their own, replayed in turn with
+    eager calls between."""
+    say(f"graphs {xt}")
+    Tn, K, I, n, rank, dt = 20, 640, 512, 4, 8, {"f32": torch.float32, "bf16": torch.bfloat16}[xt]
+    d = moe_inputs(3, Tn, 3, 2, K, I, K, 4, 64, xt)
+    ids, w = i32_dev(d["ids"]), f32_dev(d["w"])
+    q = {k: v[0].contiguous() for k, v in d["gate_up"].items() if k != "s"}
+    s, M = d["gate_up"]["s"], 2 * I
+    rng = np.random.default_rng(1)
+    A, B = enc(rng.standard_normal((n, rank, K)) / 16, xt)[0], enc(rng.standard_normal((n, M, rank)), xt)[0]
+    X, aid = torch.zeros((Tn, K), dtype=dt, device="cuda"), torch.zeros(Tn, dtype=torch.int32, device="cuda")
+
+    def layer(ws=None):
+        return T.ttq_moe(X, ids, w, d["gate_up"], d["down"], 4, 64, ws=ws)
+
+    def shared(ws=None):
+        return T.ttq_qgemm_adapters(X, s, q["codes"], q["scale_f16"], q["zero_f16"], M, 4, 64, A, B, aid, ws=ws)
+    own = [T.moe_workspace(Tn, 2, K, I, K, 3, 4, 64), T.qgemm_adapters_workspace(Tn, K, M, 4, 64, rank)]
+    graphs, held = [], []
+    for call, ws in zip((layer, shared), own):
+        call(ws)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            held.append(call(ws))
+    for seed in range(4):
+        r = np.random.default_rng(seed)
+        X.copy_(enc(r.standard_normal((Tn, K)), xt)[0])
+        aid.copy_(i32_dev(r.integers(-1, n, Tn)))
+        for i in (seed % 2, 1 - seed % 2):
+            graphs[i].replay()
+        got = [h.clone() for h in held]
+        eager = layer(), shared()
+        torch.cuda.synchronize()
+        for a, b in zip(got, eager):
+            assert torch.equal(a, b)
