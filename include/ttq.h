@@ -476,6 +476,164 @@ ttq_status ttq_qgemm_adapters(const void* X, int xt, int64_t T, int64_t K, int64
 /* Workspace bytes for ttq_qgemm_adapters (0 for sizes it does not accept). */
 size_t ttq_qgemm_adapters_workspace_bytes(int64_t T, int64_t K, int64_t M, int bits, int group, int rank);
 
+/*
+ * Linear layers in 8-bit integers.  [TTQ §method b1, b2, b7] the quantized
+ * projection with the scaled weight W diag(s) and the input X / s both in 8
+ * bits, one scale per output channel and one per token: twice the rate of the
+ * bf16 matrix cores, and rows of activations that several layers share.
+ *
+ * 8-bit rows: codes [R][K] int8, row stride a multiple of 16 bytes, codes
+ * 16-byte aligned; scale [R] fp32; row r stands for codes * scale[r].  K a
+ * positive multiple of 16, at most 2^17, so that a sum of K products of codes
+ * of -127..127 is exact in int32.
+ */
+
+/*
+ * ttq_quantize_rows — rows of X in 8 bits.
+ *   v[r][j] = X[r][j] (s NULL), fp32(X[r][j] / s[j]) (divide != 0: the input of
+ *   a projection) or fp32(X[r][j] * s[j]) (divide == 0: a weight [M][K]).
+ *   a = max_j |v[r][j]|;  scale[r] = fp32(a / 127), 1 where that is 0;
+ *   codes[r][j] = clamp(rne(v[r][j] / scale[r]), -127, 127), the rounding of the
+ *   exact quotient.
+ *   A row with an infinite or NaN v gets scale NaN and codes 0, so that its
+ *   products are NaN and no other row's.
+ *   X: [R][K] (xt), stride ldx.  s: [K] or NULL.  codes: stride ldc >= K.
+ *   R == 0 is an empty call.  No workspace.
+ */
+ttq_status ttq_quantize_rows(const void* X, int xt, int64_t R, int64_t K, int64_t ldx, const float* s,
+                             int divide, int8_t* codes, int64_t ldc, float* scale, void* stream);
+
+/*
+ * ttq_gemm_i8 — product of 8-bit rows.
+ *   Y[t][o] = x_scale[t] * w_scale[o] * sum_j X[t][j] W[o][j]: the sum exact in
+ *   int32, converted to fp32 and multiplied by x_scale[t], then by w_scale[o],
+ *   rounded once more to a bf16 Y.
+ *   X: [T][K] int8, stride ldx;  W: [M][K] int8, stride ldw, e.g. both from
+ *   ttq_quantize_rows.  Y: [T][M] (yt), stride ldy, overwritten; no overlap.
+ *   ldx and ldw up to 2^22 (else TTQ_ERR_UNSUPPORTED).  T == 0 or M == 0 is an
+ *   empty call.  ws: ttq_gemm_i8_workspace_bytes(T, K, M) bytes, 256-byte
+ *   aligned; calls that may run at the same time need workspaces of their own.
+ */
+ttq_status ttq_gemm_i8(const int8_t* X, const float* x_scale, int64_t T, int64_t K, int64_t ldx, const int8_t* W,
+                       const float* w_scale, int64_t M, int64_t ldw, void* Y, int yt, int64_t ldy, void* ws,
+                       size_t ws_bytes, void* stream);
+
+/* Workspace bytes for ttq_gemm_i8 (0 for sizes it does not accept). */
+size_t ttq_gemm_i8_workspace_bytes(int64_t T, int64_t K, int64_t M);
+
+/*
+ * ttq_qgemm_i8 — ttq_qgemm on an 8-bit state: Y = W_hat (X / s).
+ *   ttq_quantize_rows of X / s (s NULL: of X) followed by ttq_gemm_i8, with the
+ *   same results.  W and w_scale: ttq_quantize_rows of the weight times s.
+ *   X: [T][K] (xt), stride ldx.  The other arguments are those of ttq_gemm_i8.
+ *   ws: ttq_qgemm_i8_workspace_bytes(T, K, M) bytes, 256-byte aligned.
+ */
+ttq_status ttq_qgemm_i8(const void* X, int xt, int64_t T, int64_t K, int64_t ldx, const float* s, const int8_t* W,
+                        const float* w_scale, int64_t M, int64_t ldw, void* Y, int yt, int64_t ldy, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* Workspace bytes for ttq_qgemm_i8 (0 for sizes it does not accept). */
+size_t ttq_qgemm_i8_workspace_bytes(int64_t T, int64_t K, int64_t M);
+
+/*
+ * Tokens sorted by the experts they chose, and back, for experts that multiply
+ * many rows each (long prompts) and for training with them.
+ */
+
+/*
+ * ttq_moe_sort — the slots (t, j) of ids [T][topk] in the order of their
+ * experts, slots of one expert in the order of their index t * topk + j.
+ *   offsets: [E + 1], expert e has the rows offsets[e] .. offsets[e + 1] - 1.
+ *   order: [T * topk], the slot of each row, -1 behind the last row.
+ *   pos: [T][topk], the row of each slot, -1 for an id outside [0, E).
+ *   1 <= E <= 1024, 1 <= topk <= 32, T * topk <= 2^30; all dense int32.  T == 0
+ *   writes offsets only.  ws: ttq_moe_sort_workspace_bytes(T, topk, E) bytes,
+ *   256-byte aligned (0 and NULL for few slots).
+ */
+ttq_status ttq_moe_sort(const int32_t* ids, int64_t T, int64_t topk, int64_t E, int32_t* offsets, int32_t* order,
+                        int32_t* pos, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes for ttq_moe_sort (0 also for sizes it does not accept). */
+size_t ttq_moe_sort_workspace_bytes(int64_t T, int64_t topk, int64_t E);
+
+/*
+ * ttq_moe_gather — R[pos[t][j]] = X[t], the tokens' rows in their experts' order.
+ *   X: [T][K] (xt), stride ldx; R: [rows][K] of the same dtype, stride ldr.  A
+ *   slot whose pos is outside [0, rows) has no row; rows that no slot names are
+ *   left as they were; no two slots may name one row.  K positive, any.  R
+ *   16-byte aligned, its row stride a multiple of 16 bytes, no overlap with X.
+ *   The gradient of X is ttq_moe_combine of R's gradient with w NULL.
+ *   T == 0 or rows == 0 is an empty call.  No workspace.
+ */
+ttq_status ttq_moe_gather(const void* X, int xt, int64_t T, int64_t K, int64_t ldx, const int32_t* pos, int64_t topk,
+                          void* R, int64_t rows, int64_t ldr, void* stream);
+
+/*
+ * ttq_moe_combine — Y[t] = sum_j w[t][j] R[pos[t][j]], the experts' rows back in
+ * the tokens' order.
+ *   R: [rows][M] (rt), stride ldr.  w: [T][topk] fp32, or NULL for ones.  A slot
+ *   whose pos is outside [0, rows) adds nothing (its weight is not read); a
+ *   token without any gets zeros.  In fp32 in the order of j, rounded once to Y
+ *   [T][M] (yt), overwritten.  M any.  T == 0 or M == 0 is an empty call.
+ */
+ttq_status ttq_moe_combine(const void* R, int rt, int64_t rows, int64_t ldr, const int32_t* pos, const float* w,
+                           int64_t T, int64_t topk, int64_t M, void* Y, int yt, int64_t ldy, void* stream);
+
+/*
+ * ttq_moe_combine_grad — the gradient of ttq_moe_combine:
+ *   dR[pos[t][j]] = w[t][j] dY[t] (rounded to rt; rows that no slot names are
+ *   left as they were; no two slots may name one row),
+ *   dw[t][j] = sum_o dY[t][o] R[pos[t][j]][o] in fp32 (0 for a slot without a
+ *   row), reproducible run to run.
+ *   dY: [T][M] (yt), stride lddy; dR: [rows][M] of R's dtype rt, stride lddr,
+ *   16-byte aligned, its row stride a multiple of 16 bytes; dw: [T][topk].  dR or
+ *   dw may be NULL (R may be, too, without dw).  dR must not overlap R or dY.
+ *   T == 0 is an empty call.
+ */
+ttq_status ttq_moe_combine_grad(const void* dY, int yt, int64_t T, int64_t M, int64_t lddy, const void* R, int rt,
+                                int64_t rows, int64_t ldr, const int32_t* pos, const float* w, int64_t topk,
+                                void* dR, int64_t lddr, float* dw, void* stream);
+
+/* 8-bit weights of E experts of equal shape: codes [E][rows][K] and scale
+ * [E][rows], dense, as ttq_quantize_rows writes them for the weight times s;
+ * expert e is scaled by s + e * s_stride (s_stride 0: one s for all; else a
+ * multiple of 4, at least K). */
+typedef struct ttq_expert_i8 {
+    const float* s;  int64_t s_stride;
+    const int8_t* codes;  const float* scale;
+} ttq_expert_i8;
+
+/*
+ * ttq_moe_i8 — ttq_moe on 8-bit experts, for any number of tokens.
+ *   Y[t] = sum_j w[t][j] D_e q(h),  h = act(g) * u / s_down,
+ *   [g; u] = G_e q(X[t] / s_in),  e = ids[t][j],
+ *   q(.) the row in 8 bits (ttq_quantize_rows), products as in ttq_gemm_i8; h
+ *   and the sum over j in fp32, Y rounded once.  ids, w, act, X, Y as for
+ *   ttq_moe: a slot whose id is not in [0, E) adds nothing, a token without any
+ *   gets zeros, an expert named twice counts twice; an infinite or NaN x / s or
+ *   h makes its token's outputs NaN and no other's.  A token's results do not
+ *   depend on the other tokens of the call.
+ *   K and I multiples of 16, at most 2^17; E <= 1024; 1 <= topk <= 32.  An
+ *   expert's gate_up or down codes of 2 GiB or more, T * topk > 2^24 or
+ *   T * topk * K >= 2^31 return TTQ_ERR_UNSUPPORTED.  T == 0 or M == 0 is an
+ *   empty call.
+ *   ws: ttq_moe_i8_workspace_bytes(T, topk, K, I, M, E) bytes, 256-byte aligned;
+ *   calls that may run at the same time need workspaces of their own.
+ */
+typedef struct ttq_moe_i8_args {
+    const void* X;  int xt;  int64_t T;  int64_t K;  int64_t ldx;
+    const int32_t* ids;  const float* w;  int64_t topk;
+    int64_t E;  int64_t I;  int64_t M;
+    ttq_expert_i8 gate_up;  ttq_expert_i8 down;
+    int act;
+    void* Y;  int yt;  int64_t ldy;
+} ttq_moe_i8_args;
+
+ttq_status ttq_moe_i8(const ttq_moe_i8_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes for ttq_moe_i8 (0 for sizes it does not accept). */
+size_t ttq_moe_i8_workspace_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E);
+
 /* Static text for a status code. */
 const char* ttq_status_str(int status);
 

@@ -20,7 +20,8 @@ OUT = os.path.join(PKG, "libttq.so")
 BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["stats.hip", "quantize.hip", "quantize_lr.hip", "qgemm.hip", "qgemv.hip", "qgemv_gs.hip", "gemm_bf16.hip", "lowrank.hip", "factors.hip",
-           "route.hip", "adapters.hip", "moe.hip", "moe_mfma.hip", "moe_dot.hip", "noalloc.hip", "ttq_api.cpp"]
+           "route.hip", "adapters.hip", "moe.hip", "moe_mfma.hip", "moe_dot.hip", "rows_i8.hip", "gemm_i8.hip", "sort.hip",
+           "moe_i8.hip", "noalloc.hip", "ttq_api.cpp"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -187,6 +187,73 @@ hipError_t launch_adapters(const void* X, bool xf32, int64_t T, int64_t K, int64
                            const ProjectionIn& c, int64_t M, void* Y, bool yf32, int64_t ldy, float* Z,
                            hipStream_t st);
 
+// Rows in 8 bits (rows_i8.hip): codes [R][K] with row stride ldc, scale [R].
+struct I8RowsArgs {
+    const void* X;
+    bool xf32;
+    int64_t ldx;
+    int64_t R, K;
+    const float* s;             // nullptr: v = x
+    bool divide;                // v = x / s, else x s
+    int8_t* codes;
+    int64_t ldc;
+    float* scale;
+    // Rows sorted by expert: at most R, *nrows of them; row r is that of X of
+    // slot order[r] (token order[r] / topk), with s + ids[slot] * s_stride
+    // (ids nullptr: one s).
+    const int32_t* nrows = nullptr;
+    const int32_t* order = nullptr;
+    int topk = 1;
+    const int32_t* ids = nullptr;
+    int64_t s_stride = 0;
+};
+hipError_t launch_quantize_rows(const I8RowsArgs& a, hipStream_t st);
+
+// Products of 8-bit codes (gemm_i8.hip).
+struct I8Product {
+    const int8_t* X;
+    int64_t ldx;
+    const float* x_scale;
+    int64_t T, K;
+    const int8_t* W;            // [M][K], with s_down [2 M][K]
+    int64_t ldw;
+    const float* w_scale;
+    int64_t M;
+    void* Y;
+    int64_t ldy;
+    // Rows sorted by expert: row r of Y is the product of row order[r] / topk of
+    // X (order nullptr: row r) and, for offsets[e] <= r < offsets[e + 1], of
+    // matrix e, w_stride codes behind the one before; T is at least offsets[E].
+    const int32_t* offsets = nullptr;
+    const int32_t* order = nullptr;
+    int topk = 1, E = 1;
+    int64_t w_stride = 0;
+    // Gate and up: Y (fp32) is act(g) u / s_down[e * s_stride + o].
+    const float* s_down = nullptr;
+    int64_t s_stride = 0;
+    int act = 0;
+    int yvec = 0;               // set by the launch
+};
+size_t i8_product_ws_bytes(int64_t T, int64_t K, int64_t M);
+bool i8_product_fits(int64_t T, int64_t M);       // a grid can cover T x M
+hipError_t launch_i8_product(const I8Product& p, bool yf32, void* ws, hipStream_t st);
+
+// Tokens sorted by expert and back (sort.hip).
+size_t moe_sort_ws_bytes(int64_t n, int64_t E);
+hipError_t launch_moe_sort(const int32_t* ids, int64_t n, int E, int32_t* offsets, int32_t* order, int32_t* pos,
+                           int32_t* ws, hipStream_t st);
+hipError_t launch_moe_gather(const void* X, int es, int64_t T, int64_t K, int64_t ldx, const int32_t* pos, int topk,
+                             void* R, int64_t rows, int64_t ldr, hipStream_t st);
+hipError_t launch_moe_combine(const void* R, bool rf32, int64_t rows, int64_t ldr, const int32_t* pos, const float* w,
+                              int64_t T, int topk, int64_t M, void* Y, bool yf32, int64_t ldy, hipStream_t st);
+hipError_t launch_moe_combine_grad(const void* dY, bool yf32, int64_t lddy, const void* R, bool rf32, int64_t rows,
+                                   int64_t ldr, const int32_t* pos, const float* w, int64_t T, int topk, int64_t M,
+                                   void* dR, int64_t lddr, float* dw, hipStream_t st);
+
+// Mixture-of-experts layer in 8-bit integers (moe_i8.hip).
+size_t moe_i8_ws_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E);
+hipError_t launch_moe_i8(const ttq_moe_i8_args* a, char* ws, hipStream_t st);
+
 // ttq_linear's argument checks (clearing the calling thread's error text
 // first) and the workspace bytes the call needs (0 for an empty call).
 ttq_status linear_check(const ttq_linear_args* a, size_t* need);

@@ -1,0 +1,345 @@
+// Tokens sorted by expert, their rows copied in that order, and the way back.
+//
+// Sort: slots (token, j) by the expert ids[t][j], stably, so that every result
+// is the same each time; a slot whose id names no expert has no row.
+//   offsets[e]: rows of the experts before e;  order[r]: row r's slot;
+//   pos[slot]: its row.
+// A workgroup owns consecutive slots and each of its 16 waves a run of them.
+// Per 64 slots the lanes of equal experts are found by a ballot per bit of the
+// id, so that a wave counts without atomics: the first such lane adds their
+// number.  Counts of waves (in LDS) and of workgroups (in memory, by a launch
+// of its own where there are several) become the places where their slots of
+// each expert begin.
+//
+// Rows are copied (gather), added (combine) and differentiated (combine_grad)
+// by token, through pos: a token's row is read or written once for all of its
+// slots, in whole vectors of 16 bytes.
+#include <algorithm>
+
+#include "common.hpp"
+#include "launch.hpp"
+#include "lds_dma.hpp"
+#include "wave.hpp"
+
+namespace ttq {
+
+constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
+constexpr int64_t kSortMaxBlocks = 256;
+
+// Slots per workgroup and workgroups for n slots.
+static int64_t sort_span(int64_t n) {
+    const int64_t per = (n + kSortMaxBlocks - 1) / kSortMaxBlocks;
+    return std::max<int64_t>((per + kSortThreads - 1) / kSortThreads, 1) * kSortThreads;
+}
+static int64_t sort_blocks(int64_t n) { return std::max<int64_t>((n + sort_span(n) - 1) / sort_span(n), 1); }
+
+size_t moe_sort_ws_bytes(int64_t n, int64_t E) {
+    return sort_blocks(n) > 1 ? (size_t)(sort_blocks(n) * E) * 4 : 0;
+}
+
+// The lanes whose key equals this lane's; `bits` bits of it count.
+__device__ __forceinline__ uint64_t same_lanes(int key, int bits) {
+    uint64_t m = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const bool one = (key >> b) & 1;
+        const uint64_t w = __ballot(one);
+        m &= one ? w : ~w;
+    }
+    return m;
+}
+
+// Counts [blocks][E] of each workgroup's slots.
+template <bool PLACE>
+__global__ __launch_bounds__(kSortThreads) void k_moe_sort(const int32_t* __restrict__ ids, int64_t n, int E, int bits,
+                                                           int64_t span, int32_t* __restrict__ counts,
+                                                           int32_t* __restrict__ offsets, int32_t* __restrict__ order,
+                                                           int32_t* __restrict__ pos) {
+    __shared__ int32_t place[kSortWaves][kMoeMaxExperts];
+    __shared__ int32_t wsum[kSortWaves];
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
+    const int64_t first = blockIdx.x * span;
+    const int64_t w0 = first + wave * (span / kSortWaves), w1 = min(w0 + span / kSortWaves, n);
+    for (int e = lane; e < E; e += kWave) place[wave][e] = 0;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    auto key_at = [&](int64_t i) __attribute__((always_inline)) {
+        const int id = i < w1 ? ids[i] : -1;
+        return id >= 0 && id < E ? id : E;        // E: no expert
+    };
+    // A wave alone touches its counts, and its LDS accesses are in order: between
+    // its rounds only the compiler is held to that.
+    for (int64_t i = w0; i < w1; i += kWave) {
+        const int key = key_at(i + lane);
+        const uint64_t m = same_lanes(key, bits);
+        if (key < E && lane == __builtin_ctzll(m)) place[wave][key] += __builtin_popcountll(m);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    __syncthreads();
+    if constexpr (!PLACE) {
+        for (int e = tid; e < E; e += kSortThreads) {
+            int c = 0;
+            for (int w = 0; w < kSortWaves; ++w) c += place[w][e];
+            counts[(int64_t)blockIdx.x * E + e] = c;
+        }
+        return;
+    }
+    // Thread e: slots of expert e in all and before this workgroup, then the
+    // experts' first rows by a scan over the threads.
+    int all = 0, mine = 0;
+    if (tid < E) {
+        if (gridDim.x == 1) {
+            for (int w = 0; w < kSortWaves; ++w) all += place[w][tid];
+        } else {
+            for (int b = 0; b < (int)gridDim.x; ++b) {
+                const int c = counts[(int64_t)b * E + tid];
+                if (b < (int)blockIdx.x) mine += c;
+                all += c;
+            }
+        }
+    }
+    int sum = all;
+#pragma unroll
+    for (int s = 1; s < kWave; s <<= 1) {
+        const int u = __shfl_up(sum, s);
+        if (lane >= s) sum += u;
+    }
+    if (lane == kWave - 1) wsum[wave] = sum;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+        if (w < wave) before += wsum[w];
+        total += wsum[w];
+    }
+    if (tid < E) {
+        const int lo = before + sum - all;
+        if (blockIdx.x == 0) {
+            offsets[tid] = lo;
+            if (tid == 0) offsets[E] = total;
+        }
+        int at = lo + mine;
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int c = place[w][tid];
+            place[w][tid] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    for (int64_t i = w0; i < w1; i += kWave) {
+        const int key = key_at(i + lane);
+        const uint64_t m = same_lanes(key, bits);
+        const int rank = __builtin_popcountll(m & ((1ull << lane) - 1));
+        int r = -1;
+        if (key < E) {
+            r = place[wave][key] + rank;
+            order[r] = (int32_t)(i + lane);
+        }
+        if (i + lane < w1) pos[i + lane] = r;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (key < E && rank == 0) place[wave][key] += __builtin_popcountll(m);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    // Behind the last row there is no slot.
+    const int64_t end = min(first + span, n);
+    for (int64_t r = max(first, (int64_t)total) + tid; r < end; r += kSortThreads) order[r] = -1;
+}
+
+hipError_t launch_moe_sort(const int32_t* ids, int64_t n, int E, int32_t* offsets, int32_t* order, int32_t* pos,
+                           int32_t* ws, hipStream_t st) {
+    const int64_t span = sort_span(n);
+    const dim3 grid((unsigned)sort_blocks(n)), block(kSortThreads);
+    int bits = 1;
+    while ((1 << bits) <= E) ++bits;              // keys 0 .. E
+    if (grid.x > 1) {
+        const hipError_t e = launch_kernel(k_moe_sort<false>, grid, block, 0, st, nullptr, nullptr, ids, n, E, bits, span, ws,
+                                           offsets, order, pos);
+        if (e != hipSuccess) return e;
+    }
+    return launch_kernel(k_moe_sort<true>, grid, block, 0, st, nullptr, nullptr, ids, n, E, bits, span, ws, offsets, order,
+                         pos);
+}
+
+// ------------------------------------------------------------------ rows
+
+constexpr int kMoveThreads = 256;
+
+// One row piece of 16 bytes, or its `n` elements of ES bytes at the row's end.
+template <int ES>
+__device__ __forceinline__ u32x4 load_piece(const char* p, int n) {
+    u32x4 v = {0, 0, 0, 0};
+    if (n >= 16 / ES) return *(const u32x4*)p;
+    if constexpr (ES == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) v[i] = ((const uint32_t*)p)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) v[i / 2] |= (uint32_t)((const uint16_t*)p)[i] << (16 * (i & 1));
+    }
+    return v;
+}
+template <int ES>
+__device__ __forceinline__ void store_piece(char* p, int n, const u32x4& v) {
+    if (n >= 16 / ES) {
+        *(u32x4*)p = v;
+    } else if constexpr (ES == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) ((uint32_t*)p)[i] = v[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) ((uint16_t*)p)[i] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+template <int ES>
+__global__ __launch_bounds__(kMoveThreads) void k_moe_gather(const char* __restrict__ X, int64_t T, int64_t K,
+                                                             int64_t ldx, const int32_t* __restrict__ pos, int topk,
+                                                             char* __restrict__ R, int64_t rows, int64_t ldr) {
+    constexpr int V = 16 / ES;
+    const int64_t pieces = (K + V - 1) / V, all = T * pieces;
+    for (int64_t i = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; i < all; i += (int64_t)gridDim.x * kMoveThreads) {
+        const int64_t t = i / pieces, k = (i - t * pieces) * V;
+        const int n = (int)min(K - k, (int64_t)V);
+        const u32x4 v = load_piece<ES>(X + (t * ldx + k) * ES, n);
+        for (int j = 0; j < topk; ++j) {
+            const int64_t r = pos[t * topk + j];
+            if (r >= 0 && r < rows) store_piece<ES>(R + (r * ldr + k) * ES, n, v);
+        }
+    }
+}
+
+hipError_t launch_moe_gather(const void* X, int es, int64_t T, int64_t K, int64_t ldx, const int32_t* pos, int topk,
+                             void* R, int64_t rows, int64_t ldr, hipStream_t st) {
+    const int64_t pieces = (K * es + 15) / 16;
+    const dim3 grid((unsigned)std::min<int64_t>((T * pieces + kMoveThreads - 1) / kMoveThreads, 1 << 20));
+    return es == 4 ? launch_kernel(k_moe_gather<4>, grid, dim3(kMoveThreads), 0, st, nullptr, nullptr, (const char*)X, T, K,
+                                   ldx, pos, topk, (char*)R, rows, ldr)
+                   : launch_kernel(k_moe_gather<2>, grid, dim3(kMoveThreads), 0, st, nullptr, nullptr, (const char*)X, T, K,
+                                   ldx, pos, topk, (char*)R, rows, ldr);
+}
+
+// Four values of a row from index k on, `n` of them there.
+template <bool F32>
+__device__ __forceinline__ f32x4 load4(const void* p, int64_t at, int n, bool vec) {
+    f32x4 f = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (F32) {
+        const float* q = (const float*)p + at;
+        if (vec && n >= 4) return *(const f32x4*)q;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) f[i] = q[i];
+    } else {
+        const uint16_t* q = (const uint16_t*)p + at;
+        if (vec && n >= 4) {
+            const u32x2 u = *(const u32x2*)q;
+            return f32x4{bf16lo_to_f32(u[0]), bf16hi_to_f32(u[0]), bf16lo_to_f32(u[1]), bf16hi_to_f32(u[1])};
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) f[i] = bf16_to_f32(q[i]);
+    }
+    return f;
+}
+
+template <bool RF32, bool YF32>
+__global__ __launch_bounds__(kMoveThreads) void k_moe_combine(const void* __restrict__ R, int64_t rows, int64_t ldr,
+                                                              const int32_t* __restrict__ pos,
+                                                              const float* __restrict__ w, int64_t T, int topk,
+                                                              int64_t M, void* __restrict__ Y, int64_t ldy, int yvec) {
+    const int64_t quads = (M + 3) / 4, all = T * quads;
+    for (int64_t i = (int64_t)blockIdx.x * kMoveThreads + threadIdx.x; i < all; i += (int64_t)gridDim.x * kMoveThreads) {
+        const int64_t t = i / quads, k = (i - t * quads) * 4;
+        const int n = (int)min(M - k, (int64_t)4);
+        f32x4 y = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < topk; ++j) {
+            const int64_t r = pos[t * topk + j];
+            if (r < 0 || r >= rows) continue;
+            const float f = w ? w[t * topk + j] : 1.f;
+            const f32x4 v = load4<RF32>(R, r * ldr + k, n, true);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[c] = __builtin_fmaf(f, v[c], y[c]);
+        }
+        store_y4<YF32>(Y, t * ldy + k, n, yvec, y);
+    }
+}
+
+hipError_t launch_moe_combine(const void* R, bool rf32, int64_t rows, int64_t ldr, const int32_t* pos, const float* w,
+                              int64_t T, int topk, int64_t M, void* Y, bool yf32, int64_t ldy, hipStream_t st) {
+    const int64_t quads = (M + 3) / 4;
+    const int yvec = (uintptr_t)Y % 16 == 0 && ldy * (yf32 ? 4 : 2) % 16 == 0;
+    const dim3 grid((unsigned)std::min<int64_t>((T * quads + kMoveThreads - 1) / kMoveThreads, 1 << 20)),
+        block(kMoveThreads);
+#define TTQ_COMBINE(RF, YF) \
+    return launch_kernel(k_moe_combine<RF, YF>, grid, block, 0, st, nullptr, nullptr, R, rows, ldr, pos, w, T, topk, M, Y, ldy, yvec)
+    if (rf32) {
+        if (yf32) TTQ_COMBINE(true, true);
+        TTQ_COMBINE(true, false);
+    }
+    if (yf32) TTQ_COMBINE(false, true);
+    TTQ_COMBINE(false, false);
+#undef TTQ_COMBINE
+}
+
+// A workgroup per token: for each slot dR's row and dw, the token's row of dY
+// read again for each (from the cache).  dw: a lane's products in order of
+// their columns, then the wave's and the waves' sums in a fixed order, in fp32.
+template <bool YF32, bool RF32>
+__global__ __launch_bounds__(kMoveThreads) void k_moe_combine_grad(const void* __restrict__ dY, int64_t lddy,
+                                                                   const void* __restrict__ R, int64_t rows,
+                                                                   int64_t ldr, const int32_t* __restrict__ pos,
+                                                                   const float* __restrict__ w, int64_t T, int topk,
+                                                                   int64_t M, void* __restrict__ dR, int64_t lddr,
+                                                                   float* __restrict__ dw) {
+    __shared__ float part[kMoveThreads / kWave];
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+        for (int j = 0; j < topk; ++j) {
+            const int64_t r = pos[t * topk + j];
+            const bool have = r >= 0 && r < rows;
+            float dot = 0.f;
+            if (have) {
+                const float f = w ? w[t * topk + j] : 1.f;
+                for (int64_t k = 4 * threadIdx.x; k < M; k += 4 * kMoveThreads) {
+                    const int n = (int)min(M - k, (int64_t)4);
+                    const f32x4 g = load4<YF32>(dY, t * lddy + k, n, true);
+                    if (dw) {
+                        const f32x4 v = load4<RF32>(R, r * ldr + k, n, true);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            if (c < n) dot = __builtin_fmaf(g[c], v[c], dot);
+                    }
+                    if (dR) store_y4<RF32>(dR, r * lddr + k, n, true, f32x4{f * g[0], f * g[1], f * g[2], f * g[3]});
+                }
+            }
+            if (dw) {
+                dot = wave_sum(dot);
+                if ((threadIdx.x & (kWave - 1)) == 0) part[threadIdx.x / kWave] = dot;
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    float s = 0.f;
+                    for (int v = 0; v < kMoveThreads / kWave; ++v) s += part[v];
+                    dw[t * topk + j] = have ? s : 0.f;
+                }
+                __syncthreads();
+            }
+        }
+    }
+}
+
+hipError_t launch_moe_combine_grad(const void* dY, bool yf32, int64_t lddy, const void* R, bool rf32, int64_t rows,
+                                   int64_t ldr, const int32_t* pos, const float* w, int64_t T, int topk, int64_t M,
+                                   void* dR, int64_t lddr, float* dw, hipStream_t st) {
+    const dim3 grid((unsigned)std::min<int64_t>(T, 1 << 20)), block(kMoveThreads);
+#define TTQ_GRAD(YF, RF)                                                                                             \
+    return launch_kernel(k_moe_combine_grad<YF, RF>, grid, block, 0, st, nullptr, nullptr, dY, lddy, R, rows, ldr, pos, w, T, \
+                         topk, M, dR, lddr, dw)
+    if (yf32) {
+        if (rf32) TTQ_GRAD(true, true);
+        TTQ_GRAD(true, false);
+    }
+    if (rf32) TTQ_GRAD(false, true);
+    TTQ_GRAD(false, false);
+#undef TTQ_GRAD
+}
+
+}  // namespace ttq

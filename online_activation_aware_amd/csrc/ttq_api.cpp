@@ -756,3 +756,248 @@ ttq_status ttq_qgemm_adapters(const void* X, int xt, int64_t T, int64_t K, int64
 }
 
 }  // extern "C"
+
+// ------------------------------------------- 8-bit integers, sorted tokens
+
+namespace {
+
+constexpr int64_t kMaxKI8 = (int64_t)1 << 17;     // 127^2 K fits in int32
+constexpr int64_t kMaxLdI8 = (int64_t)1 << 22;    // 256 rows lie within one buffer descriptor
+constexpr int64_t kMaxSlots = (int64_t)1 << 30;
+constexpr int64_t kMaxMoeI8Slots = (int64_t)1 << 24;
+
+ttq_status check_k_i8(const char* name, int64_t K) {
+    TTQ_REQUIRE(K > 0 && K <= kMaxKI8 && K % 16 == 0, "%s must be a positive multiple of 16, at most 2^17", name);
+    return TTQ_OK;
+}
+
+ttq_status check_codes(const char* name, const void* p, int64_t rows, int64_t K, int64_t ld) {
+    TTQ_REQUIRE(ld >= K && ld <= kMaxDim && ld % 16 == 0,
+                "%s: row stride %lld is below the row length or not a multiple of 16", name, (long long)ld);
+    TTQ_REQUIRE(rows == 0 || (p != nullptr && aligned(p, 16)), "%s: null or not 16-byte aligned", name);
+    return TTQ_OK;
+}
+
+ttq_status check_floats(const char* name, const void* p) {
+    TTQ_REQUIRE(p != nullptr && aligned(p, 4), "%s: null or misaligned", name);
+    return TTQ_OK;
+}
+
+// The product's arguments (X is checked by the caller).
+ttq_status check_product_i8(int64_t T, int64_t K, int64_t M, const int8_t* W, const float* w_scale, int64_t ldw,
+                            const void* Y, int yt, int64_t ldy) {
+    TTQ_REQUIRE(dim_ok(T) && dim_ok(M), "T or M out of range");
+    if (ttq_status e = check_k_i8("K", K)) return e;
+    if (ttq_status e = check_codes("W", W, T == 0 ? 0 : M, K, ldw)) return e;
+    if (ttq_status e = check_output(Y, yt, T, M, ldy)) return e;
+    if (T > 0 && M > 0)
+        if (ttq_status e = check_floats("w_scale", w_scale)) return e;
+    if (ldw > kMaxLdI8) return fail(TTQ_ERR_UNSUPPORTED, "W: row stride above 2^22");
+    if (!ttq::i8_product_fits(T, M)) return fail(TTQ_ERR_UNSUPPORTED, "T x M is beyond one launch");
+    return TTQ_OK;
+}
+
+size_t ws_qgemm_i8_codes(int64_t T, int64_t K) { return round_up((size_t)T * K); }
+size_t ws_qgemm_i8_head(int64_t T, int64_t K) { return ws_qgemm_i8_codes(T, K) + round_up((size_t)T * 4); }
+
+ttq_status check_rows_moe(const char* name, const void* p, int t, int64_t rows, int64_t K, int64_t ld) {
+    TTQ_REQUIRE(dim_ok(rows), "rows out of range");
+    return check_matrix(name, p, t, rows, K, ld);
+}
+
+ttq_status check_slots(int64_t T, int64_t topk) {
+    TTQ_REQUIRE(dim_ok(T), "T out of range");
+    TTQ_REQUIRE(topk >= 1 && topk <= ttq::kRouteMaxTopk, "topk must be in [1, %d]", ttq::kRouteMaxTopk);
+    TTQ_REQUIRE(T * topk <= kMaxSlots, "T * topk above 2^30");
+    return TTQ_OK;
+}
+
+ttq_status check_ints(const char* name, const void* p) {
+    TTQ_REQUIRE(p != nullptr && aligned(p, 4), "%s: null or misaligned", name);
+    return TTQ_OK;
+}
+
+ttq_status check_experts_i8(const char* name, const ttq_expert_i8& q, int64_t K) {
+    TTQ_REQUIRE(q.s != nullptr && aligned(q.s, 16), "%s.s: null or not 16-byte aligned", name);
+    TTQ_REQUIRE(q.s_stride == 0 || (q.s_stride >= K && q.s_stride % 4 == 0 && q.s_stride <= kMaxDim),
+                "%s.s_stride: neither 0 nor a multiple of 4 of at least the row length", name);
+    TTQ_REQUIRE(q.codes != nullptr && aligned(q.codes, 16), "%s.codes: null or not 16-byte aligned", name);
+    TTQ_REQUIRE(q.scale != nullptr && aligned(q.scale, 4), "%s.scale: null or misaligned", name);
+    return TTQ_OK;
+}
+
+ttq_status check_moe_i8_sizes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E) {
+    if (ttq_status e = check_slots(T, topk)) return e;
+    TTQ_REQUIRE(E >= 1 && E <= ttq::kMoeMaxExperts, "E (experts) must be in [1, %d]", ttq::kMoeMaxExperts);
+    TTQ_REQUIRE(dim_ok(M), "M out of range");
+    if (ttq_status e = check_k_i8("K", K)) return e;
+    if (ttq_status e = check_k_i8("I", I)) return e;
+    if (2 * I * K >= kMaxExpertBytes || M * I >= kMaxExpertBytes)
+        return fail(TTQ_ERR_UNSUPPORTED, "an expert's codes take 2 GiB or more");
+    if (T * topk > kMaxMoeI8Slots || T * topk * K >= kMaxExpertBytes)
+        return fail(TTQ_ERR_UNSUPPORTED, "more than 2^24 slots, or 2 GiB of their codes: pass the tokens in chunks");
+    if (!ttq::i8_product_fits(T * topk + E * 256, I > M ? I : M))
+        return fail(TTQ_ERR_UNSUPPORTED, "slots x channels is beyond one launch");
+    return TTQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ttq_status ttq_quantize_rows(const void* X, int xt, int64_t R, int64_t K, int64_t ldx, const float* s, int divide,
+                             int8_t* codes, int64_t ldc, float* scale, void* stream) {
+    g_last_error.clear();
+    TTQ_REQUIRE(dim_ok(R), "R out of range");
+    if (ttq_status e = check_k_i8("K", K)) return e;
+    if (ttq_status e = check_matrix("X", X, xt, R, K, ldx)) return e;
+    TTQ_REQUIRE(aligned(s, 16), "s: pointer not 16-byte aligned");
+    if (ttq_status e = check_codes("codes", codes, R, K, ldc)) return e;
+    if (R == 0) return TTQ_OK;
+    if (ttq_status e = check_floats("scale", scale)) return e;
+    return device_status(ttq::launch_quantize_rows({X, xt == TTQ_F32, ldx, R, K, s, divide != 0, codes, ldc, scale},
+                                                   as_stream(stream)),
+                         "ttq_quantize_rows launch");
+}
+
+size_t ttq_gemm_i8_workspace_bytes(int64_t T, int64_t K, int64_t M) {
+    if (!dim_ok(T) || !dim_ok(M) || K <= 0 || K > kMaxKI8 || K % 16 || !ttq::i8_product_fits(T, M)) return 0;
+    return round_up(ttq::i8_product_ws_bytes(T, K, M)) + kAlign;
+}
+
+ttq_status ttq_gemm_i8(const int8_t* X, const float* x_scale, int64_t T, int64_t K, int64_t ldx, const int8_t* W,
+                       const float* w_scale, int64_t M, int64_t ldw, void* Y, int yt, int64_t ldy, void* ws,
+                       size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    if (ttq_status e = check_product_i8(T, K, M, W, w_scale, ldw, Y, yt, ldy)) return e;
+    if (ttq_status e = check_codes("X", X, M == 0 ? 0 : T, K, ldx)) return e;
+    if (ldx > kMaxLdI8) return fail(TTQ_ERR_UNSUPPORTED, "X: row stride above 2^22");
+    if (T == 0 || M == 0) return TTQ_OK;
+    if (ttq_status e = check_floats("x_scale", x_scale)) return e;
+    if (ttq_status e = check_ws(ws, ws_bytes, ttq_gemm_i8_workspace_bytes(T, K, M))) return e;
+    return device_status(ttq::launch_i8_product({X, ldx, x_scale, T, K, W, ldw, w_scale, M, Y, ldy}, yt == TTQ_F32, ws,
+                                                as_stream(stream)),
+                         "ttq_gemm_i8 launch");
+}
+
+size_t ttq_qgemm_i8_workspace_bytes(int64_t T, int64_t K, int64_t M) {
+    const size_t n = ttq_gemm_i8_workspace_bytes(T, K, M);
+    return n == 0 ? 0 : ws_qgemm_i8_head(T, K) + n;
+}
+
+ttq_status ttq_qgemm_i8(const void* X, int xt, int64_t T, int64_t K, int64_t ldx, const float* s, const int8_t* W,
+                        const float* w_scale, int64_t M, int64_t ldw, void* Y, int yt, int64_t ldy, void* ws,
+                        size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    if (ttq_status e = check_product_i8(T, K, M, W, w_scale, ldw, Y, yt, ldy)) return e;
+    if (ttq_status e = check_matrix("X", X, xt, M == 0 ? 0 : T, K, ldx)) return e;
+    TTQ_REQUIRE(aligned(s, 16), "s: pointer not 16-byte aligned");
+    if (T == 0 || M == 0) return TTQ_OK;
+    if (ttq_status e = check_ws(ws, ws_bytes, ttq_qgemm_i8_workspace_bytes(T, K, M))) return e;
+    char* w = (char*)ws;
+    int8_t* q = (int8_t*)w;
+    float* qs = (float*)(w + ws_qgemm_i8_codes(T, K));
+    hipStream_t st = as_stream(stream);
+    if (ttq_status e = device_status(ttq::launch_quantize_rows({X, xt == TTQ_F32, ldx, T, K, s, true, q, K, qs}, st),
+                                     "ttq_qgemm_i8 launch"))
+        return e;
+    return device_status(ttq::launch_i8_product({q, K, qs, T, K, W, ldw, w_scale, M, Y, ldy}, yt == TTQ_F32,
+                                                w + ws_qgemm_i8_head(T, K), st),
+                         "ttq_qgemm_i8 launch");
+}
+
+size_t ttq_moe_sort_workspace_bytes(int64_t T, int64_t topk, int64_t E) {
+    if (!dim_ok(T) || topk < 1 || topk > ttq::kRouteMaxTopk || T * topk > kMaxSlots || E < 1 || E > ttq::kMoeMaxExperts)
+        return 0;
+    return round_up(ttq::moe_sort_ws_bytes(T * topk, E));
+}
+
+ttq_status ttq_moe_sort(const int32_t* ids, int64_t T, int64_t topk, int64_t E, int32_t* offsets, int32_t* order,
+                        int32_t* pos, void* ws, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    if (ttq_status e = check_slots(T, topk)) return e;
+    TTQ_REQUIRE(E >= 1 && E <= ttq::kMoeMaxExperts, "E (experts) must be in [1, %d]", ttq::kMoeMaxExperts);
+    if (ttq_status e = check_ints("offsets", offsets)) return e;
+    if (T > 0) {
+        if (ttq_status e = check_ints("ids", ids)) return e;
+        if (ttq_status e = check_ints("order", order)) return e;
+        if (ttq_status e = check_ints("pos", pos)) return e;
+        if (ttq_status e = check_ws(ws, ws_bytes, ttq_moe_sort_workspace_bytes(T, topk, E))) return e;
+    }
+    return device_status(ttq::launch_moe_sort(ids, T * topk, (int)E, offsets, order, pos, (int32_t*)ws, as_stream(stream)),
+                         "ttq_moe_sort launch");
+}
+
+ttq_status ttq_moe_gather(const void* X, int xt, int64_t T, int64_t K, int64_t ldx, const int32_t* pos, int64_t topk,
+                          void* R, int64_t rows, int64_t ldr, void* stream) {
+    g_last_error.clear();
+    if (ttq_status e = check_slots(T, topk)) return e;
+    TTQ_REQUIRE(K > 0 && K <= kMaxDim, "K out of range");
+    if (ttq_status e = check_matrix("X", X, xt, T, K, ldx)) return e;
+    if (ttq_status e = check_rows_moe("R", R, xt, T == 0 ? 0 : rows, K, ldr)) return e;
+    if (T == 0 || rows == 0) return TTQ_OK;
+    if (ttq_status e = check_ints("pos", pos)) return e;
+    return device_status(ttq::launch_moe_gather(X, (int)esize(xt), T, K, ldx, pos, (int)topk, R, rows, ldr,
+                                                as_stream(stream)),
+                         "ttq_moe_gather launch");
+}
+
+ttq_status ttq_moe_combine(const void* R, int rt, int64_t rows, int64_t ldr, const int32_t* pos, const float* w,
+                           int64_t T, int64_t topk, int64_t M, void* Y, int yt, int64_t ldy, void* stream) {
+    g_last_error.clear();
+    if (ttq_status e = check_slots(T, topk)) return e;
+    TTQ_REQUIRE(dim_ok(M), "M out of range");
+    if (ttq_status e = check_rows_moe("R", R, rt, T == 0 || M == 0 ? 0 : rows, M, ldr)) return e;
+    if (ttq_status e = check_output(Y, yt, T, M, ldy)) return e;
+    if (T == 0 || M == 0) return TTQ_OK;
+    if (ttq_status e = check_ints("pos", pos)) return e;
+    TTQ_REQUIRE(aligned(w, 4), "w: misaligned");
+    return device_status(ttq::launch_moe_combine(R, rt == TTQ_F32, rows, ldr, pos, w, T, (int)topk, M, Y, yt == TTQ_F32,
+                                                 ldy, as_stream(stream)),
+                         "ttq_moe_combine launch");
+}
+
+ttq_status ttq_moe_combine_grad(const void* dY, int yt, int64_t T, int64_t M, int64_t lddy, const void* R, int rt,
+                                int64_t rows, int64_t ldr, const int32_t* pos, const float* w, int64_t topk, void* dR,
+                                int64_t lddr, float* dw, void* stream) {
+    g_last_error.clear();
+    if (ttq_status e = check_slots(T, topk)) return e;
+    TTQ_REQUIRE(M > 0 && dim_ok(M), "M out of range");
+    if (ttq_status e = check_matrix("dY", dY, yt, T, M, lddy)) return e;
+    TTQ_REQUIRE(dtype_ok(rt), "R: unknown dtype %d", rt);
+    TTQ_REQUIRE(dim_ok(rows), "rows out of range");
+    if (T > 0 && dw != nullptr)
+        if (ttq_status e = check_rows_moe("R", R, rt, rows, M, ldr)) return e;
+    if (T > 0 && dR != nullptr)
+        if (ttq_status e = check_rows_moe("dR", dR, rt, rows, M, lddr)) return e;
+    TTQ_REQUIRE(dR == nullptr || dR != R, "dR must not be R");
+    TTQ_REQUIRE(aligned(w, 4) && aligned(dw, 4), "w or dw: misaligned");
+    if (T == 0 || (dR == nullptr && dw == nullptr)) return TTQ_OK;
+    if (ttq_status e = check_ints("pos", pos)) return e;
+    return device_status(ttq::launch_moe_combine_grad(dY, yt == TTQ_F32, lddy, R, rt == TTQ_F32, rows, ldr, pos, w, T,
+                                                      (int)topk, M, dR, lddr, dw, as_stream(stream)),
+                         "ttq_moe_combine_grad launch");
+}
+
+size_t ttq_moe_i8_workspace_bytes(int64_t T, int64_t topk, int64_t K, int64_t I, int64_t M, int64_t E) {
+    if (check_moe_i8_sizes(T, topk, K, I, M, E)) return 0;
+    return ttq::moe_i8_ws_bytes(T, topk, K, I, M, E) + kAlign;
+}
+
+ttq_status ttq_moe_i8(const ttq_moe_i8_args* a, void* ws, size_t ws_bytes, void* stream) {
+    g_last_error.clear();
+    TTQ_REQUIRE(a != nullptr, "args: null pointer");
+    if (ttq_status e = check_moe_i8_sizes(a->T, a->topk, a->K, a->I, a->M, a->E)) return e;
+    TTQ_REQUIRE(a->act == TTQ_ACT_SILU || a->act == TTQ_ACT_GELU_TANH, "act: unknown value %d", a->act);
+    if (ttq_status e = check_matrix("X", a->X, a->xt, a->T, a->K, a->ldx)) return e;
+    if (ttq_status e = check_output(a->Y, a->yt, a->T, a->M, a->ldy)) return e;
+    if (a->T == 0 || a->M == 0) return TTQ_OK;
+    TTQ_REQUIRE(a->ids != nullptr && aligned(a->ids, 4) && a->w != nullptr && aligned(a->w, 4),
+                "ids or w: null or misaligned");
+    if (ttq_status e = check_experts_i8("gate_up", a->gate_up, a->K)) return e;
+    if (ttq_status e = check_experts_i8("down", a->down, a->I)) return e;
+    if (ttq_status e = check_ws(ws, ws_bytes, ttq::moe_i8_ws_bytes(a->T, a->topk, a->K, a->I, a->M, a->E))) return e;
+    return device_status(ttq::launch_moe_i8(a, (char*)ws, as_stream(stream)), "ttq_moe_i8 launch");
+}
+
+}  // extern "C"

@@ -25,6 +25,9 @@ EXPORTS = ("ttq_stats", "ttq_stats_p", "ttq_awq_scales", "ttq_quantize_groups", 
            "ttq_workspace_bytes", "ttq_linear", "ttq_linear_shared", "ttq_linear_shared_workspace_bytes",
            "ttq_linear_noalloc", "ttq_moe_route", "ttq_moe", "ttq_moe_workspace_bytes", "ttq_adapters_add",
            "ttq_adapters_workspace_bytes", "ttq_qgemm_adapters", "ttq_qgemm_adapters_workspace_bytes",
+           "ttq_quantize_rows", "ttq_gemm_i8", "ttq_gemm_i8_workspace_bytes", "ttq_qgemm_i8",
+           "ttq_qgemm_i8_workspace_bytes", "ttq_moe_sort", "ttq_moe_sort_workspace_bytes", "ttq_moe_gather",
+           "ttq_moe_combine", "ttq_moe_combine_grad", "ttq_moe_i8", "ttq_moe_i8_workspace_bytes",
            "ttq_status_str", "ttq_last_error")
 
 
@@ -72,6 +75,21 @@ class AdaptersArgs(ctypes.Structure):
                 ("ids", ctypes.c_void_p)]
 
 
+class ExpertI8(ctypes.Structure):
+    _fields_ = [("s", ctypes.c_void_p), ("s_stride", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p)]
+
+
+class MoeI8Args(ctypes.Structure):
+    _fields_ = [
+        ("X", ctypes.c_void_p), ("xt", ctypes.c_int), ("T", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("ldx", ctypes.c_int64), ("ids", ctypes.c_void_p), ("w", ctypes.c_void_p), ("topk", ctypes.c_int64),
+        ("E", ctypes.c_int64), ("I", ctypes.c_int64), ("M", ctypes.c_int64),
+        ("gate_up", ExpertI8), ("down", ExpertI8), ("act", ctypes.c_int),
+        ("Y", ctypes.c_void_p), ("yt", ctypes.c_int), ("ldy", ctypes.c_int64),
+    ]
+
+
 _lib_handle = None
 
 
@@ -109,6 +127,18 @@ def lib() -> ctypes.CDLL:
         "ttq_qgemm_adapters": [vp, i32, i64, i64, i64, vp, vp, vp, vp, i64, i32, i32, ctypes.POINTER(AdaptersArgs),
                                vp, i32, i64, vp, sz, vp],
         "ttq_qgemm_adapters_workspace_bytes": [i64, i64, i64, i32, i32, i32],
+        "ttq_quantize_rows": [vp, i32, i64, i64, i64, vp, i32, vp, i64, vp, vp],
+        "ttq_gemm_i8": [vp, vp, i64, i64, i64, vp, vp, i64, i64, vp, i32, i64, vp, sz, vp],
+        "ttq_gemm_i8_workspace_bytes": [i64, i64, i64],
+        "ttq_qgemm_i8": [vp, i32, i64, i64, i64, vp, vp, vp, i64, i64, vp, i32, i64, vp, sz, vp],
+        "ttq_qgemm_i8_workspace_bytes": [i64, i64, i64],
+        "ttq_moe_sort": [vp, i64, i64, i64, vp, vp, vp, vp, sz, vp],
+        "ttq_moe_sort_workspace_bytes": [i64, i64, i64],
+        "ttq_moe_gather": [vp, i32, i64, i64, i64, vp, i64, vp, i64, i64, vp],
+        "ttq_moe_combine": [vp, i32, i64, i64, vp, vp, i64, i64, i64, vp, i32, i64, vp],
+        "ttq_moe_combine_grad": [vp, i32, i64, i64, i64, vp, i32, i64, i64, vp, vp, i64, vp, i64, vp, vp],
+        "ttq_moe_i8": [ctypes.POINTER(MoeI8Args), vp, sz, vp],
+        "ttq_moe_i8_workspace_bytes": [i64, i64, i64, i64, i64, i64],
         "ttq_status_str": [i32],
         "ttq_last_error": [],
     }
@@ -119,7 +149,9 @@ def lib() -> ctypes.CDLL:
     L.ttq_workspace_bytes.restype = ctypes.c_size_t
     L.ttq_lowrank_factors_workspace_bytes.restype = ctypes.c_size_t
     L.ttq_linear_shared_workspace_bytes.restype = ctypes.c_size_t
-    for name in ("ttq_moe_workspace_bytes", "ttq_adapters_workspace_bytes", "ttq_qgemm_adapters_workspace_bytes"):
+    for name in ("ttq_moe_workspace_bytes", "ttq_adapters_workspace_bytes", "ttq_qgemm_adapters_workspace_bytes",
+                 "ttq_gemm_i8_workspace_bytes", "ttq_qgemm_i8_workspace_bytes", "ttq_moe_sort_workspace_bytes",
+                 "ttq_moe_i8_workspace_bytes"):
         getattr(L, name).restype = ctypes.c_size_t
     L.ttq_status_str.restype = ctypes.c_char_p
     L.ttq_last_error.restype = ctypes.c_char_p
@@ -696,6 +728,257 @@ def ttq_qgemm_adapters(X: torch.Tensor, s: torch.Tensor, codes: torch.Tensor, sc
         _dense(scale_f16, "scale_f16", torch.float16, (M, K // group), dev),
         _dense(zero_f16, "zero_f16", torch.float16, (M, K // group), dev), M, bits, group, ctypes.byref(ad),
         Y.data_ptr(), _code(Y), _row_stride(Y, "Y"), wp, wn, stream))
+    return Y
+
+
+# ------------------------------------------------------------------ 8-bit integers, sorted tokens
+
+def _rows8(codes: torch.Tensor, name: str, dev: int) -> int:
+    """Row stride of a matrix of 8-bit codes."""
+    if not isinstance(codes, torch.Tensor) or codes.dtype is not torch.int8:
+        raise TypeError(f"{name} must be a torch.int8 tensor")
+    if codes.get_device() != dev:
+        raise ValueError(f"{name} must be on device {dev}")
+    return _row_stride(codes, name)
+
+
+def _on(t: torch.Tensor, name: str, dev: int) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a device tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on device {dev}")
+    return t
+
+
+def _wide_stride(t: torch.Tensor, name: str) -> int:
+    """Row stride of a matrix whose rows need not be whole 16-byte pieces
+    long; that of a single row does not matter."""
+    ld = _row_stride(t, name)
+    return ld if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+@_on_tensor_device
+def ttq_quantize_rows(X: torch.Tensor, s: Optional[torch.Tensor] = None, divide: bool = False,
+                      codes: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, stream=None):
+    """Rows of X [R][K] (times s [K], or with divide=True by it) in 8 bits:
+    codes int8 [R][K] and scale float32 [R]."""
+    ldx = _row_stride(X, "X")
+    R, K = X.shape
+    dev = X.get_device()
+    codes = _output(codes, (R, K), torch.int8, X, "codes")
+    ldc = _rows8(codes, "codes", dev)
+    if scale is None:
+        scale = X.new_empty((R,), dtype=torch.float32)
+    _check(lib().ttq_quantize_rows(X.data_ptr(), _code(X), R, K, ldx,
+                                   None if s is None else _dense(s, "s", torch.float32, (K,), dev), int(bool(divide)),
+                                   codes.data_ptr(), ldc, _dense(scale, "scale", torch.float32, (R,), dev), stream))
+    return codes, scale
+
+
+def ttq_gemm_i8_workspace_bytes(T: int, K: int, M: int) -> int:
+    return int(lib().ttq_gemm_i8_workspace_bytes(T, K, M))
+
+
+def gemm_i8_workspace(T: int, K: int, M: int, device="cuda") -> torch.Tensor:
+    """Allocate a workspace tensor of ttq_gemm_i8_workspace_bytes() bytes."""
+    return _bytes_tensor(ttq_gemm_i8_workspace_bytes(T, K, M), device)
+
+
+@_on_tensor_device
+def ttq_gemm_i8(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
+                Y: Optional[torch.Tensor] = None, y_dtype=torch.float32, ws: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """Product of 8-bit rows (ttq_quantize_rows): Y[t][o] = x_scale[t]
+    w_scale[o] sum_j X[t][j] W[o][j], X int8 [T][K], W int8 [M][K]."""
+    dev = X.get_device()
+    ldx, ldw = _rows8(X, "X", dev), _rows8(W, "W", dev)
+    T, K = X.shape
+    M = W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError(f"W must be [M][{K}] (got {list(W.shape)})")
+    Y = _output(Y, (T, M), y_dtype, X)
+    wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_gemm_i8_workspace_bytes(T, K, M), X)
+    _check(lib().ttq_gemm_i8(X.data_ptr(), _dense(x_scale, "x_scale", torch.float32, (T,), dev), T, K, ldx, W.data_ptr(),
+                             _dense(w_scale, "w_scale", torch.float32, (M,), dev), M, ldw, Y.data_ptr(), _code(Y),
+                             _row_stride(Y, "Y"), wp, wn, stream))
+    return Y
+
+
+def ttq_qgemm_i8_workspace_bytes(T: int, K: int, M: int) -> int:
+    return int(lib().ttq_qgemm_i8_workspace_bytes(T, K, M))
+
+
+def qgemm_i8_workspace(T: int, K: int, M: int, device="cuda") -> torch.Tensor:
+    """Allocate a workspace tensor of ttq_qgemm_i8_workspace_bytes() bytes."""
+    return _bytes_tensor(ttq_qgemm_i8_workspace_bytes(T, K, M), device)
+
+
+@_on_tensor_device
+def ttq_qgemm_i8(X: torch.Tensor, s: Optional[torch.Tensor], W: torch.Tensor, w_scale: torch.Tensor,
+                 Y: Optional[torch.Tensor] = None, y_dtype=torch.float32, ws: Optional[torch.Tensor] = None,
+                 stream=None) -> torch.Tensor:
+    """The projection W_hat (X / s) in 8-bit integers: X [T][K] is quantized
+    per token (ttq_quantize_rows with divide=True), W int8 [M][K] and w_scale
+    [M] are the weight times s in 8 bits."""
+    dev = X.get_device()
+    ldx, ldw = _row_stride(X, "X"), _rows8(W, "W", dev)
+    T, K = X.shape
+    M = W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError(f"W must be [M][{K}] (got {list(W.shape)})")
+    Y = _output(Y, (T, M), y_dtype, X)
+    wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_qgemm_i8_workspace_bytes(T, K, M), X)
+    _check(lib().ttq_qgemm_i8(X.data_ptr(), _code(X), T, K, ldx,
+                              None if s is None else _dense(s, "s", torch.float32, (K,), dev), W.data_ptr(),
+                              _dense(w_scale, "w_scale", torch.float32, (M,), dev), M, ldw, Y.data_ptr(), _code(Y),
+                              _row_stride(Y, "Y"), wp, wn, stream))
+    return Y
+
+
+def ttq_moe_sort_workspace_bytes(T: int, topk: int, E: int) -> int:
+    return int(lib().ttq_moe_sort_workspace_bytes(T, topk, E))
+
+
+def moe_sort_workspace(T: int, topk: int, E: int, device="cuda") -> torch.Tensor:
+    """Allocate a workspace tensor of ttq_moe_sort_workspace_bytes() bytes."""
+    return torch.empty(ttq_moe_sort_workspace_bytes(T, topk, E), dtype=torch.uint8, device=device)
+
+
+@_on_tensor_device
+def ttq_moe_sort(ids: torch.Tensor, E: int, offsets: Optional[torch.Tensor] = None,
+                 order: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None, stream=None):
+    """The slots of ids (int32 [T][topk]) sorted by expert, stably: offsets
+    [E + 1] (each expert's rows), order [T * topk] (each row's slot, -1 behind
+    the last) and pos [T][topk] (each slot's row, -1 without an expert)."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T][topk]")
+    T, topk = ids.shape
+    dev = ids.get_device()
+    ip = _dense(ids, "ids", torch.int32, (T, topk), dev)
+    n = E + 1 if 0 <= E <= 1024 else 0       # others are refused below
+    offsets = ids.new_empty((n,)) if offsets is None else offsets
+    order = ids.new_empty((T * topk,)) if order is None else order
+    pos = ids.new_empty((T, topk)) if pos is None else pos
+    if ws is None:
+        ws = ids.new_empty(lib().ttq_moe_sort_workspace_bytes(T, topk, E), dtype=torch.uint8)
+    wp, wn, ws = _scratch(ws, 0, ids)
+    _check(lib().ttq_moe_sort(ip, T, topk, E, _dense(offsets, "offsets", torch.int32, (n,), dev),
+                              _dense(order, "order", torch.int32, (T * topk,), dev),
+                              _dense(pos, "pos", torch.int32, (T, topk), dev), wp, wn, stream))
+    return offsets, order, pos
+
+
+@_on_tensor_device
+def ttq_moe_gather(X: torch.Tensor, pos: torch.Tensor, R: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """R[pos[t][j]] = X[t]: the tokens' rows in their experts' order (pos from
+    ttq_moe_sort).  R [rows][K] has X's dtype (default: new, a row for each
+    slot); rows that no slot names are left as they were."""
+    ldx = _wide_stride(X, "X")
+    T, K = X.shape
+    if pos.dim() != 2:
+        raise ValueError("pos must be [T][topk]")
+    topk = pos.shape[1]
+    if R is None:
+        R = X.new_empty((T * topk, K))
+    elif _on(R, "R", X.get_device()).dtype != X.dtype or R.dim() != 2 or R.shape[1] != K:
+        raise ValueError(f"R must be [rows][{K}] of X's dtype")
+    _check(lib().ttq_moe_gather(X.data_ptr(), _code(X), T, K, ldx,
+                                _dense(pos, "pos", torch.int32, (T, topk), X.get_device()), topk, R.data_ptr(),
+                                R.shape[0], _wide_stride(R, "R"), stream))
+    return R
+
+
+@_on_tensor_device
+def ttq_moe_combine(R: torch.Tensor, pos: torch.Tensor, w: Optional[torch.Tensor] = None,
+                    Y: Optional[torch.Tensor] = None, y_dtype=None, stream=None) -> torch.Tensor:
+    """Y[t] = sum_j w[t][j] R[pos[t][j]] (w None: ones, the gradient of
+    ttq_moe_gather); a slot without a row adds nothing.  Y: R's dtype unless
+    given."""
+    ldr = _wide_stride(R, "R")
+    rows, M = R.shape
+    if pos.dim() != 2:
+        raise ValueError("pos must be [T][topk]")
+    T, topk = pos.shape
+    dev = R.get_device()
+    Y = _output(Y, (T, M), R.dtype if y_dtype is None else y_dtype, R)
+    _check(lib().ttq_moe_combine(R.data_ptr(), _code(R), rows, ldr, _dense(pos, "pos", torch.int32, (T, topk), dev),
+                                 None if w is None else _dense(w, "w", torch.float32, (T, topk), dev), T, topk, M,
+                                 Y.data_ptr(), _code(Y), _row_stride(Y, "Y"), stream))
+    return Y
+
+
+@_on_tensor_device
+def ttq_moe_combine_grad(dY: torch.Tensor, R: torch.Tensor, pos: torch.Tensor, w: Optional[torch.Tensor] = None,
+                         dR: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, stream=None):
+    """The gradient of ttq_moe_combine: (dR [rows][M], dw [T][topk]) from dY
+    [T][M].  dR (default: new) keeps the rows that no slot names."""
+    lddy, ldr = _wide_stride(dY, "dY"), _wide_stride(R, "R")
+    T, M = dY.shape
+    dev = dY.get_device()
+    if _on(R, "R", dev).shape[1] != M or pos.dim() != 2:
+        raise ValueError(f"R must be [rows][{M}] and pos [T][topk]")
+    topk = pos.shape[1]
+    dR = _output(dR, tuple(R.shape), R.dtype, dY, "dR")
+    if dR.dtype != R.dtype:
+        raise TypeError("dR must have R's dtype")
+    if dw is None:
+        dw = dY.new_empty((T, topk), dtype=torch.float32)
+    _check(lib().ttq_moe_combine_grad(dY.data_ptr(), _code(dY), T, M, lddy, R.data_ptr(), _code(R), R.shape[0], ldr,
+                                      _dense(pos, "pos", torch.int32, (T, topk), dev),
+                                      None if w is None else _dense(w, "w", torch.float32, (T, topk), dev), topk,
+                                      dR.data_ptr(), _wide_stride(dR, "dR"),
+                                      _dense(dw, "dw", torch.float32, (T, topk), dev), stream))
+    return dR, dw
+
+
+def ttq_moe_i8_workspace_bytes(T: int, topk: int, K: int, I: int, M: int, E: int) -> int:
+    return int(lib().ttq_moe_i8_workspace_bytes(T, topk, K, I, M, E))
+
+
+def moe_i8_workspace(T: int, topk: int, K: int, I: int, M: int, E: int, device="cuda") -> torch.Tensor:
+    """Allocate a workspace tensor of ttq_moe_i8_workspace_bytes() bytes."""
+    return _bytes_tensor(ttq_moe_i8_workspace_bytes(T, topk, K, I, M, E), device)
+
+
+def _expert_i8(name: str, q: dict, E: int, rows: int, K: int, dev) -> ExpertI8:
+    s = q["s"]
+    per = isinstance(s, torch.Tensor) and s.dim() == 2
+    return ExpertI8(          # in the order of its fields
+        _dense(s, name + " s", torch.float32, (E, K) if per else (K,), dev), K if per else 0,
+        _dense(q["codes"], name + " codes", torch.int8, (E, rows, K), dev),
+        _dense(q["scale"], name + " scale", torch.float32, (E, rows), dev))
+
+
+@_on_tensor_device
+def ttq_moe_i8(X: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up: dict, down: dict, act: str = "silu",
+               Y: Optional[torch.Tensor] = None, y_dtype=torch.float32, ws: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """A gated mixture-of-experts layer in 8-bit integers, any number of
+    tokens: X [T][K], ids and w [T][topk] (ttq_moe_route); gate_up and down:
+    dicts of ``codes`` int8 [E][rows][K], ``scale`` [E][rows] and ``s`` ([K],
+    or [E][K] for scales per expert), with 2 I rows of K channels (gate first)
+    and M rows of I channels.  Returns Y [T][M]."""
+    if act not in TTQ_ACTS:
+        raise ValueError(f"act must be one of {sorted(TTQ_ACTS)}")
+    ldx = _row_stride(X, "X")
+    T, K = X.shape
+    dev = X.get_device()
+    if ids.dim() != 2 or gate_up["codes"].dim() != 3 or down["codes"].dim() != 3:
+        raise ValueError("ids must be [T][topk] and codes [E][rows][channels]")
+    topk = ids.shape[1]
+    E, rows2, _ = gate_up["codes"].shape
+    M, I = down["codes"].shape[1], rows2 // 2
+    if rows2 % 2:
+        raise ValueError("gate_up must have an even number of rows")
+    Y = _output(Y, (T, M), y_dtype, X)
+    wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_moe_i8_workspace_bytes(T, topk, K, I, M, E), X)
+    a = MoeI8Args(            # in the order of its fields
+        X.data_ptr(), _code(X), T, K, ldx, _dense(ids, "ids", torch.int32, (T, topk), dev),
+        _dense(w, "w", torch.float32, (T, topk), dev), topk, E, I, M, _expert_i8("gate_up", gate_up, E, rows2, K, dev),
+        _expert_i8("down", down, E, M, I, dev), TTQ_ACTS[act], Y.data_ptr(), _code(Y), _row_stride(Y, "Y"))
+    _check(lib().ttq_moe_i8(ctypes.byref(a), wp, wn, stream))
     return Y
 
 
