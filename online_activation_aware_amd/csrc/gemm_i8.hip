@@ -3,31 +3,43 @@
 // the sum exact in int32 on the matrix cores (K <= 2^17), for one matrix or for
 // rows sorted by expert that multiply their own expert's; optionally
 //   Y[t][o] = act(g) u / s[o],  g and u the products with rows o and M + o of W.
+//
+// Two kernels: k_i8_stream for few rows, bound by W's bytes, and k_i8_tile, with
+// tiles from 64 x 32 (bound by W's bytes as well) to 256 x 256 (bound by the matrix
+// cores, their power and the LDS that feeds them).  As every sum is exact, a
+// result is the same whichever computes it.
 #include <algorithm>
+#include <cmath>
+#include <type_traits>
 
 #include "i8.hpp"
 
 namespace ttq {
 
-constexpr int kStreamRows = 16;                   // rows of W a workgroup
+enum { kOutBf16, kOutF32, kOutGate, kOutSums };  // Y in bf16, in fp32, gated in fp32; sums of a part of the channels
 
-// W streamed once per tile of 16 NT rows of X: a workgroup owns 16 rows of W (16
-// of gate and of up), its waves share out the channels, 64 at a time, and add
-// their sums through LDS.
-template <int NT, bool GATE, bool YF32>
-__global__ __launch_bounds__(NT <= 2 ? 1024 : 512) void k_i8_stream(I8Product p) {
-    constexpr int NW = NT <= 2 ? 16 : 8, G = GATE ? 2 : 1;
+constexpr int kStreamRows = 16;                   // rows of W a workgroup
+constexpr int kXcdRows = 8;                       // tiles of W a group
+
+// W streamed once per tile of 16 NT rows of X, straight into registers: a
+// workgroup owns 16 rows of W (16 of gate and of up), its NW waves share out the
+// channels and add their sums through LDS.  A wave requests U steps of 64
+// channels of W and X together before the first product.
+template <int NT, int NW, int OUT>
+__global__ __launch_bounds__(NW * kWave) void k_i8_stream(I8Product p) {
+    constexpr bool GATE = OUT == kOutGate, YF32 = OUT != kOutBf16;
+    constexpr int G = GATE ? 2 : 1, U = NT == 1 ? 8 / G : 4 / G;
     __shared__ i32x4 sums[NW][G][NT][kWave];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-    const int64_t mt = (p.M + kStreamRows - 1) / kStreamRows;
-    const int64_t o0 = blockIdx.x % mt * kStreamRows;
-    const I8Tile tile = find_tile(p.offsets, p.E, p.T, 16 * NT, blockIdx.x / mt);
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int mt = (int)((p.M + kStreamRows - 1) / kStreamRows);
+    const int64_t o0 = (int64_t)(blockIdx.x % mt) * kStreamRows;
+    const I8Tile tile = find_tile(p.offsets, p.E, (int)p.T, 16 * NT, (int)(blockIdx.x / mt));
     if (tile.first >= tile.last) return;
-    const int64_t r16 = lane & 15;
-    const int64_t kq = 16 * (lane >> 4);
+    const int r16 = lane & 15, kq = 16 * (lane >> 4);
     const int64_t wrow = min(o0 + r16, p.M - 1);  // rows behind the last one repeat it
-    const int8_t* w = p.W + tile.expert * p.w_stride + wrow * p.ldw + kq;
-    const int8_t* up = w + p.M * p.ldw;
+    const int8_t* w[G];
+    w[0] = p.W + tile.expert * p.w_stride + wrow * p.ldw + kq;
+    if constexpr (GATE) w[1] = w[0] + p.M * p.ldw;
     const int8_t* x[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -35,35 +47,53 @@ __global__ __launch_bounds__(NT <= 2 ? 1024 : 512) void k_i8_stream(I8Product p)
         if (p.order) r = p.order[r] / p.topk;
         x[n] = p.X + r * p.ldx + kq;
     }
+    // The scales of the results of waves that add, requested ahead.
+    float xs = 0.f;
+    I8Scales<GATE> ws[4];
+    if (wave < NT) {
+        const int t = min(tile.first + 16 * wave + r16, tile.last - 1);
+        xs = p.x_scale[p.order ? p.order[t] / p.topk : t];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ws[i] = i8_scales<GATE>(p, tile.expert, min(o0 + 4 * (lane >> 4) + i, p.M - 1));
+    }
     i32x4 acc[G][NT];
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[g][n] = i32x4{0, 0, 0, 0};
-    const int64_t steps = p.K / 64;               // whole ones
-    const int64_t s1 = steps * (wave + 1) / NW;
-    for (int64_t s = steps * wave / NW; s < s1; ++s) {
-        const u32x4 a = *(const u32x4*)(w + 64 * s);
-        u32x4 b = {0, 0, 0, 0};
-        if constexpr (GATE) b = *(const u32x4*)(up + 64 * s);
+    const int steps = (int)(p.K / 64);            // whole ones
+    const int s1 = steps * (wave + 1) / NW;
+    auto batch = [&](int s, auto count) __attribute__((always_inline)) {
+        constexpr int C = decltype(count)::value;
+        u32x4 a[C][G], b[C][NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const u32x4 v = *(const u32x4*)(x[n] + 64 * s);
-            acc[0][n] = mfma_i8(a, v, acc[0][n]);
-            if constexpr (GATE) acc[G - 1][n] = mfma_i8(b, v, acc[G - 1][n]);
-        }
-    }
+        for (int u = 0; u < C; ++u)
+#pragma unroll
+            for (int g = 0; g < G; ++g) a[u][g] = *(const u32x4*)(w[g] + 64 * (int64_t)(s + u));
+#pragma unroll
+        for (int u = 0; u < C; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) b[u][n] = *(const u32x4*)(x[n] + 64 * (int64_t)(s + u));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < C; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int g = 0; g < G; ++g) acc[g][n] = mfma_i8(a[u][g], b[u][n], acc[g][n]);
+    };
+    int s = steps * wave / NW;
+    for (; s + U <= s1; s += U) batch(s, std::integral_constant<int, U>{});
+    for (; s < s1; ++s) batch(s, std::integral_constant<int, 1>{});
     if (p.K % 64 != 0 && wave == NW - 1) {        // the channels behind the last whole step
         const bool in = 64 * steps + kq < p.K;
         const u32x4 none = {0, 0, 0, 0};
-        const u32x4 a = in ? *(const u32x4*)(w + 64 * steps) : none;
-        u32x4 b = none;
-        if constexpr (GATE) b = in ? *(const u32x4*)(up + 64 * steps) : none;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const u32x4 v = in ? *(const u32x4*)(x[n] + 64 * steps) : none;
-            acc[0][n] = mfma_i8(a, v, acc[0][n]);
-            if constexpr (GATE) acc[G - 1][n] = mfma_i8(b, v, acc[G - 1][n]);
+            const u32x4 v = in ? *(const u32x4*)(x[n] + 64 * (int64_t)steps) : none;
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+                acc[g][n] = mfma_i8(in ? *(const u32x4*)(w[g] + 64 * (int64_t)steps) : none, v, acc[g][n]);
         }
     }
 #pragma unroll
@@ -73,46 +103,344 @@ __global__ __launch_bounds__(NT <= 2 ? 1024 : 512) void k_i8_stream(I8Product p)
     __syncthreads();
     if (wave >= NT) return;
     // Wave n adds token fragment n: the lane's 4 rows of W of one row of X.
-    i32x4 s[G];
+    i32x4 t4[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        s[g] = sums[0][g][wave][lane];
+        t4[g] = sums[0][g][wave][lane];
 #pragma unroll
-        for (int v = 1; v < NW; ++v) s[g] += sums[v][g][wave][lane];
+        for (int v = 1; v < NW; ++v) t4[g] += sums[v][g][wave][lane];
     }
     const int64_t t = tile.first + 16 * wave + r16, o = o0 + 4 * (lane >> 4);
     if (t >= tile.last || o >= p.M) return;
-    const float xs = p.x_scale[p.order ? p.order[t] / p.topk : t];
     f32x4 y;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = i8_result<GATE>(p, tile.expert, min(o + i, p.M - 1), xs, s[0][i], s[G - 1][i]);
+    for (int i = 0; i < 4; ++i) y[i] = i8_result<GATE>(ws[i], p.act, xs, t4[0][i], t4[G - 1][i]);
     store_y4<YF32>(p.Y, t * p.ldy + o, p.M - o, p.yvec, y);
 }
 
-template <int NT>
-static hipError_t stream(const I8Product& p, bool gate, bool yf32, hipStream_t st) {
+template <int NT, int NW>
+static hipError_t stream(const I8Product& p, int out, hipStream_t st) {
     const int64_t mt = (p.M + kStreamRows - 1) / kStreamRows;
     const int64_t tiles = p.offsets ? i8_tiles(p.T, p.E, 16 * NT) : (p.T + 16 * NT - 1) / (16 * NT);
-    const int nt = NT <= 2 ? 1024 : 512;
-    if (mt * tiles * nt >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)(mt * tiles)), block((unsigned)nt);
-    if (gate) return launch_kernel(k_i8_stream<NT, true, true>, grid, block, 0, st, nullptr, nullptr, p);
-    return yf32 ? launch_kernel(k_i8_stream<NT, false, true>, grid, block, 0, st, nullptr, nullptr, p)
-                : launch_kernel(k_i8_stream<NT, false, false>, grid, block, 0, st, nullptr, nullptr, p);
+    const dim3 grid((unsigned)(mt * tiles)), block(NW * kWave);
+    if (out == kOutGate) return launch_kernel(k_i8_stream<NT, NW, kOutGate>, grid, block, 0, st, nullptr, nullptr, p);
+    return out == kOutF32 ? launch_kernel(k_i8_stream<NT, NW, kOutF32>, grid, block, 0, st, nullptr, nullptr, p)
+                          : launch_kernel(k_i8_stream<NT, NW, kOutBf16>, grid, block, 0, st, nullptr, nullptr, p);
 }
 
-size_t i8_product_ws_bytes(int64_t T, int64_t K, int64_t M) { return 0; }
+// Tiles of BM rows of W x BN rows of X, WM x WN waves.  Both operands arrive by
+// buffer -> LDS DMA, 128 channels (a line) a row and step, in two slots; an LDS
+// row's 16-byte chunks are exclusive-or'ed with its number (conflict-free).
+//
+// A step has two phases: X and the first half of every wave's rows of W, then the
+// second half; each part of a slot is requested again for the next step but one
+// as soon as every wave has read it, so that a part is in flight for three
+// phases (a step's 64 KB take longer than one step's products to arrive).
+template <int BM, int BN, int WM, int WN, int OUT>
+__global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
+    constexpr bool GATE = OUT == kOutGate, YF32 = OUT != kOutBf16;
+    constexpr int NW = WM * WN;
+    constexpr int FA = BM / WM / 16, FB = BN / WN / 16;         // fragments of 16 rows per wave
+    constexpr int HR = BM / WM / 2;                             // a wave's rows of W a phase
+    constexpr int XOPS = BN * kLdsRowB / 1024 / NW, WOPS = BM / 2 * kLdsRowB / 1024 / NW;   // DMA operations of 1 KB per wave
+    constexpr int G = GATE ? 2 : 1, BO = BM / G;                // outputs of a tile
+    constexpr int SLOT = (BM + BN) * kLdsRowB;                  // W of the first phase, of the second, X
+    constexpr int kStep = kLdsRowB;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * SLOT];
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wm = wave % WM, wn = wave / WM;
+    // Workgroups go to the eight XCDs in turn; the ones an XCD receives are
+    // consecutive in an order that walks groups of kXcdRows tiles of W across the
+    // tiles of X, so that its L2 holds what they share.
+    const int mt = (int)((p.M + BO - 1) / BO), n = (int)gridDim.x / p.splits, nt = n / mt;
+    const int part = OUT == kOutSums ? (int)blockIdx.x / n : 0, bx = (int)blockIdx.x - part * n;
+    const int x = bx % 8, v = x * (n / 8) + min(x, n % 8) + bx / 8;
+    const int g0 = v / (kXcdRows * nt) * kXcdRows, gw = min(kXcdRows, mt - g0), in = v - g0 * nt;
+    const int64_t o0 = (int64_t)(g0 + in % gw) * BO;
+    const I8Tile tile = find_tile(p.offsets, p.E, (int)p.T, BN, in / gw);
+    const int rows = tile.last - tile.first;
+    if (rows <= 0) return;
+    const int8_t* W = p.W + tile.expert * p.w_stride + o0 * p.ldw;
+    const int64_t wrows = GATE ? 2 * p.M - o0 : min((int64_t)BM, p.M - o0);
+    const rsrc_t rw = make_rsrc(W, (wrows - 1) * p.ldw + p.K);
+    const int8_t* X = p.X + (p.order ? 0 : (int64_t)tile.first * p.ldx);
+    const rsrc_t rx = make_rsrc(X, ((p.order ? p.xrows : rows) - 1) * p.ldx + p.K);
 
-bool i8_product_fits(int64_t T, int64_t M) { return (T + 15) / 16 * ((M + 15) / 16) < (int64_t)1 << 22; }
+    // A DMA operation fills eight LDS rows; lane l lands in row l / 8 of them at
+    // position l % 8, holding chunk (l % 8) ^ (row & 7).
+    const int rl = lane >> 3, ch = (lane & 7) ^ rl;
+    int xoff[XOPS], woff[2][WOPS];
+#pragma unroll
+    for (int i = 0; i < XOPS; ++i) {
+        const int r = 8 * (XOPS * wave + i) + rl;
+        const int src = r >= rows ? 0 : p.order ? p.order[tile.first + r] / p.topk : r;
+        xoff[i] = r >= rows ? INT32_MIN : src * (int)p.ldx + 16 * ch;   // behind the last row: zeros, not read
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < WOPS; ++i) {
+            const int l = 8 * (WOPS * wave + i) + rl, w = l / HR * 2 * HR + h * HR + l % HR;
+            // Gate and up: 16 rows of either in turn.
+            const int r = GATE ? (w >> 5) * 16 + (w & 15) + ((w >> 4) & 1) * (int)p.M : w;
+            woff[h][i] = r * (int)p.ldw + 16 * ch;
+        }
+    i32x4 acc[FA][FB];
+#pragma unroll
+    for (int i = 0; i < FA; ++i)
+#pragma unroll
+        for (int j = 0; j < FB; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+
+    int nk = (int)((p.K + kStep - 1) / kStep), k0 = 0;
+    if constexpr (OUT == kOutSums) {              // this part's steps
+        k0 = nk * part / p.splits;
+        nk = nk * (part + 1) / p.splits;
+    }
+    auto issue_w = [&](int slot, int k, int h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < WOPS; ++i)
+            dma_to_lds<16>(rw, lds + slot + h * (BM / 2) * kLdsRowB + (wave * WOPS + i) * 1024, woff[h][i], k * kStep);
+    };
+    auto issue_x = [&](int slot, int k) __attribute__((always_inline)) {
+        // Behind the last channel X is zero: an offset past the descriptor.
+        const int gone = 16 * ch >= (int)p.K - k * kStep ? INT32_MIN : 0;
+#pragma unroll
+        for (int i = 0; i < XOPS; ++i)
+            dma_to_lds<16>(rx, lds + slot + BM * kLdsRowB + (wave * XOPS + i) * 1024, xoff[i] | gone, k * kStep);
+    };
+    u32x4 a[2][FA / 2], b[2][FB];                 // fragments of the two 64-channel halves
+    const int ar = wm * HR + (lane & 15);
+    const int off[2] = {lds_swz(ar, lane >> 4), lds_swz(ar, 4 + (lane >> 4))};
+    const int boff = (BM + wn * FB * 16 - wm * HR) * kLdsRowB;
+    // Waves whose rows lie behind the tile's last one have no products.  (The
+    // waves of a column of the tile lie on all SIMDs: a tile of half the rows
+    // takes half the time.)
+    const bool active = wn * FB * 16 < rows && (GATE || o0 + wm * FA * 16 < p.M);
+    auto phase = [&](int slot, int h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const uint8_t* from = lds + slot + off[s];
+            if (h == 0)
+#pragma unroll
+                for (int j = 0; j < FB; ++j) b[s][j] = *(const u32x4*)(from + boff + j * 16 * kLdsRowB);
+#pragma unroll
+            for (int i = 0; i < FA / 2; ++i) a[s][i] = *(const u32x4*)(from + (h * (BM / 2) + i * 16) * kLdsRowB);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < FA / 2; ++i)
+#pragma unroll
+                for (int j = 0; j < FB; ++j)
+                    acc[h * (FA / 2) + i][j] = mfma_i8(a[s][i], b[s][j], acc[h * (FA / 2) + i][j]);
+    };
+    // (Steps behind the last one are requested too: they read nothing or zeros.)
+    issue_w(0, k0, 0);
+    issue_x(0, k0);
+    issue_w(0, k0, 1);
+    issue_w(SLOT, k0 + 1, 0);
+    issue_x(SLOT, k0 + 1);
+    // The tile's scales, a thread one of either side: through LDS to their lanes
+    // once the products are done.  (Other LDS arrays, or stores to this one before
+    // the loop, make the compiler wait for every DMA before a fragment is read.)
+    static_assert(BN <= NW * kWave && BO <= NW * kWave, "a thread holds one scale of either side");
+    const int ts = tile.first + min((int)threadIdx.x, rows - 1);
+    const float xs = p.x_scale[p.order ? p.order[ts] / p.topk : ts];
+    const I8Scales<GATE> wscale = i8_scales<GATE>(p, tile.expert, min(o0 + threadIdx.x, p.M - 1));
+    constexpr int kLater = 2 * WOPS + XOPS;       // operations requested after the part that is needed next
+    wait_vmcnt<kLater>();                         // the first phase of step 0
+    sync_lds();
+    int slot = 0;
+    auto steps = [&](auto with) __attribute__((always_inline)) {
+        for (int k = k0; k < nk; ++k) {
+            issue_w(SLOT - slot, k + 1, 1);
+            if constexpr (decltype(with)::value) phase(slot, 0);
+            wait_vmcnt<kLater>();
+            sync_lds();
+            issue_w(slot, k + 2, 0);
+            issue_x(slot, k + 2);
+            if constexpr (decltype(with)::value) phase(slot, 1);
+            wait_vmcnt<kLater>();
+            sync_lds();
+            slot = SLOT - slot;
+        }
+    };
+    if (active) steps(std::true_type{});
+    else steps(std::false_type{});
+    wait_vmcnt<0>();
+
+    if constexpr (OUT == kOutSums) {              // [parts][T][mp] int32, added by k_i8_sum
+        const int64_t mp = (p.M + 3) / 4 * 4;
+        int* out = p.sums + (int64_t)part * p.T * mp;
+#pragma unroll
+        for (int i = 0; i < FA; ++i) {
+            const int64_t o = o0 + (wm * FA + i) * 16 + 4 * (lane >> 4);
+#pragma unroll
+            for (int j = 0; j < FB; ++j) {
+                const int tl = (wn * FB + j) * 16 + (lane & 15);
+                if (tl < rows && o < p.M) *(i32x4*)(out + (int64_t)(tile.first + tl) * mp + o) = acc[i][j];
+            }
+        }
+        return;
+    }
+    // (Every wave has read its last fragments.)
+    float *sx = (float*)lds, *sw = sx + BN;
+    if (threadIdx.x < BN) sx[threadIdx.x] = xs;
+    if (threadIdx.x < BO) {
+        sw[threadIdx.x] = wscale.g;
+        if constexpr (GATE) {
+            sw[BO + threadIdx.x] = wscale.u;
+            sw[2 * BO + threadIdx.x] = wscale.s;
+        }
+    }
+    __syncthreads();
+    if (!active) return;
+    // The lane's 4 consecutive outputs of a row of X, for each pair of fragments.
+    const bool whole = rows == BN && o0 + BO <= p.M && p.yvec;
+#pragma unroll
+    for (int i = 0; i < FA; i += G) {
+        const int ol = (wm * FA + i) * (16 / G) + 4 * (lane >> 4);
+        const int64_t o = o0 + ol;
+        f32x4 w[3];
+#pragma unroll
+        for (int c = 0; c < (GATE ? 3 : 1); ++c) w[c] = *(const f32x4*)(sw + c * BO + ol);
+#pragma unroll
+        for (int j = 0; j < FB; ++j) {
+            const int tl = (wn * FB + j) * 16 + (lane & 15);
+            const float xt = sx[tl];
+            f32x4 y;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                y[r] = i8_result<GATE>(I8Scales<GATE>{w[0][r], w[GATE ? 1 : 0][r], w[GATE ? 2 : 0][r]}, p.act, xt,
+                                       acc[i][j][r], acc[i + G - 1][j][r]);
+            const int64_t at = (int64_t)(tile.first + tl) * p.ldy + o;
+            if (whole) store_y4<YF32>(p.Y, at, 4, 1, y);
+            else if (tl < rows && o < p.M) store_y4<YF32>(p.Y, at, p.M - o, p.yvec, y);
+        }
+    }
+}
+
+// Y from the parts' sums, added exactly in int32.
+template <bool YF32>
+__global__ __launch_bounds__(256) void k_i8_sum(I8Product p) {
+    const int64_t quads = (p.M + 3) / 4, all = p.T * quads;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / quads, o = (i - t * quads) * 4;
+        i32x4 s = {0, 0, 0, 0};
+        for (int c = 0; c < p.splits; ++c) s += *(const i32x4*)(p.sums + (c * all + i) * 4);
+        f32x4 y;
+        const float xs = p.x_scale[t];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) y[r] = i8_result<false>(i8_scales<false>(p, 0, min(o + r, p.M - 1)), 0, xs, s[r], 0);
+        store_y4<YF32>(p.Y, t * p.ldy + o, p.M - o, p.yvec, y);
+    }
+}
+
+template <int BM, int BN, int WM, int WN>
+static hipError_t tiled(const I8Product& p, int out, hipStream_t st) {
+    const bool gate = out == kOutGate, yf32 = out == kOutF32;
+    const int64_t bo = gate ? BM / 2 : BM, mt = (p.M + bo - 1) / bo;
+    const int64_t tiles = p.offsets ? i8_tiles(p.T, p.E, BN) : (p.T + BN - 1) / BN;
+    const dim3 grid((unsigned)(mt * tiles * p.splits)), block(WM * WN * kWave);
+    if (p.splits > 1) {
+        const hipError_t e = launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutSums>, grid, block, 0, st, nullptr, nullptr, p);
+        if (e != hipSuccess) return e;
+        const int64_t work = p.T * ((p.M + 3) / 4);
+        const dim3 sum((unsigned)std::min<int64_t>((work + 255) / 256, 8192));
+        return yf32 ? launch_kernel(k_i8_sum<true>, sum, dim3(256), 0, st, nullptr, nullptr, p)
+                    : launch_kernel(k_i8_sum<false>, sum, dim3(256), 0, st, nullptr, nullptr, p);
+    }
+    if (gate) return launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutGate>, grid, block, 0, st, nullptr, nullptr, p);
+    return yf32 ? launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutF32>, grid, block, 0, st, nullptr, nullptr, p)
+                : launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutBf16>, grid, block, 0, st, nullptr, nullptr, p);
+}
+
+// What a product takes by each kernel, in us, fitted to 170 shapes (1 to 8192
+// rows, 512 to 14336 channels and outputs), each timed with every kernel; the
+// choice by these costs lies 1.6% over the best kernel of each shape on average,
+// 25% at most.  Some of them (us): 8192 rows of 4096 -> 4096: 256 x 256 128, 256 x 128
+// 153, 128 x 64 193; 2048: 56, 40, 52; 512: 57, 31, 18, 64 x 32 20; 64: 64 x 32 12,
+// streamed 14; 16: 12 and 7; 14336 -> 4096, 1024 rows: 256 x 128 in two parts 78, in
+// one 103; 64 rows: 128 x 64 in eight parts 21, in one 48.
+//
+// A tile takes `start` and for each 128 channels `step`, `full` where every
+// compute unit has a tile and `more` for each further one that it works on at the
+// same time, at most `fit`.  Parts of the channels cost a second launch and the
+// traffic of their sums.  Nothing is faster than W's bytes.
+struct I8Kernel {
+    int bm, bn, fit;
+    double start, step, full, more;
+};
+constexpr I8Kernel kTiles[] = {{64, 32, 4, 3.0, 0.33, 0.25, 0.15},
+                               {128, 64, 3, 4.3, 0.48, 0.44, 0.31},
+                               {256, 128, 1, 5.0, 0.74, 0.91, 0},
+                               {256, 256, 1, 6.8, 0.96, 1.53, 0}};
+constexpr int kMaxSplits = 16;
+
+struct I8Choice {
+    int kernel;                                   // of kTiles; -1, -2: streamed for tiles of 16, 32 rows
+    int splits;
+};
+
+static I8Choice choose(int64_t T, int64_t K, int64_t M, int64_t E, bool experts, bool gate) {
+    const int64_t rows = experts ? std::max<int64_t>((T + E - 1) / E, 1) : T;    // of a matrix, on average
+    const double mats = experts ? (double)std::min(T, E) : 1;
+    const double steps = (double)((K + kLdsRowB - 1) / kLdsRowB), codes = mats * (double)(K * M) * (gate ? 2 : 1) / 1e6;
+    I8Choice best{0, 1};
+    double least = 0;
+    auto offer = [&](double us, int kernel, int splits) {
+        us = std::max(us, 3.0 + codes / 5.2 + (splits > 1 ? 3.1 : 0.0));
+        if (least > 0 && us >= least) return;
+        least = us;
+        best = {kernel, splits};
+    };
+    for (int k = 0; k < 4; ++k) {
+        const I8Kernel& c = kTiles[k];
+        const int64_t bo = gate ? c.bm / 2 : c.bm;
+        for (int s = 1; s <= (experts ? 1 : kMaxSplits); s *= 2) {
+            if (s > 1 && steps < 2 * s) break;
+            const double tiles = (double)(((M + bo - 1) / bo) * ((rows + c.bn - 1) / c.bn) * s) * mats;
+            const double n = std::ceil(tiles / 256), at_once = std::min(n, (double)c.fit);
+            const double step = c.step + (c.full - c.step) * std::min(tiles / 256, 1.0) + c.more * (at_once - 1);
+            offer(n / at_once * (c.start + steps / s * step) +
+                      (s > 1 ? 3.1 + (double)(s + 1) * T * M * 4 / 3.1e6 : 0.0), k, s);
+        }
+    }
+    for (int nt = 1; nt <= 2 && rows <= 64; ++nt) {
+        const double tiles = (double)((rows + 16 * nt - 1) / (16 * nt));
+        const double x = codes * tiles * std::min<double>(rows, 16 * nt) / 16;
+        offer(3.2 + codes / 10.2 + 0.097 * x + 0.8 * K / 4096 + 0.4 * (nt - 1), -nt, 1);
+    }
+    return best;
+}
+
+size_t i8_product_ws_bytes(int64_t T, int64_t K, int64_t M) {
+    const I8Choice c = choose(T, K, M, 1, false, false);
+    return c.splits > 1 ? (size_t)c.splits * T * ((M + 3) / 4 * 4) * 4 : 0;
+}
+
+// A grid has fewer than 2^32 threads: of the kernel with the smallest tiles, and
+// of the streaming one, which few rows may take.
+bool i8_product_fits(int64_t T, int64_t M) {
+    const double most = 4294967296.0;
+    return (double)((T + 31) / 32) * (double)((M + 63) / 64) * 128 < most && (T > 64 || (double)M / 16 * 4 * 256 < most);
+}
 
 hipError_t launch_i8_product(const I8Product& q, bool yf32, void* ws, hipStream_t st) {
     I8Product p = q;
     p.yvec = (uintptr_t)p.Y % 16 == 0 && p.ldy * (yf32 ? 4 : 2) % 16 == 0;
-    const bool gate = p.s_down != nullptr;
-    const int64_t rows = p.offsets ? (p.T + p.E - 1) / p.E : p.T;   // of one matrix, on average
-    if (rows <= 16) return stream<1>(p, gate, yf32, st);
-    if (rows <= 32) return stream<2>(p, gate, yf32, st);
-    return stream<4>(p, gate, yf32, st);
+    const int out = p.s_down != nullptr ? kOutGate : yf32 ? kOutF32 : kOutBf16;
+    const I8Choice c = choose(p.T, p.K, p.M, p.E, p.offsets != nullptr, out == kOutGate);
+    p.splits = c.splits;
+    p.sums = (int*)ws;
+    switch (c.kernel) {
+        case 0: return tiled<64, 32, 2, 1>(p, out, st);
+        case 1: return tiled<128, 64, 2, 2>(p, out, st);
+        case 2: return tiled<256, 128, 2, 4>(p, out, st);
+        case 3: return tiled<256, 256, 2, 4>(p, out, st);
+        case -1: return stream<1, 4>(p, out, st);
+    }
+    return stream<2, 4>(p, out, st);
 }
 
 }  // namespace ttq

@@ -18,20 +18,20 @@ __device__ __forceinline__ i32x4 mfma_i8(const u32x4& a, const u32x4& b, const i
 // The matrix of a tile of rows and the rows of it: [first, last).
 struct I8Tile {
     int expert;
-    int64_t first, last;
+    int first, last;
 };
 
 // Tile `tile` of at most `size` rows each, where rows [offsets[e], offsets[e+1])
 // multiply matrix e (offsets null: all rows matrix 0); first == last where
 // there are fewer.  Every wave finds its own: the tiles of 64 experts at a
 // time by a scan over the lanes.
-__device__ __forceinline__ I8Tile find_tile(const int32_t* offsets, int E, int64_t rows, int size, int64_t tile) {
+__device__ __forceinline__ I8Tile find_tile(const int32_t* offsets, int E, int rows, int size, int tile) {
     if (offsets == nullptr) {
-        const int64_t f = tile * size;
-        return {0, f < rows ? f : rows, f + size < rows ? f + size : rows};
+        const int f = min(tile * size, rows);
+        return {0, f, min(f + size, rows)};
     }
     const int lane = threadIdx.x & (kWave - 1);
-    int64_t before = 0;                           // tiles of the experts before these 64
+    int before = 0;                               // tiles of the experts before these 64
     for (int e0 = 0; e0 < E; e0 += kWave) {
         const int e = e0 + lane;
         const int lo = e < E ? offsets[e] : 0, hi = e < E ? offsets[e + 1] : 0;
@@ -44,12 +44,13 @@ __device__ __forceinline__ I8Tile find_tile(const int32_t* offsets, int E, int64
         }
         const uint64_t who = __ballot(before + p > tile);
         if (who) {
+            // (Read as scalars: a descriptor made of them is one for the wave.)
             const int l = __builtin_ctzll(who);
-            const int64_t first = __shfl(lo, l) + (tile - before - (__shfl(p, l) - __shfl(nt, l))) * size;
-            const int64_t end = __shfl(hi, l);
-            return {e0 + l, first, first + size < end ? first + size : end};
+            auto at = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
+            const int first = at(lo) + (tile - before - (at(p) - at(nt))) * size;
+            return {e0 + l, first, min(first + size, at(hi))};
         }
-        before += __shfl(p, kWave - 1);
+        before += __builtin_amdgcn_readlane(p, kWave - 1);
     }
     return {0, 0, 0};
 }
@@ -60,14 +61,25 @@ inline int64_t i8_tiles(int64_t rows, int64_t E, int64_t size) {
     return a + (rows - a) / size;
 }
 
-// A result of the sums s (of gate and up: sg and su).
+// The scales of output o: of its sum, or of gate's and up's and 1 / s_down's s.
 template <bool GATE>
-__device__ __forceinline__ float i8_result(const I8Product& p, int expert, int64_t o, float xs, int sg, int su) {
+struct I8Scales {
+    float g, u, s;
+};
+template <bool GATE>
+__device__ __forceinline__ I8Scales<GATE> i8_scales(const I8Product& p, int expert, int64_t o) {
     const float* ws = p.w_scale + expert * p.M * (GATE ? 2 : 1);
-    const float g = (float)sg * xs * ws[o];
+    if constexpr (GATE) return {ws[o], ws[p.M + o], p.s_down[expert * p.s_stride + o]};
+    return {ws[o], 0.f, 0.f};
+}
+
+// A result of the sums sg (and su, of gate and up).
+template <bool GATE>
+__device__ __forceinline__ float i8_result(const I8Scales<GATE>& w, int act, float xs, int sg, int su) {
+    const float g = (float)sg * xs * w.g;
     if constexpr (!GATE) return g;
-    const float u = (float)su * xs * ws[p.M + o];
-    return moe_act(g, p.act) * u / p.s_down[expert * p.s_stride + o];
+    const float u = (float)su * xs * w.u;
+    return moe_act(g, act) * u / w.s;
 }
 
 }  // namespace ttq

@@ -227,12 +227,16 @@ struct I8Product {
     const int32_t* offsets = nullptr;
     const int32_t* order = nullptr;
     int topk = 1, E = 1;
+    int64_t xrows = 0;          // of X, with order
     int64_t w_stride = 0;
     // Gate and up: Y (fp32) is act(g) u / s_down[e * s_stride + o].
     const float* s_down = nullptr;
     int64_t s_stride = 0;
     int act = 0;
-    int yvec = 0;               // set by the launch
+    // Set by the launch:
+    int yvec = 0;
+    int splits = 1;             // parts of the channels, their sums in `sums`
+    int* sums = nullptr;
 };
 size_t i8_product_ws_bytes(int64_t T, int64_t K, int64_t M);
 bool i8_product_fits(int64_t T, int64_t M);       // a grid can cover T x M

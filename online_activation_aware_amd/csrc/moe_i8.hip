@@ -64,6 +64,7 @@ hipError_t launch_moe_i8(const ttq_moe_i8_args* a, char* ws, hipStream_t st) {
     p.offsets = offsets;
     p.order = per ? nullptr : order;
     p.topk = topk;
+    p.xrows = a->T;
     p.E = E;
     p.w_stride = 2 * a->I * a->K;
     p.s_down = a->down.s;
