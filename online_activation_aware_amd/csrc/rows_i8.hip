@@ -4,141 +4,137 @@
 // A row with an infinity or NaN among its v gets the scale NaN and codes 0, so
 // that every product of it is NaN and no other row's is touched.
 //
-// The code is the exact quotient's rounding, not that of a rounded quotient: q0 =
+// The code is the exact quotient's rounding, not that of a rounded quotient: q =
 // rne(v r), r = fp32(1 / scale), is off by one only next to a border, and the
-// remainder e = v - q0 scale, exact in one fma (a multiple of the smaller ulp,
-// at most half a scale and a little), says on which side v lies.
+// remainder e = v - q scale, exact in one fma (a multiple of the smaller ulp,
+// at most half a scale and a little), says on which side v lies.  v = x / s is
+// the IEEE quotient from fp32(1 / s) by two corrections (as in Markstein, "IA-64
+// and Elementary Functions", 2000), where no exponent is extreme.
 //
-// A workgroup takes whole rows: a lane holds two runs of eight values, read and
-// written as whole vectors by consecutive lanes, and the row's maximum is that
-// of the bit patterns (a NaN is above every number).  Rows of more than 16384
-// values are read twice, the second time from the cache.
+// A workgroup takes whole rows, one after the other, the next one's values
+// requested before the work on this one: a lane holds two runs of eight values,
+// read and written as whole vectors by consecutive lanes, and its s and 1 / s;
+// the row's maximum is that of the bit patterns (a NaN is above every number).
+// Rows of more than 16384 values are read twice, the second time from the cache.
 #include <algorithm>
 
 #include "i8.hpp"
+#include "rows_i8.hpp"
 #include "wave.hpp"
 
 namespace ttq {
 
-constexpr int kRowSeg = 8;                        // values of a vector
 constexpr int kRowSegs = 2;                       // vectors a lane holds
-
-template <bool F32>
-__device__ __forceinline__ void load8(const void* X, int64_t at, float (&f)[kRowSeg]) {
-    if constexpr (F32) {
-        const f32x4 a = *(const f32x4*)((const float*)X + at), b = *(const f32x4*)((const float*)X + at + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[i] = a[i];
-            f[4 + i] = b[i];
-        }
-    } else {
-        const u32x4 u = *(const u32x4*)((const uint16_t*)X + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = bf16lo_to_f32(u[i]);
-            f[2 * i + 1] = bf16hi_to_f32(u[i]);
-        }
-    }
-}
-
-__device__ __forceinline__ uint32_t pack4(const int (&q)[4]) {
-    return (q[0] & 0xFF) | (q[1] & 0xFF) << 8 | (q[2] & 0xFF) << 16 | (uint32_t)q[3] << 24;
-}
-
-// rne(v / scale) of the exact quotient, |v| <= 127.5 scale or so.
-__device__ __forceinline__ float code_of(float v, float scale, float r) {
-    float q = __builtin_rintf(v * r);
-    const float e = __builtin_fmaf(-q, scale, v), d = 2.f * __builtin_fabsf(e);
-    const bool odd = ((int)q & 1) != 0;
-    if (d > scale || (d == scale && odd)) q += __builtin_copysignf(1.f, e);
-    return fminf(fmaxf(q, -127.f), 127.f);
-}
-// The same where 1 / scale overflows or e could be rounded: in 64 bits the
-// quotient of two 24-bit numbers lands on a border only if it is one.
-__device__ __forceinline__ float code_of_tiny(float v, float scale) {
-    return fminf(fmaxf((float)__builtin_rint((double)v / (double)scale), -127.f), 127.f);
-}
 
 template <bool F32, int SMODE, bool HOLD>
 __global__ __launch_bounds__(1024) void k_quantize_rows(I8RowsArgs a) {
-    __shared__ uint32_t part[16];
+    constexpr int S = HOLD ? kRowSegs : 1;
+    __shared__ uint32_t part[2][16];
     const int tid = threadIdx.x, nt = blockDim.x, nw = nt / kWave;
     const int64_t R = a.nrows ? *a.nrows : a.R;
-    const int runs = (int)((a.K + (int64_t)nt * kRowSeg - 1) / ((int64_t)nt * kRowSeg));
-    for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
-        const int slot = a.order ? a.order[r] : 0;
-        const int64_t src = a.order ? slot / a.topk : r;
-        const float* s = SMODE ? a.s + (a.ids ? (int64_t)a.ids[slot] * a.s_stride : 0) : nullptr;
-        float v[kRowSegs][kRowSeg];
-        auto value = [&](int64_t k, float (&f)[kRowSeg]) __attribute__((always_inline)) {
-            load8<F32>(a.X, src * a.ldx + k, f);
-            if constexpr (SMODE) {
-                float sf[kRowSeg];
-                load8<true>(s, k, sf);
+    const int K = (int)a.K, runs = (K + nt * kRowSeg - 1) / (nt * kRowSeg);
+    RowScale<SMODE> s[S];
+    RowVector<F32> next[S];
+    auto source = [&](int64_t r, int& slot) __attribute__((always_inline)) {
+        slot = a.order ? a.order[r] : 0;
+        return a.order ? slot / a.topk : r;
+    };
+    auto request = [&](int64_t r) __attribute__((always_inline)) {
+        int slot;
+        const int64_t src = source(r, slot);
 #pragma unroll
-                for (int i = 0; i < kRowSeg; ++i) f[i] = SMODE == 1 ? f[i] * sf[i] : f[i] / sf[i];
+        for (int u = 0; u < S; ++u) {
+            const int k = (u * nt + tid) * kRowSeg;
+            if (k < K) {
+                next[u].load(a.X, src * a.ldx + k);
+                if (a.ids) s[u].load(a.s + (int64_t)a.ids[slot] * a.s_stride + k);
             }
-        };
+        }
+    };
+    if (HOLD && !a.ids)
+#pragma unroll
+        for (int u = 0; u < S; ++u) {
+            const int k = (u * nt + tid) * kRowSeg;
+            if (k < K) s[u].load(a.s + k);
+        }
+    if (HOLD && blockIdx.x < R) request(blockIdx.x);
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < R; r += gridDim.x, turn ^= 1) {
+        float v[S][kRowSeg] = {};
         uint32_t top = 0;
-        auto highest = [&](const float (&f)[kRowSeg]) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < kRowSeg; ++i) top = max(top, __builtin_bit_cast(uint32_t, f[i]) & 0x7FFFFFFFu);
+        int slot;
+        const int64_t src = source(r, slot);
+        // (Rows read twice: run u's values into v[0].)
+        auto value = [&](int k, bool exact) __attribute__((always_inline)) {
+            RowVector<F32> x;
+            x.load(a.X, src * a.ldx + k);
+            s[0].load(a.s + (a.ids ? (int64_t)a.ids[slot] * a.s_stride : 0) + k);
+            row_values(x, s[0], exact, v[0]);
         };
+        RowVector<F32> x[S];
         if constexpr (HOLD) {
 #pragma unroll
-            for (int u = 0; u < kRowSegs; ++u) {
-                const int64_t k = ((int64_t)u * nt + tid) * kRowSeg;
-                if (k < a.K) value(k, v[u]);
-                else
-#pragma unroll
-                    for (int i = 0; i < kRowSeg; ++i) v[u][i] = 0.f;
-                highest(v[u]);
+            for (int u = 0; u < S; ++u) {
+                x[u] = next[u];
+                if ((u * nt + tid) * kRowSeg < K) row_values(x[u], s[u], false, v[u]);
+                top = row_top(v[u], top);
             }
+            if (r + gridDim.x < R && !a.ids) request(r + gridDim.x);
         } else {
             for (int u = 0; u < runs; ++u) {
-                const int64_t k = ((int64_t)u * nt + tid) * kRowSeg;
-                if (k >= a.K) break;
-                value(k, v[0]);
-                highest(v[0]);
+                const int k = (u * nt + tid) * kRowSeg;
+                if (k >= K) break;
+                value(k, false);
+                top = row_top(v[0], top);
             }
         }
-        top = wave_max_u32(top);
-        if (nw > 1) {
-            if ((tid & (kWave - 1)) == 0) part[tid / kWave] = top;
+        auto whole = [&](int half) __attribute__((always_inline)) {   // of the row
+            top = wave_max_u32(top);
+            if (nw > 1) {
+                // (Turns alternate between two arrays: one barrier a turn.)
+                if ((tid & (kWave - 1)) == 0) part[half][tid / kWave] = top;
+                __syncthreads();
+                for (int w = 0; w < nw; ++w) top = max(top, part[half][w]);
+            }
+        };
+        whole(turn);
+        bool exact = false;
+        if (SMODE == 2 && top < kRowTiny) {       // quotients near the lowest exponents
+            exact = true;
             __syncthreads();
-            for (int w = 0; w < nw; ++w) top = max(top, part[w]);
+            top = 0;
+            if constexpr (HOLD) {
+#pragma unroll
+                for (int u = 0; u < S; ++u) {
+                    if ((u * nt + tid) * kRowSeg < K) row_values(x[u], s[u], true, v[u]);
+                    top = row_top(v[u], top);
+                }
+            } else {
+                for (int u = 0; u < runs; ++u) {
+                    const int k = (u * nt + tid) * kRowSeg;
+                    if (k >= K) break;
+                    value(k, true);
+                    top = row_top(v[0], top);
+                }
+            }
+            whole(turn);
             __syncthreads();
         }
-        const bool bad = top >= 0x7F800000u;      // an infinity or NaN
-        float scale = __builtin_bit_cast(float, top) / 127.f;
-        if (scale == 0.f) scale = 1.f;
-        if (bad) scale = __builtin_nanf("");
+        const float scale = row_scale(top);
         if (tid == 0) a.scale[r] = scale;
-        const float rs = 1.f / scale;
-        const bool tiny = scale < 0x1p-100f;
-        auto store = [&](int64_t k, const float (&f)[kRowSeg]) __attribute__((always_inline)) {
-            int q[kRowSeg];
-#pragma unroll
-            for (int i = 0; i < kRowSeg; ++i)
-                q[i] = bad ? 0 : (int)(tiny ? code_of_tiny(f[i], scale) : code_of(f[i], scale, rs));
-            u32x2 p;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) p[h] = pack4({q[4 * h], q[4 * h + 1], q[4 * h + 2], q[4 * h + 3]});
-            *(u32x2*)(a.codes + r * a.ldc + k) = p;
-        };
         if constexpr (HOLD) {
 #pragma unroll
-            for (int u = 0; u < kRowSegs; ++u) {
-                const int64_t k = ((int64_t)u * nt + tid) * kRowSeg;
-                if (k < a.K) store(k, v[u]);
+            for (int u = 0; u < S; ++u) {
+                const int k = (u * nt + tid) * kRowSeg;
+                if (k < K) *(u32x2*)(a.codes + r * a.ldc + k) = row_codes(v[u], scale);
             }
+            if (r + gridDim.x < R && a.ids) request(r + gridDim.x);
         } else {
             for (int u = 0; u < runs; ++u) {
-                const int64_t k = ((int64_t)u * nt + tid) * kRowSeg;
-                if (k >= a.K) break;
-                value(k, v[0]);
-                store(k, v[0]);
+                const int k = (u * nt + tid) * kRowSeg;
+                if (k >= K) break;
+                value(k, exact);
+                *(u32x2*)(a.codes + r * a.ldc + k) = row_codes(v[0], scale);
             }
         }
     }
@@ -148,8 +144,8 @@ hipError_t launch_quantize_rows(const I8RowsArgs& a, hipStream_t st) {
     const int64_t lanes = (a.K + kRowSeg * kRowSegs - 1) / (kRowSeg * kRowSegs);
     const int nt = (int)std::min<int64_t>((lanes + kWave - 1) / kWave * kWave, 1024);
     const bool hold = lanes <= 1024;
-    // Rows are taken in turn by at most eight rounds of the workgroups that fit.
-    const dim3 grid((unsigned)std::min<int64_t>(a.R, 256 * 2048 / nt * 8)), block((unsigned)nt);
+    // As many workgroups as fit the chip at 1024 lanes a compute unit.
+    const dim3 grid((unsigned)std::min<int64_t>(a.R, 256 * (1024 / nt))), block((unsigned)nt);
     const int mode = a.s == nullptr ? 0 : a.divide ? 2 : 1;
 #define TTQ_R3(F, S, H) return launch_kernel(k_quantize_rows<F, S, H>, grid, block, 0, st, nullptr, nullptr, a)
 #define TTQ_R2(F, S)          \

@@ -1,0 +1,130 @@
+// A lane's part of a row in 8 bits (rows_i8.hip has the mathematics).
+#pragma once
+
+#include "common.hpp"
+
+namespace ttq {
+
+constexpr int kRowSeg = 8;                        // values of a vector
+constexpr uint32_t kRowTiny = 0x21800000u;        // 2^-60
+
+// Eight values of a row as they lie in memory.
+template <bool F32>
+struct RowVector {
+    u32x4 w[F32 ? 2 : 1];
+    __device__ __forceinline__ void load(const void* X, int64_t at) {
+        const u32x4* p = (const u32x4*)((const char*)X + at * (F32 ? 4 : 2));
+        w[0] = p[0];
+        if constexpr (F32) w[1] = p[1];
+    }
+    __device__ __forceinline__ float operator[](int i) const {
+        const uint32_t u = w[F32 ? i / 4 : 0][F32 ? i % 4 : i / 2];   // (a copy: a bit cast of the element takes the first)
+        if constexpr (F32) return __builtin_bit_cast(float, u);
+        return i % 2 ? bf16hi_to_f32(u) : bf16lo_to_f32(u);
+    }
+};
+
+// The eight channels' scales: none (MODE 0), factors (1) or divisors (2).
+template <int MODE>
+struct RowScale {
+    float s[MODE ? kRowSeg : 1], r[MODE == 2 ? kRowSeg : 1];
+    bool plain;                                   // no exponent of s is extreme
+    __device__ __forceinline__ void load(const float* p) {
+        if constexpr (MODE) {
+            const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
+#pragma unroll
+            for (int i = 0; i < kRowSeg; ++i) s[i] = i < 4 ? a[i] : b[i - 4];
+        }
+        if constexpr (MODE == 2) {
+            plain = true;
+#pragma unroll
+            for (int i = 0; i < kRowSeg; ++i) {
+                r[i] = 1.f / s[i];
+                plain &= __builtin_fabsf(s[i]) > 0x1p-40f && __builtin_fabsf(s[i]) < 0x1p40f;
+            }
+        }
+    }
+};
+
+// v of the eight values: x, fp32(x s) or fp32(x / s).  exact: by the division
+// itself, for rows whose quotients are tiny (the corrections' remainders would
+// be rounded).  Elsewhere a quotient below 2^-100 may be off in its last bit,
+// where its code is 0 either way.
+template <bool F32, int MODE>
+__device__ __forceinline__ void row_values(const RowVector<F32>& x, const RowScale<MODE>& s, bool exact,
+                                           float (&v)[kRowSeg]) {
+    if constexpr (MODE == 2) {
+        if (exact || !s.plain) {
+#pragma unroll
+            for (int i = 0; i < kRowSeg; ++i) v[i] = x[i] / s.s[i];
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kRowSeg; ++i) {
+            float q = x[i] * s.r[i];
+            q = __builtin_fmaf(__builtin_fmaf(-q, s.s[i], x[i]), s.r[i], q);
+            v[i] = __builtin_fmaf(__builtin_fmaf(-q, s.s[i], x[i]), s.r[i], q);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kRowSeg; ++i) v[i] = MODE == 1 ? x[i] * s.s[i] : x[i];
+    }
+}
+
+__device__ __forceinline__ uint32_t row_top(const float (&v)[kRowSeg], uint32_t top) {
+#pragma unroll
+    for (int i = 0; i < kRowSeg; ++i) top = max(top, __builtin_bit_cast(uint32_t, v[i]) & 0x7FFFFFFFu);
+    return top;
+}
+
+// The scale of a row whose largest |v| has these bits.
+__device__ __forceinline__ float row_scale(uint32_t top) {
+    if (top >= 0x7F800000u) return __builtin_nanf("");
+    const float scale = __builtin_bit_cast(float, top) / 127.f;
+    return scale == 0.f ? 1.f : scale;
+}
+
+// The codes of eight values; 0 for a row whose scale is NaN.
+__device__ __forceinline__ u32x2 row_codes(const float (&v)[kRowSeg], float scale) {
+    constexpr float kMagic = 12582912.f;          // 1.5 2^23: a sum with it is a whole number, its low byte the code
+    uint32_t b[kRowSeg];
+    if (!(scale >= 0x1p-100f)) {
+        // 1 / scale could overflow, the remainder be rounded, the scale lie well
+        // below a / 127: in 64 bits the quotient of two 24-bit numbers lands on a
+        // border only if it is one.
+#pragma unroll
+        for (int i = 0; i < kRowSeg; ++i) {
+            const double q = __builtin_rint((double)v[i] / (double)scale);
+            b[i] = scale == scale ? (uint32_t)(int)fmin(fmax(q, -127.0), 127.0) : 0u;
+        }
+    } else {
+        const float r = 1.f / scale, half = 0.5f * scale;
+        float t[kRowSeg];
+        bool off = false;
+#pragma unroll
+        for (int i = 0; i < kRowSeg; ++i) {
+            t[i] = __builtin_fmaf(v[i], r, kMagic);
+            off |= !(__builtin_fabsf(__builtin_fmaf(-(t[i] - kMagic), scale, v[i])) < half);
+        }
+        if (off) {                                // a value on a border or on its wrong side
+#pragma unroll
+            for (int i = 0; i < kRowSeg; ++i) {
+                const float e = __builtin_fmaf(-(t[i] - kMagic), scale, v[i]), d = __builtin_fabsf(e);
+                const bool odd = __builtin_bit_cast(uint32_t, t[i]) & 1u;
+                if (d > half || (d == half && odd)) t[i] += __builtin_copysignf(1.f, e);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRowSeg; ++i) b[i] = __builtin_bit_cast(uint32_t, t[i]);
+    }
+    u32x2 p;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t lo = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0C0C0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x04000C0Cu);
+        p[h] = lo | hi;
+    }
+    return p;
+}
+
+}  // namespace ttq
