@@ -13,6 +13,8 @@
 #include <type_traits>
 
 #include "i8.hpp"
+#include "rows_i8.hpp"
+#include "wave.hpp"
 
 namespace ttq {
 
@@ -126,6 +128,144 @@ static hipError_t stream(const I8Product& p, int out, hipStream_t st) {
     if (out == kOutGate) return launch_kernel(k_i8_stream<NT, NW, kOutGate>, grid, block, 0, st, nullptr, nullptr, p);
     return out == kOutF32 ? launch_kernel(k_i8_stream<NT, NW, kOutF32>, grid, block, 0, st, nullptr, nullptr, p)
                           : launch_kernel(k_i8_stream<NT, NW, kOutBf16>, grid, block, 0, st, nullptr, nullptr, p);
+}
+
+// One token whose row is quantized on the way, in one launch: every workgroup
+// forms the codes itself, in LDS, the token's values requested first and its own
+// first codes of W behind them.  Its waves take `blocks` blocks of 16 rows of W
+// at a time and share out the channels of each.  (14336 -> 4096: k_quantize_rows
+// and k_i8_stream take 5 and 12 us one after the other.)
+constexpr int kOneWaves = 16, kOneSegs = 2;       // vectors of eight values a lane holds
+__host__ __device__ constexpr int one_pad(int64_t K) { return (int)((K + 63) / 64 * 64); }
+
+template <bool XF32, bool DIV, bool YF32>
+__global__ __launch_bounds__(kOneWaves * kWave) void k_i8_one(I8RowsArgs x, I8Product p, int blocks,
+                                                                int share, int turns) {
+    constexpr int NT = kOneWaves * kWave, U = 4;
+    __shared__ i32x4 sums[kOneWaves][kWave];
+    uint32_t* part = (uint32_t*)sums;             // of the waves' maxima
+    extern __shared__ __attribute__((aligned(16))) int8_t codes[];   // [kp + 64], zeros from channel K on
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int K = (int)p.K, kp = one_pad(K), r16 = lane & 15, kq = 16 * (lane >> 4);
+    const int wb = wave / share, wk = wave % share;   // this wave's block, its place among the `share` waves of it
+    const int steps = kp / 64, s0 = steps * wk / share, s1 = steps * (wk + 1) / share;
+    const int last = max(s1 - 1, 0);              // (a wave may have no step)
+
+    RowScale<DIV ? 1 : 0> s[kOneSegs];            // (divisions: a reciprocal of one use costs more)
+    RowVector<XF32> y[kOneSegs];                  // (lanes behind the last channel repeat it)
+#pragma unroll
+    for (int u = 0; u < kOneSegs; ++u) {
+        const int k = min((u * NT + tid) * kRowSeg, K - kRowSeg);
+        y[u].load(x.X, k);
+        s[u].load(x.s + k);
+    }
+    f32x4 ws;                                     // of the turn's outputs
+    auto load_ws = [&](int turn) __attribute__((always_inline)) {
+        const int64_t o = (int64_t)(turn * blocks + wb) * kStreamRows + 4 * (lane >> 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ws[i] = p.w_scale[min(o + i, p.M - 1)];
+    };
+    load_ws(blockIdx.x);
+    const int8_t* w;
+    auto rows_of = [&](int turn) __attribute__((always_inline)) {
+        return p.W + min((int64_t)(turn * blocks + wb) * kStreamRows + r16, p.M - 1) * p.ldw;   // rows behind the last one repeat it
+    };
+    // U steps of this wave's rows of W from step s on; behind the wave's last step,
+    // and behind the last channel, any codes: the token's are zero there.
+    auto fetch = [&](u32x4 (&a)[U], int s) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) a[u] = *(const u32x4*)(w + min(64 * min(s + u, last) + kq, K - 16));
+    };
+    u32x4 a[2][U];
+    w = rows_of(blockIdx.x);
+    fetch(a[0], s0);
+    fetch(a[1], s0 + U);
+    __builtin_amdgcn_sched_barrier(0);
+
+    float v[kOneSegs][kRowSeg];
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < kOneSegs; ++u) {
+#pragma unroll
+        for (int c = 0; c < kRowSeg; ++c) v[u][c] = DIV ? y[u][c] / s[u].s[DIV ? c : 0] : y[u][c];
+        top = row_top(v[u], top);
+    }
+    top = wave_max_u32(top);
+    if (lane == 0) part[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kOneWaves; ++n) top = max(top, part[n]);
+    const float xs = row_scale(top);
+#pragma unroll
+    for (int u = 0; u < kOneSegs; ++u) {
+        const int k = (u * NT + tid) * kRowSeg;
+        if (k < K) *(u32x2*)(codes + k) = row_codes(v[u], xs);
+    }
+    if (tid < kp + 64 - K) codes[K + tid] = 0;
+    __syncthreads();
+
+#pragma unroll 1
+    for (int g = blockIdx.x; g < turns; g += gridDim.x) {
+        const int64_t o = (int64_t)(g * blocks + wb) * kStreamRows + 4 * (lane >> 4);
+        i32x4 acc = {0, 0, 0, 0};
+        auto multiply = [&](const u32x4 (&f)[U], int s) __attribute__((always_inline)) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                acc = mfma_i8(f[u], *(const u32x4*)(codes + (s + u < s1 ? 64 * (s + u) : kp) + kq), acc);
+        };
+#pragma unroll 1
+        for (int s = s0; s < s1; s += 2 * U) {
+            multiply(a[0], s);
+            if (s + 2 * U < s1) fetch(a[0], s + 2 * U);
+            multiply(a[1], s + U);
+            if (s + 3 * U < s1) fetch(a[1], s + 3 * U);
+        }
+        if (g + gridDim.x < turns) {              // the next turn's first codes
+            w = rows_of(g + gridDim.x);
+            fetch(a[0], s0);
+            fetch(a[1], s0 + U);
+        }
+        sums[wave][lane] = acc;
+        __syncthreads();
+        if (wk == 0 && r16 == 0 && o < p.M) {     // (all columns are the token's)
+            for (int n = 1; n < share; ++n) acc += sums[wave + n][lane];
+            f32x4 r;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = (float)acc[i] * xs * ws[i];
+            load_ws(g + gridDim.x);
+            store_y4<YF32>(p.Y, o, p.M - o, p.yvec, r);
+        }
+        __syncthreads();
+    }
+}
+
+// (64 KB of LDS in all.)
+bool i8_one_fits(int64_t T, int64_t K) { return T == 1 && K <= kOneWaves * kWave * kRowSeg * kOneSegs; }
+
+hipError_t launch_i8_one(const I8RowsArgs& x, const I8Product& q, bool yf32, hipStream_t st) {
+    I8Product p = q;
+    p.yvec = (uintptr_t)p.Y % 16 == 0;
+    // One workgroup a compute unit, so that each quantizes once for its turns;
+    // more blocks a turn where rows of W allow it, so that a wave has more steps.
+    const int64_t groups = (p.M + kStreamRows - 1) / kStreamRows;
+    const int blocks = groups >= 768 ? 4 : groups >= 384 ? 2 : 1;
+    const int64_t turns = (groups + blocks - 1) / blocks;
+    const dim3 grid((unsigned)std::min<int64_t>(turns, 256)), block(kOneWaves * kWave);
+    const size_t lds = (size_t)one_pad(p.K) + 64;
+#define TTQ_ONE(XF, DV)                                                                                             \
+    do {                                                                                                            \
+        if (yf32) return launch_kernel(k_i8_one<XF, DV, true>, grid, block, lds, st, nullptr, nullptr, x, p, blocks,       \
+                                                         kOneWaves / blocks, (int)turns);                                    \
+        return launch_kernel(k_i8_one<XF, DV, false>, grid, block, lds, st, nullptr, nullptr, x, p, blocks,              \
+                             kOneWaves / blocks, (int)turns);                                                                \
+    } while (0)
+    if (x.xf32) {
+        if (x.s) TTQ_ONE(true, true);
+        TTQ_ONE(true, false);
+    }
+    if (x.s) TTQ_ONE(false, true);
+    TTQ_ONE(false, false);
+#undef TTQ_ONE
 }
 
 // Tiles of BM rows of W x BN rows of X, WM x WN waves.  Both operands arrive by

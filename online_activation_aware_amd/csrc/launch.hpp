@@ -242,6 +242,10 @@ size_t i8_product_ws_bytes(int64_t T, int64_t K, int64_t M);
 bool i8_product_fits(int64_t T, int64_t M);       // a grid can cover T x M
 hipError_t launch_i8_product(const I8Product& p, bool yf32, void* ws, hipStream_t st);
 
+// ttq_qgemm_i8 of one token in one launch (codes and scales of X unused).
+bool i8_one_fits(int64_t T, int64_t K);
+hipError_t launch_i8_one(const I8RowsArgs& x, const I8Product& p, bool yf32, hipStream_t st);
+
 // Tokens sorted by expert and back (sort.hip).
 size_t moe_sort_ws_bytes(int64_t n, int64_t E);
 hipError_t launch_moe_sort(const int32_t* ids, int64_t n, int E, int32_t* offsets, int32_t* order, int32_t* pos,

@@ -898,12 +898,12 @@ ttq_status ttq_qgemm_i8(const void* X, int xt, int64_t T, int64_t K, int64_t ldx
     int8_t* q = (int8_t*)w;
     float* qs = (float*)(w + ws_qgemm_i8_codes(T, K));
     hipStream_t st = as_stream(stream);
-    if (ttq_status e = device_status(ttq::launch_quantize_rows({X, xt == TTQ_F32, ldx, T, K, s, true, q, K, qs}, st),
-                                     "ttq_qgemm_i8 launch"))
-        return e;
-    return device_status(ttq::launch_i8_product({q, K, qs, T, K, W, ldw, w_scale, M, Y, ldy}, yt == TTQ_F32,
-                                                w + ws_qgemm_i8_head(T, K), st),
-                         "ttq_qgemm_i8 launch");
+    const ttq::I8RowsArgs rows{X, xt == TTQ_F32, ldx, T, K, s, true, q, K, qs};
+    const ttq::I8Product p{q, K, qs, T, K, W, ldw, w_scale, M, Y, ldy};
+    if (ttq::i8_one_fits(T, K))
+        return device_status(ttq::launch_i8_one(rows, p, yt == TTQ_F32, st), "ttq_qgemm_i8 launch");
+    if (ttq_status e = device_status(ttq::launch_quantize_rows(rows, st), "ttq_qgemm_i8 launch")) return e;
+    return device_status(ttq::launch_i8_product(p, yt == TTQ_F32, w + ws_qgemm_i8_head(T, K), st), "ttq_qgemm_i8 launch");
 }
 
 size_t ttq_moe_sort_workspace_bytes(int64_t T, int64_t topk, int64_t E) {

@@ -177,6 +177,24 @@ def test_qgemm(T, Tn, K, M, xt, yt, scaled):
     same(Y, want)
 
 
+@pytest.mark.parametrize("K,M", [(16, 1), (48, 33), (80, 17), (144, 6161), (320, 12300), (1040, 4097), (16384, 40), (16400, 40)])
+@pytest.mark.parametrize("xt,yt", [("bf16", "bf16"), ("f32", "f32")])
+def test_qgemm_one_token(T, K, M, xt, yt):
+    """One launch: fewer channels than its waves take at once, several turns of
+    one, two and four blocks; more channels than it holds."""
+    say(f"qgemm_i8 one token K={K} M={M} {xt} {yt}")
+    rng = np.random.default_rng(K + M)
+    X, x = enc(rng.standard_normal((1, K)), xt)
+    s = np.exp(rng.standard_normal(K) * 0.5).astype(np.float32)
+    wq = rng.integers(-127, 128, (M, K)).astype(np.int8)
+    ws = rng.random(M).astype(np.float32)
+    big, Y = within(torch.empty((1, M), dtype=DT[yt], device="cuda"), 3, -3.0)
+    for sv in (s, None):
+        T.ttq_qgemm_i8(X, None if sv is None else f32_dev(sv), i8_dev(wq), f32_dev(ws), Y=Y)
+        same(Y, rounded(ref.product(*ref.quantize(x, sv, True), wq, ws), yt))
+        assert untouched(big, Y, -3.0)
+
+
 @pytest.mark.parametrize("Tn", [1, 3, 20, 200])
 def test_qgemm_rows_that_are_not_finite(T, Tn):
     say(f"qgemm_i8 not finite T={Tn}")
