@@ -34,9 +34,11 @@ __global__ __launch_bounds__(NW * kWave) void k_i8_stream(I8Product p) {
     __shared__ i32x4 sums[NW][G][NT][kWave];
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int mt = (int)((p.M + kStreamRows - 1) / kStreamRows);
-    const int64_t o0 = (int64_t)(blockIdx.x % mt) * kStreamRows;
-    const I8Tile tile = find_tile(p.offsets, p.E, (int)p.T, 16 * NT, (int)(blockIdx.x / mt));
+    I8Tile tile{0, (int)blockIdx.x / mt * 16 * NT, 0, (int)blockIdx.x % mt};
+    tile.last = min(tile.first + 16 * NT, (int)p.T);
+    if (p.offsets) tile = find_tile(p.offsets, p.E, 16 * NT, mt, blockIdx.x);
     if (tile.first >= tile.last) return;
+    const int64_t o0 = (int64_t)tile.mtile * kStreamRows;
     const int r16 = lane & 15, kq = 16 * (lane >> 4);
     const int64_t wrow = min(o0 + r16, p.M - 1);  // rows behind the last one repeat it
     const int8_t* w[G];
@@ -123,8 +125,8 @@ __global__ __launch_bounds__(NW * kWave) void k_i8_stream(I8Product p) {
 template <int NT, int NW>
 static hipError_t stream(const I8Product& p, int out, hipStream_t st) {
     const int64_t mt = (p.M + kStreamRows - 1) / kStreamRows;
-    const int64_t tiles = p.offsets ? i8_tiles(p.T, p.E, 16 * NT) : (p.T + 16 * NT - 1) / (16 * NT);
-    const dim3 grid((unsigned)(mt * tiles)), block(NW * kWave);
+    const int64_t blocks = p.offsets ? i8_blocks(p.T, p.E, 16 * NT, mt) : mt * ((p.T + 16 * NT - 1) / (16 * NT));
+    const dim3 grid((unsigned)blocks), block(NW * kWave);
     if (out == kOutGate) return launch_kernel(k_i8_stream<NT, NW, kOutGate>, grid, block, 0, st, nullptr, nullptr, p);
     return out == kOutF32 ? launch_kernel(k_i8_stream<NT, NW, kOutF32>, grid, block, 0, st, nullptr, nullptr, p)
                           : launch_kernel(k_i8_stream<NT, NW, kOutBf16>, grid, block, 0, st, nullptr, nullptr, p);
@@ -273,10 +275,12 @@ hipError_t launch_i8_one(const I8RowsArgs& x, const I8Product& q, bool yf32, hip
 // row's 16-byte chunks are exclusive-or'ed with its number (conflict-free).
 //
 // A step has two phases: X and the first half of every wave's rows of W, then the
-// second half; each part of a slot is requested again for the next step but one
-// as soon as every wave has read it, so that a part is in flight for three
-// phases (a step's 64 KB take longer than one step's products to arrive).
-template <int BM, int BN, int WM, int WN, int OUT>
+// second half; each part of a slot is requested again as soon as every wave has
+// read it: X, which tiles share in the L2, three phases ahead of its use, W two
+// more for each of its WS slots beyond two.  (A step's 64 KB take longer than one
+// step's products to arrive.  Eight experts of 14336 -> 4096, two tiles of 256 rows
+// each: two slots of W 340 us, three 000.)
+template <int BM, int BN, int WM, int WN, int WS, int OUT>
 __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
     constexpr bool GATE = OUT == kOutGate, YF32 = OUT != kOutBf16;
     constexpr int NW = WM * WN;
@@ -284,22 +288,28 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
     constexpr int HR = BM / WM / 2;                             // a wave's rows of W a phase
     constexpr int XOPS = BN * kLdsRowB / 1024 / NW, WOPS = BM / 2 * kLdsRowB / 1024 / NW;   // DMA operations of 1 KB per wave
     constexpr int G = GATE ? 2 : 1, BO = BM / G;                // outputs of a tile
-    constexpr int SLOT = (BM + BN) * kLdsRowB;                  // W of the first phase, of the second, X
+    constexpr int SW = BM * kLdsRowB, SX = BN * kLdsRowB;       // slots: W of the first phase and of the second; X
     constexpr int kStep = kLdsRowB;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * SLOT];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[WS * SW + 2 * SX];
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave % WM, wn = wave / WM;
-    // Workgroups go to the eight XCDs in turn; the ones an XCD receives are
-    // consecutive in an order that walks groups of kXcdRows tiles of W across the
-    // tiles of X, so that its L2 holds what they share.
-    const int mt = (int)((p.M + BO - 1) / BO), n = (int)gridDim.x / p.splits, nt = n / mt;
+    // One matrix: the workgroups that an XCD receives are consecutive in an order
+    // that walks groups of kXcdRows tiles of W across the tiles of X, so that its L2
+    // holds what they share.
+    const int mt = (int)((p.M + BO - 1) / BO), n = (int)gridDim.x / p.splits;
     const int part = OUT == kOutSums ? (int)blockIdx.x / n : 0, bx = (int)blockIdx.x - part * n;
-    const int x = bx % 8, v = x * (n / 8) + min(x, n % 8) + bx / 8;
-    const int g0 = v / (kXcdRows * nt) * kXcdRows, gw = min(kXcdRows, mt - g0), in = v - g0 * nt;
-    const int64_t o0 = (int64_t)(g0 + in % gw) * BO;
-    const I8Tile tile = find_tile(p.offsets, p.E, (int)p.T, BN, in / gw);
+    I8Tile tile;
+    if (p.offsets) {
+        tile = find_tile(p.offsets, p.E, BN, mt, bx);
+    } else {
+        const int x = bx % 8, v = x * (n / 8) + min(x, n % 8) + bx / 8, nt = n / mt;
+        const int g0 = v / (kXcdRows * nt) * kXcdRows, gw = min(kXcdRows, mt - g0), in = v - g0 * nt;
+        const int first = in / gw * BN;
+        tile = {0, first, min(first + BN, (int)p.T), g0 + in % gw};
+    }
     const int rows = tile.last - tile.first;
     if (rows <= 0) return;
+    const int64_t o0 = (int64_t)tile.mtile * BO;
     const int8_t* W = p.W + tile.expert * p.w_stride + o0 * p.ldw;
     const int64_t wrows = GATE ? 2 * p.M - o0 : min((int64_t)BM, p.M - o0);
     const rsrc_t rw = make_rsrc(W, (wrows - 1) * p.ldw + p.K);
@@ -337,49 +347,51 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
         nk = nk * (part + 1) / p.splits;
     }
     auto issue_w = [&](int slot, int k, int h) __attribute__((always_inline)) {
+        const int none = k >= nk ? INT32_MIN : 0; // behind the last step: not read
 #pragma unroll
         for (int i = 0; i < WOPS; ++i)
-            dma_to_lds<16>(rw, lds + slot + h * (BM / 2) * kLdsRowB + (wave * WOPS + i) * 1024, woff[h][i], k * kStep);
+            dma_to_lds<16>(rw, lds + slot + h * (SW / 2) + (wave * WOPS + i) * 1024, woff[h][i] | none, k * kStep);
     };
     auto issue_x = [&](int slot, int k) __attribute__((always_inline)) {
         // Behind the last channel X is zero: an offset past the descriptor.
-        const int gone = 16 * ch >= (int)p.K - k * kStep ? INT32_MIN : 0;
+        const int gone = k >= nk || 16 * ch >= (int)p.K - k * kStep ? INT32_MIN : 0;
 #pragma unroll
         for (int i = 0; i < XOPS; ++i)
-            dma_to_lds<16>(rx, lds + slot + BM * kLdsRowB + (wave * XOPS + i) * 1024, xoff[i] | gone, k * kStep);
+            dma_to_lds<16>(rx, lds + WS * SW + slot + (wave * XOPS + i) * 1024, xoff[i] | gone, k * kStep);
     };
     u32x4 a[2][FA / 2], b[2][FB];                 // fragments of the two 64-channel halves
-    const int ar = wm * HR + (lane & 15);
-    const int off[2] = {lds_swz(ar, lane >> 4), lds_swz(ar, 4 + (lane >> 4))};
-    const int boff = (BM + wn * FB * 16 - wm * HR) * kLdsRowB;
-    // Waves whose rows lie behind the tile's last one have no products.  (The
-    // waves of a column of the tile lie on all SIMDs: a tile of half the rows
-    // takes half the time.)
-    const bool active = wn * FB * 16 < rows && (GATE || o0 + wm * FA * 16 < p.M);
-    auto phase = [&](int slot, int h) __attribute__((always_inline)) {
+    const int off[2] = {lds_swz(lane & 15, lane >> 4), lds_swz(lane & 15, 4 + (lane >> 4))};
+    const int wread = wm * HR * kLdsRowB, xread = WS * SW + wn * 16 * kLdsRowB;
+    // The fragments of X are dealt out to the waves one by one: a tile with fewer
+    // rows has fewer products in every wave (fb of them a fragment of W).
+    const int frags = (rows + 15) / 16, fb = GATE || o0 + wm * FA * 16 < p.M ? max((frags - wn + WN - 1) / WN, 0) : 0;
+    auto phase = [&](int wslot, int xslot, int h, auto count) __attribute__((always_inline)) {
+        constexpr int NB = decltype(count)::value;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            const uint8_t* from = lds + slot + off[s];
+            const uint8_t* from = lds + off[s] + wslot + wread + h * (SW / 2);
+            const uint8_t* x = lds + off[s] + xslot + xread;
             if (h == 0)
 #pragma unroll
-                for (int j = 0; j < FB; ++j) b[s][j] = *(const u32x4*)(from + boff + j * 16 * kLdsRowB);
+                for (int j = 0; j < NB; ++j) b[s][j] = *(const u32x4*)(x + j * WN * 16 * kLdsRowB);
 #pragma unroll
-            for (int i = 0; i < FA / 2; ++i) a[s][i] = *(const u32x4*)(from + (h * (BM / 2) + i * 16) * kLdsRowB);
+            for (int i = 0; i < FA / 2; ++i) a[s][i] = *(const u32x4*)(from + i * 16 * kLdsRowB);
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
             for (int i = 0; i < FA / 2; ++i)
 #pragma unroll
-                for (int j = 0; j < FB; ++j)
+                for (int j = 0; j < NB; ++j)
                     acc[h * (FA / 2) + i][j] = mfma_i8(a[s][i], b[s][j], acc[h * (FA / 2) + i][j]);
     };
-    // (Steps behind the last one are requested too: they read nothing or zeros.)
-    issue_w(0, k0, 0);
-    issue_x(0, k0);
-    issue_w(0, k0, 1);
-    issue_w(SLOT, k0 + 1, 0);
-    issue_x(SLOT, k0 + 1);
+    // In the order of the steps: the parts that step 0 finds requested.
+#pragma unroll
+    for (int k = -WS; k < 0; ++k) {
+        if (k > -WS) issue_w((k + WS - 1) * SW, k0 + k + WS - 1, 1);
+        if (k >= -2) issue_x((k + 2) * SX, k0 + k + 2);
+        issue_w((k + WS) * SW, k0 + k + WS, 0);
+    }
     // The tile's scales, a thread one of either side: through LDS to their lanes
     // once the products are done.  (Other LDS arrays, or stores to this one before
     // the loop, make the compiler wait for every DMA before a fragment is read.)
@@ -387,26 +399,34 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
     const int ts = tile.first + min((int)threadIdx.x, rows - 1);
     const float xs = p.x_scale[p.order ? p.order[ts] / p.topk : ts];
     const I8Scales<GATE> wscale = i8_scales<GATE>(p, tile.expert, min(o0 + threadIdx.x, p.M - 1));
-    constexpr int kLater = 2 * WOPS + XOPS;       // operations requested after the part that is needed next
-    wait_vmcnt<kLater>();                         // the first phase of step 0
+    // Operations requested after the parts that the second phase and that the next
+    // step's first one need.
+    constexpr int kLater1 = (WS - 1) * (2 * WOPS + XOPS), kLater0 = (WS > 2 ? 3 : 2) * WOPS + XOPS;
+    wait_vmcnt<kLater0>();
     sync_lds();
-    int slot = 0;
-    auto steps = [&](auto with) __attribute__((always_inline)) {
+    int wcur = 0, wprev = (WS - 1) * SW, xcur = 0;
+    auto steps = [&](auto count) __attribute__((always_inline)) {
+        constexpr bool kWork = decltype(count)::value > 0;
         for (int k = k0; k < nk; ++k) {
-            issue_w(SLOT - slot, k + 1, 1);
-            if constexpr (decltype(with)::value) phase(slot, 0);
-            wait_vmcnt<kLater>();
+            issue_w(wprev, k + WS - 1, 1);
+            if constexpr (kWork) phase(wcur, xcur, 0, count);
+            wait_vmcnt<kLater1>();
             sync_lds();
-            issue_w(slot, k + 2, 0);
-            issue_x(slot, k + 2);
-            if constexpr (decltype(with)::value) phase(slot, 1);
-            wait_vmcnt<kLater>();
+            issue_x(xcur, k + 2);
+            issue_w(wcur, k + WS, 0);
+            if constexpr (kWork) phase(wcur, xcur, 1, count);
+            wait_vmcnt<kLater0>();
             sync_lds();
-            slot = SLOT - slot;
+            wprev = wcur;
+            wcur = wcur == (WS - 1) * SW ? 0 : wcur + SW;
+            xcur = SX - xcur;
         }
     };
-    if (active) steps(std::true_type{});
-    else steps(std::false_type{});
+    if (fb == FB) steps(std::integral_constant<int, FB>{});
+    else if (FB > 3 && fb == 3) steps(std::integral_constant<int, FB < 3 ? FB : 3>{});
+    else if (FB > 2 && fb == 2) steps(std::integral_constant<int, FB < 2 ? FB : 2>{});
+    else if (fb == 1) steps(std::integral_constant<int, 1>{});
+    else steps(std::integral_constant<int, 0>{});
     wait_vmcnt<0>();
 
     if constexpr (OUT == kOutSums) {              // [parts][T][mp] int32, added by k_i8_sum
@@ -417,7 +437,7 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
             const int64_t o = o0 + (wm * FA + i) * 16 + 4 * (lane >> 4);
 #pragma unroll
             for (int j = 0; j < FB; ++j) {
-                const int tl = (wn * FB + j) * 16 + (lane & 15);
+                const int tl = (j * WN + wn) * 16 + (lane & 15);
                 if (tl < rows && o < p.M) *(i32x4*)(out + (int64_t)(tile.first + tl) * mp + o) = acc[i][j];
             }
         }
@@ -430,11 +450,11 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
         sw[threadIdx.x] = wscale.g;
         if constexpr (GATE) {
             sw[BO + threadIdx.x] = wscale.u;
-            sw[2 * BO + threadIdx.x] = wscale.s;
+            sw[2 * BO + threadIdx.x] = wscale.r;
         }
     }
     __syncthreads();
-    if (!active) return;
+    if (fb == 0) return;
     // The lane's 4 consecutive outputs of a row of X, for each pair of fragments.
     const bool whole = rows == BN && o0 + BO <= p.M && p.yvec;
 #pragma unroll
@@ -446,7 +466,7 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
         for (int c = 0; c < (GATE ? 3 : 1); ++c) w[c] = *(const f32x4*)(sw + c * BO + ol);
 #pragma unroll
         for (int j = 0; j < FB; ++j) {
-            const int tl = (wn * FB + j) * 16 + (lane & 15);
+            const int tl = (j * WN + wn) * 16 + (lane & 15);
             const float xt = sx[tl];
             f32x4 y;
 #pragma unroll
@@ -476,23 +496,23 @@ __global__ __launch_bounds__(256) void k_i8_sum(I8Product p) {
     }
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int WS>
 static hipError_t tiled(const I8Product& p, int out, hipStream_t st) {
     const bool gate = out == kOutGate, yf32 = out == kOutF32;
     const int64_t bo = gate ? BM / 2 : BM, mt = (p.M + bo - 1) / bo;
-    const int64_t tiles = p.offsets ? i8_tiles(p.T, p.E, BN) : (p.T + BN - 1) / BN;
-    const dim3 grid((unsigned)(mt * tiles * p.splits)), block(WM * WN * kWave);
+    const int64_t blocks = p.offsets ? i8_blocks(p.T, p.E, BN, mt) : mt * ((p.T + BN - 1) / BN);
+    const dim3 grid((unsigned)(blocks * p.splits)), block(WM * WN * kWave);
     if (p.splits > 1) {
-        const hipError_t e = launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutSums>, grid, block, 0, st, nullptr, nullptr, p);
+        const hipError_t e = launch_kernel(k_i8_tile<BM, BN, WM, WN, WS, kOutSums>, grid, block, 0, st, nullptr, nullptr, p);
         if (e != hipSuccess) return e;
         const int64_t work = p.T * ((p.M + 3) / 4);
         const dim3 sum((unsigned)std::min<int64_t>((work + 255) / 256, 8192));
         return yf32 ? launch_kernel(k_i8_sum<true>, sum, dim3(256), 0, st, nullptr, nullptr, p)
                     : launch_kernel(k_i8_sum<false>, sum, dim3(256), 0, st, nullptr, nullptr, p);
     }
-    if (gate) return launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutGate>, grid, block, 0, st, nullptr, nullptr, p);
-    return yf32 ? launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutF32>, grid, block, 0, st, nullptr, nullptr, p)
-                : launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutBf16>, grid, block, 0, st, nullptr, nullptr, p);
+    if (gate) return launch_kernel(k_i8_tile<BM, BN, WM, WN, WS, kOutGate>, grid, block, 0, st, nullptr, nullptr, p);
+    return yf32 ? launch_kernel(k_i8_tile<BM, BN, WM, WN, WS, kOutF32>, grid, block, 0, st, nullptr, nullptr, p)
+                : launch_kernel(k_i8_tile<BM, BN, WM, WN, WS, kOutBf16>, grid, block, 0, st, nullptr, nullptr, p);
 }
 
 // What a product takes by each kernel, in us, fitted to 170 shapes (1 to 8192
@@ -546,7 +566,7 @@ static I8Choice choose(int64_t T, int64_t K, int64_t M, int64_t E, bool experts,
                       (s > 1 ? 3.1 + (double)(s + 1) * T * M * 4 / 3.1e6 : 0.0), k, s);
         }
     }
-    for (int nt = 1; nt <= 2 && rows <= 64; ++nt) {
+    for (int nt = 1; nt <= 2 && rows <= 128; ++nt) {
         const double tiles = (double)((rows + 16 * nt - 1) / (16 * nt));
         const double x = codes * tiles * std::min<double>(rows, 16 * nt) / 16;
         offer(3.2 + codes / 10.2 + 0.097 * x + 0.8 * K / 4096 + 0.4 * (nt - 1), -nt, 1);
@@ -574,10 +594,10 @@ hipError_t launch_i8_product(const I8Product& q, bool yf32, void* ws, hipStream_
     p.splits = c.splits;
     p.sums = (int*)ws;
     switch (c.kernel) {
-        case 0: return tiled<64, 32, 2, 1>(p, out, st);
-        case 1: return tiled<128, 64, 2, 2>(p, out, st);
-        case 2: return tiled<256, 128, 2, 4>(p, out, st);
-        case 3: return tiled<256, 256, 2, 4>(p, out, st);
+        case 0: return tiled<64, 32, 2, 1, 3>(p, out, st);
+        case 1: return tiled<128, 64, 2, 2, 2>(p, out, st);
+        case 2: return tiled<256, 128, 2, 4, 3>(p, out, st);
+        case 3: return tiled<256, 256, 2, 4, 2>(p, out, st);
         case -1: return stream<1, 4>(p, out, st);
     }
     return stream<2, 4>(p, out, st);

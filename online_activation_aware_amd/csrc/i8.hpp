@@ -4,7 +4,6 @@
 #include "common.hpp"
 #include "launch.hpp"
 #include "lds_dma.hpp"
-#include "moe.hpp"
 
 namespace ttq {
 
@@ -15,62 +14,86 @@ __device__ __forceinline__ i32x4 mfma_i8(const u32x4& a, const u32x4& b, const i
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
-// The matrix of a tile of rows and the rows of it: [first, last).
+// A workgroup's tile where rows [offsets[e], offsets[e+1]) multiply matrix e: the
+// rows [first, last) of its matrix and its tile of W.  first == last: none.
+constexpr int kFewTiles = 96;                     // of an XCD: three for each of its compute units
+
 struct I8Tile {
-    int expert;
-    int first, last;
+    int expert, first, last, mtile;
 };
 
-// Tile `tile` of at most `size` rows each, where rows [offsets[e], offsets[e+1])
-// multiply matrix e (offsets null: all rows matrix 0); first == last where
-// there are fewer.  Every wave finds its own: the tiles of 64 experts at a
-// time by a scan over the lanes.
-__device__ __forceinline__ I8Tile find_tile(const int32_t* offsets, int E, int rows, int size, int tile) {
-    if (offsets == nullptr) {
-        const int f = min(tile * size, rows);
-        return {0, f, min(f + size, rows)};
-    }
-    const int lane = threadIdx.x & (kWave - 1);
-    int before = 0;                               // tiles of the experts before these 64
+// Workgroups go to the eight XCDs in turn: an XCD has every eighth tile of each W
+// (mt in all), so that all XCDs have the same work, and takes an expert's tiles of
+// at most `size` rows one after the other for each of them, so that W comes from
+// memory once.  Where the chip has few tiles a compute unit, the experts' last
+// tiles of less than half the rows come behind all others instead (2048 tokens,
+// two of eight experts, 14336 -> 4096: 310 us, 000 so).
+//
+// Every wave finds its own: the tiles of 64 experts at a time by a scan over the
+// lanes.
+__device__ __forceinline__ I8Tile find_tile(const int32_t* offsets, int E, int size, int mt, int block) {
+    const int lane = threadIdx.x & (kWave - 1), per = (mt + 7) / 8, j = block / 8;
+    int total = 0;
     for (int e0 = 0; e0 < E; e0 += kWave) {
         const int e = e0 + lane;
-        const int lo = e < E ? offsets[e] : 0, hi = e < E ? offsets[e + 1] : 0;
-        const int nt = (hi - lo + size - 1) / size;
-        int p = nt;
+        int n = e < E ? (offsets[e + 1] - offsets[e] + size - 1) / size : 0;
 #pragma unroll
-        for (int s = 1; s < kWave; s <<= 1) {
-            const int u = __shfl_up(p, s);
-            if (lane >= s) p += u;
-        }
-        const uint64_t who = __ballot(before + p > tile);
-        if (who) {
-            // (Read as scalars: a descriptor made of them is one for the wave.)
-            const int l = __builtin_ctzll(who);
-            auto at = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
-            const int first = at(lo) + (tile - before - (at(p) - at(nt))) * size;
-            return {e0 + l, first, min(first + size, at(hi))};
-        }
-        before += __builtin_amdgcn_readlane(p, kWave - 1);
+        for (int s = 1; s < kWave; s <<= 1) n += __shfl_xor(n, s);
+        total += __builtin_amdgcn_readfirstlane(n);
     }
-    return {0, 0, 0};
+    const int late = total * per <= kFewTiles ? size / 2 : 0;   // rows of tiles that come last
+    int before = 0;                               // tiles of the experts before these 64
+    for (int last = 0; last < (late ? 2 : 1); ++last)
+        for (int e0 = 0; e0 < E; e0 += kWave) {
+            const int e = e0 + lane;
+            const int lo = e < E ? offsets[e] : 0, hi = e < E ? offsets[e + 1] : 0;
+            const int first = late ? (hi - lo + late) / size : (hi - lo + size - 1) / size;   // tiles that come first
+            const int nt = last ? (hi - lo > first * size) : first;
+            int p = nt;
+#pragma unroll
+            for (int s = 1; s < kWave; s <<= 1) {
+                const int u = __shfl_up(p, s);
+                if (lane >= s) p += u;
+            }
+            const uint64_t who = __ballot((before + p) * per > j);
+            if (who) {
+                // (Read as scalars: a descriptor made of them is one for the wave.)
+                const int l = __builtin_ctzll(who);
+                auto at = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
+                const int n = at(nt), mine = j - (before + at(p) - n) * per, m = mine / n;
+                const int row = at(lo) + ((last ? at(first) : 0) + mine - m * n) * size, mtile = block % 8 + 8 * m;
+                return {e0 + l, row, mtile < mt ? min(row + size, at(hi)) : row, mtile};
+            }
+            before += __builtin_amdgcn_readlane(p, kWave - 1);
+        }
+    return {0, 0, 0, 0};
 }
 
-// Upper bound of the tiles of `size` rows over E experts.
-inline int64_t i8_tiles(int64_t rows, int64_t E, int64_t size) {
+// Workgroups of find_tile: for an upper bound of the tiles of `size` rows.
+inline int64_t i8_blocks(int64_t rows, int64_t E, int64_t size, int64_t mt) {
     const int64_t a = rows < E ? rows : E;
-    return a + (rows - a) / size;
+    return (a + (rows - a) / size) * ((mt + 7) / 8 * 8);
 }
 
-// The scales of output o: of its sum, or of gate's and up's and 1 / s_down's s.
+// The scales of output o: of its sum, or of gate's and up's and 1 / s_down.
 template <bool GATE>
 struct I8Scales {
-    float g, u, s;
+    float g, u, r;
 };
 template <bool GATE>
 __device__ __forceinline__ I8Scales<GATE> i8_scales(const I8Product& p, int expert, int64_t o) {
     const float* ws = p.w_scale + expert * p.M * (GATE ? 2 : 1);
-    if constexpr (GATE) return {ws[o], ws[p.M + o], p.s_down[expert * p.s_stride + o]};
+    if constexpr (GATE) return {ws[o], ws[p.M + o], 1.f / p.s_down[expert * p.s_stride + o]};
     return {ws[o], 0.f, 0.f};
+}
+
+// act(x) within a few units of the last place: x / (1 + exp(-y)) by the
+// hardware's exp2 and reciprocal (a whole division and expf are half of a gated
+// tile's work behind its products).
+__device__ __forceinline__ float i8_act(float x, int act) {
+    float y = x;
+    if (act != TTQ_ACT_SILU) y = 1.5957691216057308f * (x + 0.044715f * x * x * x);   // 2 sqrt(2 / pi)
+    return x * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * y));
 }
 
 // A result of the sums sg (and su, of gate and up).
@@ -79,7 +102,7 @@ __device__ __forceinline__ float i8_result(const I8Scales<GATE>& w, int act, flo
     const float g = (float)sg * xs * w.g;
     if constexpr (!GATE) return g;
     const float u = (float)su * xs * w.u;
-    return moe_act(g, act) * u / w.s;
+    return i8_act(g, act) * u * w.r;
 }
 
 }  // namespace ttq

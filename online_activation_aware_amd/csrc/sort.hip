@@ -24,7 +24,7 @@
 namespace ttq {
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
-constexpr int64_t kSortMaxBlocks = 256, kSortAlone = 8192;
+constexpr int64_t kSortMaxBlocks = 256, kSortAlone = 2048;
 
 // Slots per workgroup and workgroups for n slots.
 static int64_t sort_span(int64_t n) {
