@@ -515,13 +515,13 @@ static hipError_t tiled(const I8Product& p, int out, hipStream_t st) {
                 : launch_kernel(k_i8_tile<BM, BN, WM, WN, WS, kOutBf16>, grid, block, 0, st, nullptr, nullptr, p);
 }
 
-// What a product takes by each kernel, in us, fitted to 170 shapes (1 to 8192
-// rows, 512 to 14336 channels and outputs), each timed with every kernel; the
-// choice by these costs lies 1.6% over the best kernel of each shape on average,
-// 25% at most.  Some of them (us): 8192 rows of 4096 -> 4096: 256 x 256 128, 256 x 128
-// 153, 128 x 64 193; 2048: 56, 40, 52; 512: 57, 31, 18, 64 x 32 20; 64: 64 x 32 12,
-// streamed 14; 16: 12 and 7; 14336 -> 4096, 1024 rows: 256 x 128 in two parts 78, in
-// one 103; 64 rows: 128 x 64 in eight parts 21, in one 48.
+// What a product takes by each kernel, in us, fitted to 220 shapes (1 to 8192
+// rows, 256 to 14336 channels, 768 to 14336 outputs), each timed with every
+// kernel; the choice by these costs lies 2% over the best kernel of each shape on
+// average, a third at most.  Some of them (us): 8192 rows of 4096 -> 4096: 256 x
+// 256 124, 256 x 128 153, 128 x 64 193; 2048: 56, 40, 52; 512: 57, 31, 18, 64 x 32
+// 20; 64: 64 x 32 12, streamed 14; 16: 12 and 7; 14336 -> 4096, 1024 rows: 256 x 128
+// in two parts 74, in one 103; 64 rows: 128 x 64 in eight parts 21, in one 48.
 //
 // A tile takes `start` and for each 128 channels `step`, `full` where every
 // compute unit has a tile and `more` for each further one that it works on at the
@@ -531,10 +531,10 @@ struct I8Kernel {
     int bm, bn, fit;
     double start, step, full, more;
 };
-constexpr I8Kernel kTiles[] = {{64, 32, 4, 3.0, 0.33, 0.25, 0.15},
-                               {128, 64, 3, 4.3, 0.48, 0.44, 0.31},
-                               {256, 128, 1, 5.0, 0.74, 0.91, 0},
-                               {256, 256, 1, 6.8, 0.96, 1.53, 0}};
+constexpr I8Kernel kTiles[] = {{64, 32, 5, 3.1, 0.29, 0.25, 0.14},
+                               {128, 64, 3, 3.7, 0.51, 0.44, 0.31},
+                               {256, 128, 1, 5.3, 0.67, 0.95, 0},
+                               {256, 256, 1, 8.5, 0.67, 1.52, 0}};
 constexpr int kMaxSplits = 16;
 
 struct I8Choice {
@@ -549,7 +549,7 @@ static I8Choice choose(int64_t T, int64_t K, int64_t M, int64_t E, bool experts,
     I8Choice best{0, 1};
     double least = 0;
     auto offer = [&](double us, int kernel, int splits) {
-        us = std::max(us, 3.0 + codes / 5.2 + (splits > 1 ? 3.1 : 0.0));
+        us = std::max(us, 3.1 + codes / 5.2 + (splits > 1 ? 3.2 : 0.0));
         if (least > 0 && us >= least) return;
         least = us;
         best = {kernel, splits};
@@ -563,13 +563,13 @@ static I8Choice choose(int64_t T, int64_t K, int64_t M, int64_t E, bool experts,
             const double n = std::ceil(tiles / 256), at_once = std::min(n, (double)c.fit);
             const double step = c.step + (c.full - c.step) * std::min(tiles / 256, 1.0) + c.more * (at_once - 1);
             offer(n / at_once * (c.start + steps / s * step) +
-                      (s > 1 ? 3.1 + (double)(s + 1) * T * M * 4 / 3.1e6 : 0.0), k, s);
+                      (s > 1 ? 3.2 + (double)(s + 1) * T * M * 4 / 3.1e6 : 0.0), k, s);
         }
     }
     for (int nt = 1; nt <= 2 && rows <= 128; ++nt) {
         const double tiles = (double)((rows + 16 * nt - 1) / (16 * nt));
         const double x = codes * tiles * std::min<double>(rows, 16 * nt) / 16;
-        offer(3.2 + codes / 10.2 + 0.097 * x + 0.8 * K / 4096 + 0.4 * (nt - 1), -nt, 1);
+        offer(3.0 + codes / 8.6 + 0.119 * x + 0.9 * K / 4096 + (nt - 1) * (0.03 + 5e-6 * M * tiles), -nt, 1);
     }
     return best;
 }

@@ -477,6 +477,7 @@ TTQ_ACTS = {"silu": 0, "gelu": 1}
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _current_stream(index: int) -> int:
@@ -505,7 +506,7 @@ def _on_tensor_device(fn):
         if not isinstance(X, torch.Tensor) or not X.is_cuda:
             raise TypeError(f"{first} must be a device tensor")
         index = X.get_device()
-        if stream is None and index == torch.cuda.current_device():
+        if stream is None and index == _current_device():
             return fn(*args, stream=_current_stream(index), **kwargs)
         with torch.cuda.device(index):
             ts = _torch_stream(stream)
@@ -516,6 +517,11 @@ def _on_tensor_device(fn):
 
 def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> int:
     """The address of a dense tensor of this dtype and shape on this device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype:
         raise TypeError(f"{name} must be a {dtype} tensor")
     if t.get_device() != device:
@@ -735,6 +741,12 @@ def ttq_qgemm_adapters(X: torch.Tensor, s: torch.Tensor, codes: torch.Tensor, sc
 
 def _rows8(codes: torch.Tensor, name: str, dev: int) -> int:
     """Row stride of a matrix of 8-bit codes."""
+    try:
+        st, shape = codes.stride(), codes.shape
+        if codes.dtype is torch.int8 and codes.get_device() == dev and len(st) == 2 and st[1] == 1:
+            return st[0] if shape[0] > 1 else shape[1]
+    except AttributeError:
+        pass
     if not isinstance(codes, torch.Tensor) or codes.dtype is not torch.int8:
         raise TypeError(f"{name} must be a torch.int8 tensor")
     if codes.get_device() != dev:
@@ -753,8 +765,10 @@ def _on(t: torch.Tensor, name: str, dev: int) -> torch.Tensor:
 def _wide_stride(t: torch.Tensor, name: str) -> int:
     """Row stride of a matrix whose rows need not be whole 16-byte pieces
     long; that of a single row does not matter."""
-    ld = _row_stride(t, name)
-    return ld if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+    st, (rows, row) = t.stride(), t.shape if t.dim() == 2 else (0, 0)
+    if len(st) != 2 or st[1] != 1 and row > 1:
+        raise ValueError(f"{name} must be 2-D with unit stride in its last dimension")
+    return st[0] if rows > 1 else -(-row // 8) * 8
 
 
 @_on_tensor_device
@@ -796,11 +810,15 @@ def ttq_gemm_i8(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_scale
     M = W.shape[0]
     if W.shape[1] != K:
         raise ValueError(f"W must be [M][{K}] (got {list(W.shape)})")
-    Y = _output(Y, (T, M), y_dtype, X)
-    wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_gemm_i8_workspace_bytes(T, K, M), X)
-    _check(lib().ttq_gemm_i8(X.data_ptr(), _dense(x_scale, "x_scale", torch.float32, (T,), dev), T, K, ldx, W.data_ptr(),
-                             _dense(w_scale, "w_scale", torch.float32, (M,), dev), M, ldw, Y.data_ptr(), _code(Y),
-                             _row_stride(Y, "Y"), wp, wn, stream))
+    if Y is None:
+        Y, ldy = X.new_empty((T, M), dtype=y_dtype), M
+    else:
+        ldy = _row_stride(_output(Y, (T, M), None, X), "Y")
+    L = lib()
+    wp, wn, ws = _scratch(ws, 0 if ws is not None else L.ttq_gemm_i8_workspace_bytes(T, K, M), X)
+    _check(L.ttq_gemm_i8(X.data_ptr(), _dense(x_scale, "x_scale", torch.float32, (T,), dev), T, K, ldx, W.data_ptr(),
+                         _dense(w_scale, "w_scale", torch.float32, (M,), dev), M, ldw, Y.data_ptr(), _code(Y), ldy,
+                         wp, wn, stream))
     return Y
 
 
@@ -826,12 +844,16 @@ def ttq_qgemm_i8(X: torch.Tensor, s: Optional[torch.Tensor], W: torch.Tensor, w_
     M = W.shape[0]
     if W.shape[1] != K:
         raise ValueError(f"W must be [M][{K}] (got {list(W.shape)})")
-    Y = _output(Y, (T, M), y_dtype, X)
-    wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_qgemm_i8_workspace_bytes(T, K, M), X)
-    _check(lib().ttq_qgemm_i8(X.data_ptr(), _code(X), T, K, ldx,
-                              None if s is None else _dense(s, "s", torch.float32, (K,), dev), W.data_ptr(),
-                              _dense(w_scale, "w_scale", torch.float32, (M,), dev), M, ldw, Y.data_ptr(), _code(Y),
-                              _row_stride(Y, "Y"), wp, wn, stream))
+    if Y is None:
+        Y, ldy = X.new_empty((T, M), dtype=y_dtype), M
+    else:
+        ldy = _row_stride(_output(Y, (T, M), None, X), "Y")
+    L = lib()
+    wp, wn, ws = _scratch(ws, 0 if ws is not None else L.ttq_qgemm_i8_workspace_bytes(T, K, M), X)
+    _check(L.ttq_qgemm_i8(X.data_ptr(), _code(X), T, K, ldx,
+                          None if s is None else _dense(s, "s", torch.float32, (K,), dev), W.data_ptr(),
+                          _dense(w_scale, "w_scale", torch.float32, (M,), dev), M, ldw, Y.data_ptr(), _code(Y), ldy,
+                          wp, wn, stream))
     return Y
 
 
@@ -857,15 +879,27 @@ def ttq_moe_sort(ids: torch.Tensor, E: int, offsets: Optional[torch.Tensor] = No
     dev = ids.get_device()
     ip = _dense(ids, "ids", torch.int32, (T, topk), dev)
     n = E + 1 if 0 <= E <= 1024 else 0       # others are refused below
-    offsets = ids.new_empty((n,)) if offsets is None else offsets
-    order = ids.new_empty((T * topk,)) if order is None else order
-    pos = ids.new_empty((T, topk)) if pos is None else pos
+    L = lib()
+    if offsets is None:
+        offsets = ids.new_empty((n,))
+        fp = offsets.data_ptr()
+    else:
+        fp = _dense(offsets, "offsets", torch.int32, (n,), dev)
+    if order is None:
+        order = ids.new_empty((T * topk,))
+        op = order.data_ptr()
+    else:
+        op = _dense(order, "order", torch.int32, (T * topk,), dev)
+    if pos is None:
+        pos = ids.new_empty((T, topk))
+        pp = pos.data_ptr()
+    else:
+        pp = _dense(pos, "pos", torch.int32, (T, topk), dev)
     if ws is None:
-        ws = ids.new_empty(lib().ttq_moe_sort_workspace_bytes(T, topk, E), dtype=torch.uint8)
-    wp, wn, ws = _scratch(ws, 0, ids)
-    _check(lib().ttq_moe_sort(ip, T, topk, E, _dense(offsets, "offsets", torch.int32, (n,), dev),
-                              _dense(order, "order", torch.int32, (T * topk,), dev),
-                              _dense(pos, "pos", torch.int32, (T, topk), dev), wp, wn, stream))
+        need = L.ttq_moe_sort_workspace_bytes(T, topk, E)
+        ws = ids.new_empty((need,), dtype=torch.uint8) if need else None
+    wp, wn = (None, 0) if ws is None else _scratch(ws, 0, ids)[:2]
+    _check(L.ttq_moe_sort(ip, T, topk, E, fp, op, pp, wp, wn, stream))
     return offsets, order, pos
 
 
@@ -902,10 +936,14 @@ def ttq_moe_combine(R: torch.Tensor, pos: torch.Tensor, w: Optional[torch.Tensor
         raise ValueError("pos must be [T][topk]")
     T, topk = pos.shape
     dev = R.get_device()
-    Y = _output(Y, (T, M), R.dtype if y_dtype is None else y_dtype, R)
+    if Y is None:
+        Y = R.new_empty((T, M), dtype=R.dtype if y_dtype is None else y_dtype)
+        ldy = M
+    else:
+        ldy = _row_stride(_output(Y, (T, M), None, R), "Y")
     _check(lib().ttq_moe_combine(R.data_ptr(), _code(R), rows, ldr, _dense(pos, "pos", torch.int32, (T, topk), dev),
                                  None if w is None else _dense(w, "w", torch.float32, (T, topk), dev), T, topk, M,
-                                 Y.data_ptr(), _code(Y), _row_stride(Y, "Y"), stream))
+                                 Y.data_ptr(), _code(Y), ldy, stream))
     return Y
 
 
@@ -920,16 +958,19 @@ def ttq_moe_combine_grad(dY: torch.Tensor, R: torch.Tensor, pos: torch.Tensor, w
     if _on(R, "R", dev).shape[1] != M or pos.dim() != 2:
         raise ValueError(f"R must be [rows][{M}] and pos [T][topk]")
     topk = pos.shape[1]
-    dR = _output(dR, tuple(R.shape), R.dtype, dY, "dR")
-    if dR.dtype != R.dtype:
+    rt = _code(R)
+    dR = _output(dR, R.shape, R.dtype, dY, "dR")
+    if dR.dtype is not R.dtype:
         raise TypeError("dR must have R's dtype")
     if dw is None:
         dw = dY.new_empty((T, topk), dtype=torch.float32)
-    _check(lib().ttq_moe_combine_grad(dY.data_ptr(), _code(dY), T, M, lddy, R.data_ptr(), _code(R), R.shape[0], ldr,
+        dwp = dw.data_ptr()
+    else:
+        dwp = _dense(dw, "dw", torch.float32, (T, topk), dev)
+    _check(lib().ttq_moe_combine_grad(dY.data_ptr(), _code(dY), T, M, lddy, R.data_ptr(), rt, R.shape[0], ldr,
                                       _dense(pos, "pos", torch.int32, (T, topk), dev),
                                       None if w is None else _dense(w, "w", torch.float32, (T, topk), dev), topk,
-                                      dR.data_ptr(), _wide_stride(dR, "dR"),
-                                      _dense(dw, "dw", torch.float32, (T, topk), dev), stream))
+                                      dR.data_ptr(), _wide_stride(dR, "dR"), dwp, stream))
     return dR, dw
 
 
