@@ -510,8 +510,8 @@ ttq_status ttq_quantize_rows(const void* X, int xt, int64_t R, int64_t K, int64_
  *   rounded once more to a bf16 Y.
  *   X: [T][K] int8, stride ldx;  W: [M][K] int8, stride ldw, e.g. both from
  *   ttq_quantize_rows.  Y: [T][M] (yt), stride ldy, overwritten; no overlap.
- *   ldx and ldw up to 2^22 (else TTQ_ERR_UNSUPPORTED).  T == 0 or M == 0 is an
- *   empty call.  ws: ttq_gemm_i8_workspace_bytes(T, K, M) bytes, 256-byte
+ *   ldx and ldw up to 2^22 and T * M up to about 2^38 (else
+ *   TTQ_ERR_UNSUPPORTED).  T == 0 or M == 0 is an empty call.  ws: ttq_gemm_i8_workspace_bytes(T, K, M) bytes, 256-byte
  *   aligned; calls that may run at the same time need workspaces of their own.
  */
 ttq_status ttq_gemm_i8(const int8_t* X, const float* x_scale, int64_t T, int64_t K, int64_t ldx, const int8_t* W,
@@ -587,8 +587,8 @@ ttq_status ttq_moe_combine(const void* R, int rt, int64_t rows, int64_t ldr, con
  *   row), reproducible run to run.
  *   dY: [T][M] (yt), stride lddy; dR: [rows][M] of R's dtype rt, stride lddr,
  *   16-byte aligned, its row stride a multiple of 16 bytes; dw: [T][topk].  dR or
- *   dw may be NULL (R may be, too, without dw).  dR must not overlap R or dY.
- *   T == 0 is an empty call.
+ *   dw may be NULL (R may be, too, without dw).  dR must not overlap R or dY.  M
+ *   positive, any.  T == 0 is an empty call.
  */
 ttq_status ttq_moe_combine_grad(const void* dY, int yt, int64_t T, int64_t M, int64_t lddy, const void* R, int rt,
                                 int64_t rows, int64_t ldr, const int32_t* pos, const float* w, int64_t topk,

@@ -528,13 +528,13 @@ static hipError_t tiled(const I8Product& p, int out, hipStream_t st) {
 // same time, at most `fit`.  Parts of the channels cost a second launch and the
 // traffic of their sums.  Nothing is faster than W's bytes.
 struct I8Kernel {
-    int bm, bn, fit;
+    int bm, bn, threads, fit;
     double start, step, full, more;
 };
-constexpr I8Kernel kTiles[] = {{64, 32, 5, 3.1, 0.29, 0.25, 0.14},
-                               {128, 64, 3, 3.7, 0.51, 0.44, 0.31},
-                               {256, 128, 1, 5.3, 0.67, 0.95, 0},
-                               {256, 256, 1, 8.5, 0.67, 1.52, 0}};
+constexpr I8Kernel kTiles[] = {{64, 32, 128, 5, 3.1, 0.29, 0.25, 0.14},
+                               {128, 64, 256, 3, 3.7, 0.51, 0.44, 0.31},
+                               {256, 128, 512, 1, 5.3, 0.67, 0.95, 0},
+                               {256, 256, 512, 1, 8.5, 0.67, 1.52, 0}};
 constexpr int kMaxSplits = 16;
 
 struct I8Choice {
@@ -542,11 +542,19 @@ struct I8Choice {
     int splits;
 };
 
+// A grid has fewer than 2^32 threads.
+static bool grid_fits(double blocks, int threads) { return blocks * threads < 4294967296.0; }
+
+// The largest tiles (of gate and up, too) cover T x M.
+bool i8_product_fits(int64_t T, int64_t M, int64_t E) {
+    return grid_fits((double)((T + 255) / 256 + E) * (double)((M + 127) / 128 + 8), 512);
+}
+
 static I8Choice choose(int64_t T, int64_t K, int64_t M, int64_t E, bool experts, bool gate) {
     const int64_t rows = experts ? std::max<int64_t>((T + E - 1) / E, 1) : T;    // of a matrix, on average
     const double mats = experts ? (double)std::min(T, E) : 1;
     const double steps = (double)((K + kLdsRowB - 1) / kLdsRowB), codes = mats * (double)(K * M) * (gate ? 2 : 1) / 1e6;
-    I8Choice best{0, 1};
+    I8Choice best{3, 1};                          // (its grid fits)
     double least = 0;
     auto offer = [&](double us, int kernel, int splits) {
         us = std::max(us, 3.1 + codes / 5.2 + (splits > 1 ? 3.2 : 0.0));
@@ -560,6 +568,7 @@ static I8Choice choose(int64_t T, int64_t K, int64_t M, int64_t E, bool experts,
         for (int s = 1; s <= (experts ? 1 : kMaxSplits); s *= 2) {
             if (s > 1 && steps < 2 * s) break;
             const double tiles = (double)(((M + bo - 1) / bo) * ((rows + c.bn - 1) / c.bn) * s) * mats;
+            if (!grid_fits(((double)T / c.bn + 1 + (double)E) * ((double)M / bo + 8) * s, c.threads)) break;
             const double n = std::ceil(tiles / 256), at_once = std::min(n, (double)c.fit);
             const double step = c.step + (c.full - c.step) * std::min(tiles / 256, 1.0) + c.more * (at_once - 1);
             offer(n / at_once * (c.start + steps / s * step) +
@@ -569,6 +578,7 @@ static I8Choice choose(int64_t T, int64_t K, int64_t M, int64_t E, bool experts,
     for (int nt = 1; nt <= 2 && rows <= 128; ++nt) {
         const double tiles = (double)((rows + 16 * nt - 1) / (16 * nt));
         const double x = codes * tiles * std::min<double>(rows, 16 * nt) / 16;
+        if (!grid_fits(((double)T / (16 * nt) + 1 + (double)E) * ((double)M / kStreamRows + 8), 256)) break;
         offer(3.0 + codes / 8.6 + 0.119 * x + 0.9 * K / 4096 + (nt - 1) * (0.03 + 5e-6 * M * tiles), -nt, 1);
     }
     return best;
@@ -577,13 +587,6 @@ static I8Choice choose(int64_t T, int64_t K, int64_t M, int64_t E, bool experts,
 size_t i8_product_ws_bytes(int64_t T, int64_t K, int64_t M) {
     const I8Choice c = choose(T, K, M, 1, false, false);
     return c.splits > 1 ? (size_t)c.splits * T * ((M + 3) / 4 * 4) * 4 : 0;
-}
-
-// A grid has fewer than 2^32 threads: of the kernel with the smallest tiles, and
-// of the streaming one, which few rows may take.
-bool i8_product_fits(int64_t T, int64_t M) {
-    const double most = 4294967296.0;
-    return (double)((T + 31) / 32) * (double)((M + 63) / 64) * 128 < most && (T > 64 || (double)M / 16 * 4 * 256 < most);
 }
 
 hipError_t launch_i8_product(const I8Product& q, bool yf32, void* ws, hipStream_t st) {

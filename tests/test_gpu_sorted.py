@@ -128,6 +128,19 @@ def test_combine_grad(T, rt, yt, Tn, topk, M, rows, weighted):
     assert np.all(got[~have] == 0)
 
 
+def test_no_rows_at_all(T):
+    say("rows 0")
+    pos = i32_dev(np.zeros((3, 2)))
+    none = torch.empty((0, 40), device="cuda")
+    assert torch.equal(T.ttq_moe_combine(none, pos), torch.zeros((3, 40), device="cuda"))
+    dY = torch.ones((3, 40), device="cuda")
+    dR, dw = T.ttq_moe_combine_grad(dY, none, pos)
+    assert dR.shape == (0, 40) and torch.count_nonzero(dw) == 0
+    assert T.ttq_moe_gather(dY, pos, R=none) is none
+    few = i32_dev(np.zeros((0, 2)))
+    assert T.ttq_moe_combine(dY, few).shape == (0, 40) and T.ttq_moe_gather(dY[:0], few).shape == (0, 40)
+
+
 def test_grad_parts(T):
     """dR or dw alone, through the C call."""
     say("combine_grad parts")
