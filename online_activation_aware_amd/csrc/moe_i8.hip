@@ -8,9 +8,21 @@
 // scale needs the whole row, and a bf16 h would move one code in eight.  The
 // rows of h in 8 bits go through the second product into fp32 rows, which are
 // weighted and added per token.
+#include <algorithm>
+
 #include "i8.hpp"
+#include "rows_i8.hpp"
+#include "sort.hpp"
 
 namespace ttq {
+
+// Few slots: workgroup 0 sorts them while the others quantize the tokens' rows.
+// (The layer for 64 tokens of 2048 channels, 6 experts each: 102.7 us with two launches, 98.3.)
+template <bool F32>
+__global__ __launch_bounds__(kSortThreads) void k_moe_sort_rows(SortArgs s, I8RowsArgs r) {
+    if (blockIdx.x == 0) sort_block<true>(s, 0, 1);
+    else quantize_rows<F32, 2, true>(r, blockIdx.x - 1, gridDim.x - 1);
+}
 
 struct MoeI8Layout {
     size_t offsets, order, pos, sort, q, qs, h, hq, hs, total;
@@ -48,18 +60,27 @@ hipError_t launch_moe_i8(const ttq_moe_i8_args* a, char* ws, hipStream_t st) {
     int32_t *offsets = (int32_t*)(ws + L.offsets), *order = (int32_t*)(ws + L.order), *pos = (int32_t*)(ws + L.pos);
     int8_t *q = (int8_t*)(ws + L.q), *hq = (int8_t*)(ws + L.hq);
     float *qs = (float*)(ws + L.qs), *hs = (float*)(ws + L.hs), *h = (float*)(ws + L.h);
-    hipError_t e = launch_moe_sort(a->ids, n, E, offsets, order, pos, (int32_t*)(ws + L.sort), st);
-    if (e != hipSuccess) return e;
     const bool per = a->gate_up.s_stride != 0;    // an s_in for each expert: rows of slots, sorted, else of tokens
     I8RowsArgs rq{a->X, a->xt == TTQ_F32, a->ldx, per ? n : a->T, a->K, a->gate_up.s, true, q, a->K, qs};
-    if (per) {
-        rq.nrows = offsets + E;
-        rq.order = order;
-        rq.topk = topk;
-        rq.ids = a->ids;
-        rq.s_stride = a->gate_up.s_stride;
+    hipError_t e;
+    if (!per && n <= kSortAlone && a->K <= kSortThreads * kRowSeg * kRowSegs) {
+        const SortArgs s = sort_args(a->ids, n, E, offsets, order, pos, nullptr);
+        const dim3 grid((unsigned)std::min<int64_t>(a->T, 511) + 1), block(kSortThreads);
+        e = rq.xf32 ? launch_kernel(k_moe_sort_rows<true>, grid, block, 0, st, nullptr, nullptr, s, rq)
+                    : launch_kernel(k_moe_sort_rows<false>, grid, block, 0, st, nullptr, nullptr, s, rq);
+    } else {
+        e = launch_moe_sort(a->ids, n, E, offsets, order, pos, (int32_t*)(ws + L.sort), st);
+        if (e != hipSuccess) return e;
+        if (per) {
+            rq.nrows = offsets + E;
+            rq.order = order;
+            rq.topk = topk;
+            rq.ids = a->ids;
+            rq.s_stride = a->gate_up.s_stride;
+        }
+        e = launch_quantize_rows(rq, st);
     }
-    if ((e = launch_quantize_rows(rq, st)) != hipSuccess) return e;
+    if (e != hipSuccess) return e;
     I8Product p{q, a->K, qs, n, a->K, a->gate_up.codes, a->K, a->gate_up.scale, a->I, h, a->I};
     p.offsets = offsets;
     p.order = per ? nullptr : order;

@@ -19,144 +19,29 @@
 #include "common.hpp"
 #include "launch.hpp"
 #include "lds_dma.hpp"
+#include "sort.hpp"
 #include "wave.hpp"
 
 namespace ttq {
-
-constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / kWave;
-constexpr int64_t kSortMaxBlocks = 256, kSortAlone = 2048;
-
-// Slots per workgroup and workgroups for n slots.
-static int64_t sort_span(int64_t n) {
-    if (n <= kSortAlone) return kSortAlone;       // one launch
-    const int64_t per = (n + kSortMaxBlocks - 1) / kSortMaxBlocks;
-    return std::max<int64_t>((per + kSortThreads - 1) / kSortThreads, 1) * kSortThreads;
-}
-static int64_t sort_blocks(int64_t n) { return std::max<int64_t>((n + sort_span(n) - 1) / sort_span(n), 1); }
 
 size_t moe_sort_ws_bytes(int64_t n, int64_t E) {
     return sort_blocks(n) > 1 ? (size_t)(sort_blocks(n) * E) * 4 : 0;
 }
 
-// The lanes whose key equals this lane's; `bits` bits of it count.
-__device__ __forceinline__ uint64_t same_lanes(int key, int bits) {
-    uint64_t m = ~0ull;
-    for (int b = 0; b < bits; ++b) {
-        const bool one = (key >> b) & 1;
-        const uint64_t w = __ballot(one);
-        m &= one ? w : ~w;
-    }
-    return m;
-}
-
-// Counts [blocks][E] of each workgroup's slots.
 template <bool PLACE>
-__global__ __launch_bounds__(kSortThreads) void k_moe_sort(const int32_t* __restrict__ ids, int64_t n, int E, int bits,
-                                                           int64_t span, int32_t* __restrict__ counts,
-                                                           int32_t* __restrict__ offsets, int32_t* __restrict__ order,
-                                                           int32_t* __restrict__ pos) {
-    __shared__ int32_t place[kSortWaves][kMoeMaxExperts];
-    __shared__ int32_t wsum[kSortWaves];
-    const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-    const int64_t first = blockIdx.x * span;
-    const int64_t w0 = first + wave * (span / kSortWaves), w1 = min(w0 + span / kSortWaves, n);
-    for (int e = lane; e < E; e += kWave) place[wave][e] = 0;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    auto key_at = [&](int64_t i) __attribute__((always_inline)) {
-        const int id = i < w1 ? ids[i] : -1;
-        return id >= 0 && id < E ? id : E;        // E: no expert
-    };
-    // A wave alone touches its counts, and its LDS accesses are in order: between
-    // its rounds only the compiler is held to that.
-    for (int64_t i = w0; i < w1; i += kWave) {
-        const int key = key_at(i + lane);
-        const uint64_t m = same_lanes(key, bits);
-        if (key < E && lane == __builtin_ctzll(m)) place[wave][key] += __builtin_popcountll(m);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-    __syncthreads();
-    if constexpr (!PLACE) {
-        for (int e = tid; e < E; e += kSortThreads) {
-            int c = 0;
-            for (int w = 0; w < kSortWaves; ++w) c += place[w][e];
-            counts[(int64_t)blockIdx.x * E + e] = c;
-        }
-        return;
-    }
-    // Thread e: slots of expert e in all and before this workgroup, then the
-    // experts' first rows by a scan over the threads.
-    int all = 0, mine = 0;
-    if (tid < E) {
-        if (gridDim.x == 1) {
-            for (int w = 0; w < kSortWaves; ++w) all += place[w][tid];
-        } else {
-#pragma unroll 16
-            for (int b = 0; b < (int)gridDim.x; ++b) {
-                const int c = counts[b * E + tid];
-                if (b < (int)blockIdx.x) mine += c;
-                all += c;
-            }
-        }
-    }
-    int sum = all;
-#pragma unroll
-    for (int s = 1; s < kWave; s <<= 1) {
-        const int u = __shfl_up(sum, s);
-        if (lane >= s) sum += u;
-    }
-    if (lane == kWave - 1) wsum[wave] = sum;
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < kSortWaves; ++w) {
-        if (w < wave) before += wsum[w];
-        total += wsum[w];
-    }
-    if (tid < E) {
-        const int lo = before + sum - all;
-        if (blockIdx.x == 0) {
-            offsets[tid] = lo;
-            if (tid == 0) offsets[E] = total;
-        }
-        int at = lo + mine;
-        for (int w = 0; w < kSortWaves; ++w) {
-            const int c = place[w][tid];
-            place[w][tid] = at;
-            at += c;
-        }
-    }
-    __syncthreads();
-    for (int64_t i = w0; i < w1; i += kWave) {
-        const int key = key_at(i + lane);
-        const uint64_t m = same_lanes(key, bits);
-        const int rank = __builtin_popcountll(m & ((1ull << lane) - 1));
-        int r = -1;
-        if (key < E) {
-            r = place[wave][key] + rank;
-            order[r] = (int32_t)(i + lane);
-        }
-        if (i + lane < w1) pos[i + lane] = r;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        if (key < E && rank == 0) place[wave][key] += __builtin_popcountll(m);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
-    // Behind the last row there is no slot.
-    const int64_t end = min(first + span, n);
-    for (int64_t r = max(first, (int64_t)total) + tid; r < end; r += kSortThreads) order[r] = -1;
+__global__ __launch_bounds__(kSortThreads) void k_moe_sort(SortArgs a) {
+    sort_block<PLACE>(a, blockIdx.x, gridDim.x);
 }
 
 hipError_t launch_moe_sort(const int32_t* ids, int64_t n, int E, int32_t* offsets, int32_t* order, int32_t* pos,
                            int32_t* ws, hipStream_t st) {
-    const int64_t span = sort_span(n);
+    const SortArgs a = sort_args(ids, n, E, offsets, order, pos, ws);
     const dim3 grid((unsigned)sort_blocks(n)), block(kSortThreads);
-    int bits = 1;
-    while ((1 << bits) <= E) ++bits;              // keys 0 .. E
     if (grid.x > 1) {
-        const hipError_t e = launch_kernel(k_moe_sort<false>, grid, block, 0, st, nullptr, nullptr, ids, n, E, bits, span, ws,
-                                           offsets, order, pos);
+        const hipError_t e = launch_kernel(k_moe_sort<false>, grid, block, 0, st, nullptr, nullptr, a);
         if (e != hipSuccess) return e;
     }
-    return launch_kernel(k_moe_sort<true>, grid, block, 0, st, nullptr, nullptr, ids, n, E, bits, span, ws, offsets, order,
-                         pos);
+    return launch_kernel(k_moe_sort<true>, grid, block, 0, st, nullptr, nullptr, a);
 }
 
 // ------------------------------------------------------------------ rows

@@ -6,7 +6,7 @@ import torch
 
 import i8_ref as ref
 from gpu_util import f32_dev, host, i32_dev, say
-from test_gpu_i8 import enc, i8_dev, moe_inputs, rounded, same
+from test_gpu_i8 import enc, i8_dev, moe_inputs, moe_ref, near, rounded, same
 
 pytestmark = pytest.mark.gpu
 
@@ -183,3 +183,16 @@ def test_quantized_state_and_projection_of_a_prompt(T):
     assert torch.equal(T.ttq_gemm_i8(q, xs, W, ws), Y)
     assert torch.equal(T.ttq_gemm_i8(q, xs, W[100:200], ws[100:200]), Y[:, 100:200])
     same(T.ttq_gemm_i8(q, xs, W, ws, y_dtype=torch.bfloat16), rounded(host(Y), "bf16"))
+
+
+@pytest.mark.parametrize("Tn,topk,K,per_in", [(600, 1, 64, False), (1024, 2, 32, False), (1025, 2, 32, False), (3, 2, 16400, False),
+                                              (5, 3, 16384, False), (600, 3, 32, True)])
+def test_moe_sorted_beside_the_rows(T, Tn, topk, K, per_in):
+    """Few slots are sorted while the tokens' rows are quantized: more rows than
+    workgroups, the most slots of it and one token more, channels that a workgroup
+    holds and that it does not."""
+    say(f"moe_i8 sorted beside the rows T={Tn} topk={topk} K={K}")
+    d = moe_inputs(Tn + K, Tn, 3, topk, K, 48, 20, "bf16", per_in, False, True)
+    ws = torch.full((T.ttq_moe_i8_workspace_bytes(Tn, topk, K, 48, 20, 3),), 0xFF, dtype=torch.uint8, device="cuda")
+    Y = T.ttq_moe_i8(d["X"], i32_dev(d["ids"]), f32_dev(d["w"]), d["gate_up"], d["down"], ws=ws)
+    near(Y, *moe_ref(d, "silu"), "f32")
