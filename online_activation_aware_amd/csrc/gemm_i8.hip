@@ -276,11 +276,10 @@ hipError_t launch_i8_one(const I8RowsArgs& x, const I8Product& q, bool yf32, hip
 //
 // A step has two phases: X and the first half of every wave's rows of W, then the
 // second half; each part of a slot is requested again as soon as every wave has
-// read it: X, which tiles share in the L2, three phases ahead of its use, W two
-// more for each of its WS slots beyond two.  (A step's 64 KB take longer than one
-// step's products to arrive.  Eight experts of 14336 -> 4096, two tiles of 256 rows
-// each: two slots of W 340 us, three 000.)
-template <int BM, int BN, int WM, int WN, int WS, int OUT>
+// read it, three phases ahead of its use.  (A step's 64 KB take longer than one
+// step's products to arrive.  A third slot of W for the smaller tiles: 64 x 4096 ->
+// 14336 15.1 us, two 14.5; 768 rows 55 and 54.)
+template <int BM, int BN, int WM, int WN, int OUT>
 __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
     constexpr bool GATE = OUT == kOutGate, YF32 = OUT != kOutBf16;
     constexpr int NW = WM * WN;
@@ -290,7 +289,7 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
     constexpr int G = GATE ? 2 : 1, BO = BM / G;                // outputs of a tile
     constexpr int SW = BM * kLdsRowB, SX = BN * kLdsRowB;       // slots: W of the first phase and of the second; X
     constexpr int kStep = kLdsRowB;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[WS * SW + 2 * SX];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * SW + 2 * SX];
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wm = wave % WM, wn = wave / WM;
     // One matrix: the workgroups that an XCD receives are consecutive in an order
@@ -357,11 +356,11 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
         const int gone = k >= nk || 16 * ch >= (int)p.K - k * kStep ? INT32_MIN : 0;
 #pragma unroll
         for (int i = 0; i < XOPS; ++i)
-            dma_to_lds<16>(rx, lds + WS * SW + slot + (wave * XOPS + i) * 1024, xoff[i] | gone, k * kStep);
+            dma_to_lds<16>(rx, lds + 2 * SW + slot + (wave * XOPS + i) * 1024, xoff[i] | gone, k * kStep);
     };
     u32x4 a[2][FA / 2], b[2][FB];                 // fragments of the two 64-channel halves
     const int off[2] = {lds_swz(lane & 15, lane >> 4), lds_swz(lane & 15, 4 + (lane >> 4))};
-    const int wread = wm * HR * kLdsRowB, xread = WS * SW + wn * 16 * kLdsRowB;
+    const int wread = wm * HR * kLdsRowB, xread = 2 * SW + wn * 16 * kLdsRowB;
     // The fragments of X are dealt out to the waves one by one: a tile with fewer
     // rows has fewer products in every wave (fb of them a fragment of W).
     const int frags = (rows + 15) / 16, fb = GATE || o0 + wm * FA * 16 < p.M ? max((frags - wn + WN - 1) / WN, 0) : 0;
@@ -386,12 +385,11 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
                     acc[h * (FA / 2) + i][j] = mfma_i8(a[s][i], b[s][j], acc[h * (FA / 2) + i][j]);
     };
     // In the order of the steps: the parts that step 0 finds requested.
-#pragma unroll
-    for (int k = -WS; k < 0; ++k) {
-        if (k > -WS) issue_w((k + WS - 1) * SW, k0 + k + WS - 1, 1);
-        if (k >= -2) issue_x((k + 2) * SX, k0 + k + 2);
-        issue_w((k + WS) * SW, k0 + k + WS, 0);
-    }
+    issue_x(0, k0);
+    issue_w(0, k0, 0);
+    issue_w(0, k0, 1);
+    issue_x(SX, k0 + 1);
+    issue_w(SW, k0 + 1, 0);
     // The tile's scales, a thread one of either side: through LDS to their lanes
     // once the products are done.  (Other LDS arrays, or stores to this one before
     // the loop, make the compiler wait for every DMA before a fragment is read.)
@@ -399,26 +397,24 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
     const int ts = tile.first + min((int)threadIdx.x, rows - 1);
     const float xs = p.x_scale[p.order ? p.order[ts] / p.topk : ts];
     const I8Scales<GATE> wscale = i8_scales<GATE>(p, tile.expert, min(o0 + threadIdx.x, p.M - 1));
-    // Operations requested after the parts that the second phase and that the next
-    // step's first one need.
-    constexpr int kLater1 = (WS - 1) * (2 * WOPS + XOPS), kLater0 = (WS > 2 ? 3 : 2) * WOPS + XOPS;
-    wait_vmcnt<kLater0>();
+    // Operations requested after the parts that the next phase needs.
+    constexpr int kLater = 2 * WOPS + XOPS;
+    wait_vmcnt<kLater>();
     sync_lds();
-    int wcur = 0, wprev = (WS - 1) * SW, xcur = 0;
+    int wcur = 0, xcur = 0;
     auto steps = [&](auto count) __attribute__((always_inline)) {
         constexpr bool kWork = decltype(count)::value > 0;
         for (int k = k0; k < nk; ++k) {
-            issue_w(wprev, k + WS - 1, 1);
+            issue_w(SW - wcur, k + 1, 1);
             if constexpr (kWork) phase(wcur, xcur, 0, count);
-            wait_vmcnt<kLater1>();
+            wait_vmcnt<kLater>();
             sync_lds();
             issue_x(xcur, k + 2);
-            issue_w(wcur, k + WS, 0);
+            issue_w(wcur, k + 2, 0);
             if constexpr (kWork) phase(wcur, xcur, 1, count);
-            wait_vmcnt<kLater0>();
+            wait_vmcnt<kLater>();
             sync_lds();
-            wprev = wcur;
-            wcur = wcur == (WS - 1) * SW ? 0 : wcur + SW;
+            wcur = SW - wcur;
             xcur = SX - xcur;
         }
     };
@@ -496,23 +492,23 @@ __global__ __launch_bounds__(256) void k_i8_sum(I8Product p) {
     }
 }
 
-template <int BM, int BN, int WM, int WN, int WS>
+template <int BM, int BN, int WM, int WN>
 static hipError_t tiled(const I8Product& p, int out, hipStream_t st) {
     const bool gate = out == kOutGate, yf32 = out == kOutF32;
     const int64_t bo = gate ? BM / 2 : BM, mt = (p.M + bo - 1) / bo;
     const int64_t blocks = p.offsets ? i8_blocks(p.T, p.E, BN, mt) : mt * ((p.T + BN - 1) / BN);
     const dim3 grid((unsigned)(blocks * p.splits)), block(WM * WN * kWave);
     if (p.splits > 1) {
-        const hipError_t e = launch_kernel(k_i8_tile<BM, BN, WM, WN, WS, kOutSums>, grid, block, 0, st, nullptr, nullptr, p);
+        const hipError_t e = launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutSums>, grid, block, 0, st, nullptr, nullptr, p);
         if (e != hipSuccess) return e;
         const int64_t work = p.T * ((p.M + 3) / 4);
         const dim3 sum((unsigned)std::min<int64_t>((work + 255) / 256, 8192));
         return yf32 ? launch_kernel(k_i8_sum<true>, sum, dim3(256), 0, st, nullptr, nullptr, p)
                     : launch_kernel(k_i8_sum<false>, sum, dim3(256), 0, st, nullptr, nullptr, p);
     }
-    if (gate) return launch_kernel(k_i8_tile<BM, BN, WM, WN, WS, kOutGate>, grid, block, 0, st, nullptr, nullptr, p);
-    return yf32 ? launch_kernel(k_i8_tile<BM, BN, WM, WN, WS, kOutF32>, grid, block, 0, st, nullptr, nullptr, p)
-                : launch_kernel(k_i8_tile<BM, BN, WM, WN, WS, kOutBf16>, grid, block, 0, st, nullptr, nullptr, p);
+    if (gate) return launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutGate>, grid, block, 0, st, nullptr, nullptr, p);
+    return yf32 ? launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutF32>, grid, block, 0, st, nullptr, nullptr, p)
+                : launch_kernel(k_i8_tile<BM, BN, WM, WN, kOutBf16>, grid, block, 0, st, nullptr, nullptr, p);
 }
 
 // What a product takes by each kernel, in us, fitted to 220 shapes (1 to 8192
@@ -597,10 +593,10 @@ hipError_t launch_i8_product(const I8Product& q, bool yf32, void* ws, hipStream_
     p.splits = c.splits;
     p.sums = (int*)ws;
     switch (c.kernel) {
-        case 0: return tiled<64, 32, 2, 1, 3>(p, out, st);
-        case 1: return tiled<128, 64, 2, 2, 2>(p, out, st);
-        case 2: return tiled<256, 128, 2, 4, 3>(p, out, st);
-        case 3: return tiled<256, 256, 2, 4, 2>(p, out, st);
+        case 0: return tiled<64, 32, 2, 1>(p, out, st);
+        case 1: return tiled<128, 64, 2, 2>(p, out, st);
+        case 2: return tiled<256, 128, 2, 4>(p, out, st);
+        case 3: return tiled<256, 256, 2, 4>(p, out, st);
         case -1: return stream<1, 4>(p, out, st);
     }
     return stream<2, 4>(p, out, st);

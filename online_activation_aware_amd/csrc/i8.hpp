@@ -27,7 +27,7 @@ struct I8Tile {
 // at most `size` rows one after the other for each of them, so that W comes from
 // memory once.  Where the chip has few tiles a compute unit, the experts' last
 // tiles of less than half the rows come behind all others instead (2048 tokens,
-// two of eight experts, 14336 -> 4096: 310 us, 000 so).
+// two of eight experts, 14336 -> 4096: 350 us, 300 so).
 //
 // Every wave finds its own: the tiles of 64 experts at a time by a scan over the
 // lanes.
