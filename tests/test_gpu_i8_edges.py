@@ -196,3 +196,42 @@ def test_moe_sorted_beside_the_rows(T, Tn, topk, K, per_in):
     ws = torch.full((T.ttq_moe_i8_workspace_bytes(Tn, topk, K, 48, 20, 3),), 0xFF, dtype=torch.uint8, device="cuda")
     Y = T.ttq_moe_i8(d["X"], i32_dev(d["ids"]), f32_dev(d["w"]), d["gate_up"], d["down"], ws=ws)
     near(Y, *moe_ref(d, "silu"), "f32")
+
+
+def codes_like(g, *shape):
+    return torch.randint(-127, 128, shape, generator=g, device="cuda", dtype=torch.int8)
+
+
+@pytest.mark.parametrize("Tn,K,M", [(2048, 528, 4100), (2001, 1040, 4000), (2300, 1072, 4097), (1024, 14336, 2050), (40, 8208, 1030)])
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+def test_gemm_of_many_tiles(T, Tn, K, M, dt):
+    """The largest tiles, with ragged ends, and channels in parts: the exact
+    sums in fp64, the scales in fp32."""
+    say(f"gemm_i8 many tiles T={Tn} K={K} M={M} {dt}")
+    g = torch.Generator(device="cuda").manual_seed(Tn + K + M)
+    x, w = codes_like(g, Tn, K), codes_like(g, M, K)
+    xs, ws = torch.rand(Tn, generator=g, device="cuda"), torch.rand(M, generator=g, device="cuda")
+    sums = x.double() @ w.double().t().contiguous()      # whole numbers below 2^53
+    want = (sums.float() * xs[:, None] * ws[None, :]).to(dt)
+    for turn in range(2):
+        assert torch.equal(T.ttq_gemm_i8(x, xs, w, ws, y_dtype=dt), want)
+
+
+@pytest.mark.parametrize("Tn,K,I,M,E,topk", [(1500, 2064, 2000, 1030, 2, 2), (4000, 1056, 1040, 1056, 2, 2), (4003, 1056, 1040, 1054, 5, 2),
+                                             (4000, 528, 2000, 1056, 3, 1)])
+def test_moe_of_many_tiles(T, Tn, K, I, M, E, topk):
+    """The largest tiles give every token what a call of a few tokens gives it,
+    whose tiles are others."""
+    say(f"moe_i8 many tiles T={Tn} K={K} I={I} M={M} E={E}")
+    g = torch.Generator(device="cuda").manual_seed(Tn + I)
+    rand = lambda *shape: torch.rand(shape, generator=g, device="cuda")
+    X = torch.randn((Tn, K), generator=g, device="cuda").bfloat16()
+    ids = torch.randint(-1, E, (Tn, topk), generator=g, device="cuda", dtype=torch.int32)
+    w = rand(Tn, topk)
+    up = dict(s=rand(K) + 0.5, codes=codes_like(g, E, 2 * I, K), scale=rand(E, 2 * I) * (0.02 / K ** 0.5))
+    down = dict(s=rand(E, I) + 0.5, codes=codes_like(g, E, M, I), scale=rand(E, M) * (0.02 / I ** 0.5))
+    every = T.ttq_moe_i8(X, ids, w, up, down)
+    assert torch.isfinite(every).all()
+    for lo, n in ((0, 100), (Tn // 2, 37), (Tn - 64, 64), (Tn - 1, 1)):
+        part = T.ttq_moe_i8(X[lo:lo + n], ids[lo:lo + n].contiguous(), w[lo:lo + n].contiguous(), up, down)
+        assert torch.equal(part, every[lo:lo + n]), lo
