@@ -442,7 +442,10 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
         }
         return;
     }
-    // (Every wave has read its last fragments.)
+    // Each wave has waited for its own DMA.  That behind the last step writes zeros
+    // where the scales go (one slot or the other, by the number of steps), so that
+    // they are stored when every wave has.
+    sync_lds();
     float *sx = (float*)lds, *sw = sx + BN;
     if (threadIdx.x < BN) sx[threadIdx.x] = xs;
     if (threadIdx.x < BO) {
