@@ -1,5 +1,5 @@
-"""8-bit products by every tile: an odd number of 128-channel steps, ragged
-ends, every kind of result; sums are exact, so results
+"""8-bit products by every tile and in parts of the channels: an odd number of
+128-channel steps, ragged ends, every kind of result; sums are exact, so results
 equal their definition, or a call of few rows, whose kernel is another."""
 import pytest
 import torch
@@ -41,6 +41,25 @@ def test_tiles_of_an_odd_number_of_steps(T, Tn, K, M, dt):
         assert torch.equal(T.ttq_gemm_i8(x, xs, w, ws, y_dtype=DT[dt]), want)
 
 
+# The same tiles, 2 to 16 parts.
+PARTS = [(145, 1888, 61), (131, 4976, 60), (2335, 4912, 269), (1421, 4432, 161), (797, 7472, 73), (433, 4976, 4728), (2085, 7792, 132), (3299, 9568, 542)]
+
+
+@pytest.mark.parametrize("Tn,K,M", PARTS)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_parts(T, Tn, K, M, dt):
+    """In parts, through a workspace of exactly the stated bytes between guards,
+    full of NaN."""
+    say(f"gemm_i8 parts T={Tn} K={K} M={M} {dt}")
+    n = T.ttq_gemm_i8_workspace_bytes(Tn, K, M)
+    assert n >= 2 * Tn * M * 4                           # the sums of two parts at least
+    x, xs, w, ws, want = inputs(Tn, K, M, dt)
+    big = torch.full((n + 8192,), 0xFF, dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        assert torch.equal(T.ttq_gemm_i8(x, xs, w, ws, y_dtype=DT[dt], ws=big[4096:4096 + n]), want)
+    assert bool((big[:4096] == 0xFF).all()) and bool((big[4096 + n:] == 0xFF).all())
+
+
 # Gate and up, and down, in tiles of 128 x 64, 256 x 128 and 256 x 256, with 1 to 23 steps.
 @pytest.mark.parametrize("Tn,E,topk,K,I,M", [(109, 5, 2, 272, 2864, 68), (4225, 4, 2, 128, 336, 60), (5291, 3, 2, 128, 592, 61), (409, 5, 2, 128, 64, 2957),
                                              (1334, 2, 2, 128, 64, 2336), (2217, 3, 2, 128, 64, 2961), (1203, 3, 2, 272, 1408, 2063),
@@ -59,3 +78,39 @@ def test_layers_of_an_odd_number_of_steps(T, Tn, E, topk, K, I, M, yt):
     some = torch.cat([T.ttq_moe_i8(X[i:i + 64], ids[i:i + 64].contiguous(), w[i:i + 64].contiguous(), up, down, y_dtype=DT[yt])
                       for i in range(0, Tn, 64)])
     assert torch.isfinite(every).all() and torch.equal(every, some)
+
+
+def test_two_captured_graphs_in_parts(T):
+    """Two products in parts, each with its own workspace, captured and replayed
+    in turn and at once, with eager work between."""
+    say("two captured graphs, parts")
+    jobs = []
+    for Tn, K, M in ((145, 1888, 61), (1421, 4432, 161)):
+        ws = torch.full((T.ttq_gemm_i8_workspace_bytes(Tn, K, M),), 0xFF, dtype=torch.uint8, device="cuda")
+        assert ws.numel() >= 2 * Tn * M * 4
+        x, xs, w, wsc, want = inputs(Tn, K, M, "f32")
+        Y = torch.empty_like(want)
+        jobs.append((lambda a=(x, xs, w, wsc), Y=Y, ws=ws: T.ttq_gemm_i8(*a, Y=Y, ws=ws), Y, want))
+    graphs = []
+    for run, _, _ in jobs:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            run()
+        graphs.append((g, side))
+    for turn in range(4):
+        for _, Y, _ in jobs:
+            Y.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for g, side in graphs:
+            with torch.cuda.stream(side):
+                g.replay()
+        torch.cuda.synchronize()
+        for run, Y, want in jobs:
+            assert torch.equal(Y, want), turn
+        jobs[turn % 2][0]()
+        torch.cuda.synchronize()
