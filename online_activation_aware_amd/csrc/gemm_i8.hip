@@ -53,12 +53,12 @@ __global__ __launch_bounds__(NW * kWave) void k_i8_stream(I8Product p) {
     }
     // The scales of the results of waves that add, requested ahead.
     float xs = 0.f;
-    I8Scales<GATE> ws[4];
+    I8Results<GATE> ws;
     if (wave < NT) {
         const int t = min(tile.first + 16 * wave + r16, tile.last - 1);
         xs = p.x_scale[p.order ? p.order[t] / p.topk : t];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ws[i] = i8_scales<GATE>(p, tile.expert, min(o0 + 4 * (lane >> 4) + i, p.M - 1));
+        for (int i = 0; i < 4; ++i) ws.set(i, i8_scales<GATE>(p, tile.expert, min(o0 + 4 * (lane >> 4) + i, p.M - 1)));
     }
     i32x4 acc[G][NT];
 #pragma unroll
@@ -116,10 +116,8 @@ __global__ __launch_bounds__(NW * kWave) void k_i8_stream(I8Product p) {
     }
     const int64_t t = tile.first + 16 * wave + r16, o = o0 + 4 * (lane >> 4);
     if (t >= tile.last || o >= p.M) return;
-    f32x4 y;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = i8_result<GATE>(ws[i], p.act, xs, t4[0][i], t4[G - 1][i]);
-    store_y4<YF32>(p.Y, t * p.ldy + o, p.M - o, p.yvec, y);
+    ws.ready();
+    store_y4<YF32>(p.Y, t * p.ldy + o, p.M - o, p.yvec, ws.of(p.act, xs, t4[0], t4[G - 1]));
 }
 
 template <int NT, int NW>
@@ -452,7 +450,7 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
         sw[threadIdx.x] = wscale.g;
         if constexpr (GATE) {
             sw[BO + threadIdx.x] = wscale.u;
-            sw[2 * BO + threadIdx.x] = wscale.r;
+            sw[2 * BO + threadIdx.x] = wscale.s;
         }
     }
     __syncthreads();
@@ -463,18 +461,18 @@ __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
     for (int i = 0; i < FA; i += G) {
         const int ol = (wm * FA + i) * (16 / G) + 4 * (lane >> 4);
         const int64_t o = o0 + ol;
-        f32x4 w[3];
-#pragma unroll
-        for (int c = 0; c < (GATE ? 3 : 1); ++c) w[c] = *(const f32x4*)(sw + c * BO + ol);
+        I8Results<GATE> w;
+        w.g = *(const f32x4*)(sw + ol);
+        if constexpr (GATE) {
+            w.u = *(const f32x4*)(sw + BO + ol);
+            w.s = *(const f32x4*)(sw + 2 * BO + ol);
+        }
+        w.ready();
 #pragma unroll
         for (int j = 0; j < FB; ++j) {
             const int tl = (j * WN + wn) * 16 + (lane & 15);
             const float xt = sx[tl];
-            f32x4 y;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                y[r] = i8_result<GATE>(I8Scales<GATE>{w[0][r], w[GATE ? 1 : 0][r], w[GATE ? 2 : 0][r]}, p.act, xt,
-                                       acc[i][j][r], acc[i + G - 1][j][r]);
+            const f32x4 y = w.of(p.act, xt, acc[i][j], acc[i + G - 1][j]);
             const int64_t at = (int64_t)(tile.first + tl) * p.ldy + o;
             if (whole) store_y4<YF32>(p.Y, at, 4, 1, y);
             else if (tl < rows && o < p.M) store_y4<YF32>(p.Y, at, p.M - o, p.yvec, y);
@@ -490,11 +488,10 @@ __global__ __launch_bounds__(256) void k_i8_sum(I8Product p) {
         const int64_t t = i / quads, o = (i - t * quads) * 4;
         i32x4 s = {0, 0, 0, 0};
         for (int c = 0; c < p.splits; ++c) s += *(const i32x4*)(p.sums + (c * all + i) * 4);
-        f32x4 y;
-        const float xs = p.x_scale[t];
+        I8Results<false> w;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) y[r] = i8_result<false>(i8_scales<false>(p, 0, min(o + r, p.M - 1)), 0, xs, s[r], 0);
-        store_y4<YF32>(p.Y, t * p.ldy + o, p.M - o, p.yvec, y);
+        for (int r = 0; r < 4; ++r) w.set(r, i8_scales<false>(p, 0, min(o + r, p.M - 1)));
+        store_y4<YF32>(p.Y, t * p.ldy + o, p.M - o, p.yvec, w.of(0, p.x_scale[t], s, s));
     }
 }
 
