@@ -9,6 +9,7 @@ namespace ttq {
 
 constexpr int kRowSeg = 8;                        // values of a vector
 constexpr uint32_t kRowTiny = 0x21800000u;        // 2^-60
+constexpr uint32_t kRowHuge = 0x7F000000u;        // 2^127
 
 // Eight values of a row as they lie in memory.
 template <bool F32>
@@ -50,7 +51,8 @@ struct RowScale {
 
 // v of the eight values: x, fp32(x s) or fp32(x / s).  exact: by the division
 // itself, for rows whose quotients are tiny (the corrections' remainders would
-// be rounded).  Elsewhere a quotient below 2^-100 may be off in its last bit,
+// be rounded) or near the largest number (x (1 / s) may be beyond it where x / s is
+// not).  Elsewhere a quotient below 2^-100 may be off in its last bit,
 // where its code is 0 either way.
 template <bool F32, int MODE>
 __device__ __forceinline__ void row_values(const RowVector<F32>& x, const RowScale<MODE>& s, bool exact,
@@ -206,7 +208,7 @@ __device__ __forceinline__ void quantize_rows(const I8RowsArgs& a, int block, in
         };
         whole(turn);
         bool exact = false;
-        if (SMODE == 2 && top < kRowTiny) {       // quotients near the lowest exponents
+        if (SMODE == 2 && (top < kRowTiny || top >= kRowHuge)) {   // quotients near the ends of fp32
             exact = true;
             __syncthreads();
             top = 0;
