@@ -8,7 +8,7 @@
 namespace ttq {
 
 constexpr int kRowSeg = 8;                        // values of a vector
-constexpr uint32_t kRowTiny = 0x21800000u;        // 2^-60
+constexpr uint32_t kRowTiny = 0x24800000u;        // 2^-54
 constexpr uint32_t kRowHuge = 0x7F000000u;        // 2^127
 
 // Eight values of a row as they lie in memory.
@@ -50,10 +50,10 @@ struct RowScale {
 };
 
 // v of the eight values: x, fp32(x s) or fp32(x / s).  exact: by the division
-// itself, for rows whose quotients are tiny (the corrections' remainders would
-// be rounded) or near the largest number (x (1 / s) may be beyond it where x / s is
-// not).  Elsewhere a quotient below 2^-100 may be off in its last bit,
-// where its code is 0 either way.
+// itself, for rows whose quotients are near the largest number (x (1 / s) may be
+// beyond it where x / s is not) or tiny: x - q s has no bit below fp32's last, 2^-149,
+// where |s| > 2^-40 and q >= 2^-63, and in a row whose largest quotient is 2^-54 or more the
+// codes of smaller ones are 0.
 template <bool F32, int MODE>
 __device__ __forceinline__ void row_values(const RowVector<F32>& x, const RowScale<MODE>& s, bool exact,
                                            float (&v)[kRowSeg]) {

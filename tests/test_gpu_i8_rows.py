@@ -52,3 +52,21 @@ def test_quotients_of_the_largest_number(T, x, s, K):
         rows = np.repeat(row, n, 0)
         want = ref.product(*ref.quantize(rows, sv, True), wq, ws)
         same(T.ttq_qgemm_i8(f32_dev(rows), f32_dev(sv), torch.from_numpy(wq).cuda(), f32_dev(ws)), want)
+
+
+# (x, s, the row's largest value): x / s lies next to half a step, and the remainder
+# x - q s of its quotient has bits below fp32's last.
+SMALL = [("0x1.046bc6p-106", "0x1.79bb8ap-40", "0x1.5e3b46p-59"), ("0x1.4b0a24p-106", "0x1.69b090p-40", "0x1.d0f38cp-59"),
+         ("0x1.229e46p-106", "0x1.ed8770p-40", "0x1.2b23bap-59"), ("0x1.83755ap-106", "0x1.a0ea0cp-40", "0x1.d81bd8p-59"),
+         ("0x1.6cacbcp-106", "0x1.ec386cp-40", "0x1.785d90p-59"), ("0x1.065d7ep-106", "0x1.683a74p-40", "0x1.71fde4p-59")]
+
+
+@pytest.mark.parametrize("K", [64, 4096, 16400])
+@pytest.mark.parametrize("x,s,top", SMALL)
+def test_small_quotients_next_to_half_a_step(T, x, s, top, K):
+    say(f"quantize_rows {x} / {s} beside {top} K={K}")
+    x, s, top = (float.fromhex(v) for v in (x, s, top))
+    assert abs(x / s / (np.float32(top) / np.float32(127)) - 0.5) < 1e-6
+    xs, ss = np.full(K // 2, 0.0), np.ones(K // 2)
+    xs[0], xs[1], ss[1] = top, x, s
+    check(T, xs, ss, K)
