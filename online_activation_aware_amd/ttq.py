@@ -771,6 +771,13 @@ def _wide_stride(t: torch.Tensor, name: str) -> int:
     return st[0] if rows > 1 else -(-row // 8) * 8
 
 
+def _new_rows(rows: int, row: int, like: torch.Tensor) -> torch.Tensor:
+    """A matrix of `like`'s dtype whose rows begin at whole 16-byte pieces
+    (dense where their length allows it)."""
+    n = 16 // like.element_size()
+    return like.new_empty((rows, -(-row // n) * n))[:, :row]
+
+
 @_on_tensor_device
 def ttq_quantize_rows(X: torch.Tensor, s: Optional[torch.Tensor] = None, divide: bool = False,
                       codes: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, stream=None):
@@ -908,14 +915,15 @@ def ttq_moe_gather(X: torch.Tensor, pos: torch.Tensor, R: Optional[torch.Tensor]
                    stream=None) -> torch.Tensor:
     """R[pos[t][j]] = X[t]: the tokens' rows in their experts' order (pos from
     ttq_moe_sort).  R [rows][K] has X's dtype (default: new, a row for each
-    slot); rows that no slot names are left as they were."""
+    slot, its row stride K rounded up to 16 bytes); rows that no slot names
+    are left as they were."""
     ldx = _wide_stride(X, "X")
     T, K = X.shape
     if pos.dim() != 2:
         raise ValueError("pos must be [T][topk]")
     topk = pos.shape[1]
     if R is None:
-        R = X.new_empty((T * topk, K))
+        R = _new_rows(T * topk, K, X)
     elif _on(R, "R", X.get_device()).dtype != X.dtype or R.dim() != 2 or R.shape[1] != K:
         raise ValueError(f"R must be [rows][{K}] of X's dtype")
     _check(lib().ttq_moe_gather(X.data_ptr(), _code(X), T, K, ldx,
@@ -951,7 +959,8 @@ def ttq_moe_combine(R: torch.Tensor, pos: torch.Tensor, w: Optional[torch.Tensor
 def ttq_moe_combine_grad(dY: torch.Tensor, R: torch.Tensor, pos: torch.Tensor, w: Optional[torch.Tensor] = None,
                          dR: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, stream=None):
     """The gradient of ttq_moe_combine: (dR [rows][M], dw [T][topk]) from dY
-    [T][M].  dR (default: new) keeps the rows that no slot names."""
+    [T][M].  dR (default: new, its row stride M rounded up to 16 bytes) keeps
+    the rows that no slot names."""
     lddy, ldr = _wide_stride(dY, "dY"), _wide_stride(R, "R")
     T, M = dY.shape
     dev = dY.get_device()
@@ -959,7 +968,7 @@ def ttq_moe_combine_grad(dY: torch.Tensor, R: torch.Tensor, pos: torch.Tensor, w
         raise ValueError(f"R must be [rows][{M}] and pos [T][topk]")
     topk = pos.shape[1]
     rt = _code(R)
-    dR = _output(dR, R.shape, R.dtype, dY, "dR")
+    dR = _new_rows(R.shape[0], M, R) if dR is None else _output(dR, R.shape, R.dtype, dY, "dR")
     if dR.dtype is not R.dtype:
         raise TypeError("dR must have R's dtype")
     if dw is None:
