@@ -510,8 +510,8 @@ ttq_status ttq_quantize_rows(const void* X, int xt, int64_t R, int64_t K, int64_
  *   rounded once more to a bf16 Y.
  *   X: [T][K] int8, stride ldx;  W: [M][K] int8, stride ldw, e.g. both from
  *   ttq_quantize_rows.  Y: [T][M] (yt), stride ldy, overwritten; no overlap.
- *   ldx and ldw up to 2^22 and T * M up to about 2^38 (else
- *   TTQ_ERR_UNSUPPORTED).  T == 0 or M == 0 is an empty call.
+ *   ldx and ldw above 2^22, or 2^23 blocks of 256 x 256 of Y and more, return
+ *   TTQ_ERR_UNSUPPORTED.  T == 0 or M == 0 is an empty call.
  *   ws: ttq_gemm_i8_workspace_bytes(T, K, M) bytes, 256-byte aligned; calls that
  *   may run at the same time need workspaces of their own.
  */

@@ -544,10 +544,15 @@ struct I8Choice {
 // A grid has fewer than 2^32 threads.
 static bool grid_fits(double blocks, int threads) { return blocks * threads < 4294967296.0; }
 
-// The largest tiles (of gate and up, too) cover T x M.
-bool i8_product_fits(int64_t T, int64_t M, int64_t E) {
-    return grid_fits((double)((T + 255) / 256 + E) * (double)((M + 127) / 128 + 8), 512);
+// Workgroups of tiles of `rows` x `outputs` of T x M: for one matrix (E == 0), or at
+// most for E (i8_blocks).
+static double grid_blocks(int64_t T, int64_t M, int64_t E, int64_t rows, int64_t outputs) {
+    if (E == 0) return (double)((T + rows - 1) / rows) * (double)((M + outputs - 1) / outputs);
+    return ((double)(T / rows) + 1 + (double)E) * ((double)(M / outputs) + 8);
 }
+
+// The largest tiles cover T x M.
+bool i8_product_fits(int64_t T, int64_t M, int64_t E) { return grid_fits(grid_blocks(T, M, E, 256, E == 0 ? 256 : 128), 512); }
 
 static I8Choice choose(int64_t T, int64_t K, int64_t M, int64_t E, bool experts, bool gate) {
     const int64_t rows = experts ? std::max<int64_t>((T + E - 1) / E, 1) : T;    // of a matrix, on average
@@ -567,7 +572,7 @@ static I8Choice choose(int64_t T, int64_t K, int64_t M, int64_t E, bool experts,
         for (int s = 1; s <= (experts ? 1 : kMaxSplits); s *= 2) {
             if (s > 1 && steps < 2 * s) break;
             const double tiles = (double)(((M + bo - 1) / bo) * ((rows + c.bn - 1) / c.bn) * s) * mats;
-            if (!grid_fits(((double)T / c.bn + 1 + (double)E) * ((double)M / bo + 8) * s, c.threads)) break;
+            if (!grid_fits(grid_blocks(T, M, experts ? E : 0, c.bn, bo) * s, c.threads)) break;
             const double n = std::ceil(tiles / 256), at_once = std::min(n, (double)c.fit);
             const double step = c.step + (c.full - c.step) * std::min(tiles / 256, 1.0) + c.more * (at_once - 1);
             offer(n / at_once * (c.start + steps / s * step) +
@@ -577,7 +582,7 @@ static I8Choice choose(int64_t T, int64_t K, int64_t M, int64_t E, bool experts,
     for (int nt = 1; nt <= 2 && rows <= 128; ++nt) {
         const double tiles = (double)((rows + 16 * nt - 1) / (16 * nt));
         const double x = codes * tiles * std::min<double>(rows, 16 * nt) / 16;
-        if (!grid_fits(((double)T / (16 * nt) + 1 + (double)E) * ((double)M / kStreamRows + 8), 256)) break;
+        if (!grid_fits(grid_blocks(T, M, experts ? E : 0, 16 * nt, kStreamRows), 256)) break;
         offer(3.0 + codes / 8.6 + 0.119 * x + 0.9 * K / 4096 + (nt - 1) * (0.03 + 5e-6 * M * tiles), -nt, 1);
     }
     return best;

@@ -239,7 +239,7 @@ struct I8Product {
     int* sums = nullptr;
 };
 size_t i8_product_ws_bytes(int64_t T, int64_t K, int64_t M);
-bool i8_product_fits(int64_t T, int64_t M, int64_t E);   // a grid can cover T x M, for E matrices
+bool i8_product_fits(int64_t T, int64_t M, int64_t E);   // a grid can cover T x M, for E matrices (0: one, without offsets)
 hipError_t launch_i8_product(const I8Product& p, bool yf32, void* ws, hipStream_t st);
 
 // ttq_qgemm_i8 of one token in one launch (codes and scales of X unused).

@@ -793,7 +793,7 @@ ttq_status check_product_i8(int64_t T, int64_t K, int64_t M, const int8_t* W, co
     if (T > 0 && M > 0)
         if (ttq_status e = check_floats("w_scale", w_scale)) return e;
     if (ldw > kMaxLdI8) return fail(TTQ_ERR_UNSUPPORTED, "W: row stride above 2^22");
-    if (!ttq::i8_product_fits(T, M, 1)) return fail(TTQ_ERR_UNSUPPORTED, "T x M is beyond one launch");
+    if (!ttq::i8_product_fits(T, M, 0)) return fail(TTQ_ERR_UNSUPPORTED, "T x M is beyond one launch");
     return TTQ_OK;
 }
 
@@ -861,7 +861,7 @@ ttq_status ttq_quantize_rows(const void* X, int xt, int64_t R, int64_t K, int64_
 }
 
 size_t ttq_gemm_i8_workspace_bytes(int64_t T, int64_t K, int64_t M) {
-    if (!dim_ok(T) || !dim_ok(M) || K <= 0 || K > kMaxKI8 || K % 16 || !ttq::i8_product_fits(T, M, 1)) return 0;
+    if (!dim_ok(T) || !dim_ok(M) || K <= 0 || K > kMaxKI8 || K % 16 || !ttq::i8_product_fits(T, M, 0)) return 0;
     return round_up(ttq::i8_product_ws_bytes(T, K, M)) + kAlign;
 }
 
