@@ -616,7 +616,7 @@ typedef struct ttq_expert_i8 {
  *   depend on the other tokens of the call.
  *   K and I multiples of 16, at most 2^17; E <= 1024; 1 <= topk <= 32.  An
  *   expert's gate_up or down codes of 2 GiB or more, T * topk > 2^24 or
- *   T * topk * K >= 2^31 return TTQ_ERR_UNSUPPORTED.  T == 0 or M == 0 is an
+ *   T * K >= 2^31 return TTQ_ERR_UNSUPPORTED.  T == 0 or M == 0 is an
  *   empty call.
  *   ws: ttq_moe_i8_workspace_bytes(T, topk, K, I, M, E) bytes, 256-byte aligned;
  *   calls that may run at the same time need workspaces of their own.

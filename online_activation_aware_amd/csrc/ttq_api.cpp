@@ -834,8 +834,8 @@ ttq_status check_moe_i8_sizes(int64_t T, int64_t topk, int64_t K, int64_t I, int
     if (ttq_status e = check_k_i8("I", I)) return e;
     if (2 * I * K >= kMaxExpertBytes || M * I >= kMaxExpertBytes)
         return fail(TTQ_ERR_UNSUPPORTED, "an expert's codes take 2 GiB or more");
-    if (T * topk > kMaxMoeI8Slots || T * topk * K >= kMaxExpertBytes)
-        return fail(TTQ_ERR_UNSUPPORTED, "more than 2^24 slots, or 2 GiB of their codes: pass the tokens in chunks");
+    if (T * topk > kMaxMoeI8Slots || T * K >= kMaxExpertBytes)
+        return fail(TTQ_ERR_UNSUPPORTED, "more than 2^24 slots, or 2 GiB of the tokens' codes: pass the tokens in chunks");
     if (!ttq::i8_product_fits(T * topk, I > M ? I : M, E))
         return fail(TTQ_ERR_UNSUPPORTED, "slots x channels is beyond one launch");
     return TTQ_OK;

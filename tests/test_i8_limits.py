@@ -28,3 +28,11 @@ def test_products_of_narrow_results(T, t, m):
 @pytest.mark.parametrize("t,m", [(1 << 30, 257), (257, 1 << 30), ((1 << 19) + 1, 1 << 20)])
 def test_products_beyond_one_launch(T, t, m):
     assert T.ttq_gemm_i8_workspace_bytes(t, 16, m) == 0
+
+
+def test_layers_of_many_codes(T):
+    """The tokens' codes are T K bytes; a token's experts share them."""
+    assert T.ttq_moe_i8_workspace_bytes(1 << 14, 8, 1 << 14, 16, 16, 8) > 0
+    assert T.ttq_moe_i8_workspace_bytes((1 << 17) - 1, 32, 1 << 14, 16, 16, 8) > 0
+    assert T.ttq_moe_i8_workspace_bytes(1 << 17, 1, 1 << 14, 16, 16, 8) == 0
+    assert T.ttq_moe_i8_workspace_bytes((1 << 24) + 1, 1, 16, 16, 16, 8) == 0
