@@ -106,35 +106,38 @@ __device__ __forceinline__ I8Recip i8_recip(const f32x4& s) {
     return c;
 }
 
-// act(g) u / s, act(x) = x / (1 + exp(-y)), within ten units of 2^-24 of it for
-// these g, u and (of gelu) y: exp2 of the rounded product of y and log2 e, corrected
-// by what the rounding left (it alone is |y| units), the quotient by a corrected
-// reciprocal, and 1 / s.  Where y or s is extreme: whole divisions and expf, which
-// everywhere take half of a tile's work behind its products (2048 tokens, two of eight
-// experts, 4096 -> 14336: the layer 925 us, with these 886, without the corrections 870).
+// act(g) u / s, act(x) = x / (1 + exp(-y)), each operation rounded once (an h below
+// 2^-100 perhaps a unit off): the quotients by corrected reciprocals, and by whole
+// divisions where y, s or h is extreme.  An h that is off in its last bits has other
+// codes next to borders: with exp2 of a rounded product and uncorrected reciprocals one
+// result in 800 was another bf16 number.  (2048 tokens, two of eight experts, 4096 ->
+// 14336: the layer 907 us, with those 878, with whole divisions alone 935.)
 __device__ __forceinline__ f32x4 i8_gate(const f32x4& g, const f32x4& u, const f32x4& s, const I8Recip& c, int act) {
+    auto top = [](const f32x4& v) __attribute__((always_inline)) {
+        return fmaxf(fmaxf(__builtin_fabsf(v[0]), __builtin_fabsf(v[1])), fmaxf(__builtin_fabsf(v[2]), __builtin_fabsf(v[3])));
+    };
     f32x4 y = g, h;
     if (act != TTQ_ACT_SILU)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             y[i] = 1.5957691216057308f * (g[i] + 0.044715f * g[i] * g[i] * g[i]);   // 2 sqrt(2 / pi)
-    const float top = fmaxf(fmaxf(__builtin_fabsf(y[0]), __builtin_fabsf(y[1])), fmaxf(__builtin_fabsf(y[2]), __builtin_fabsf(y[3])));
-    if (c.plain && top < 87.f) {
+    bool plain = c.plain && top(y) < 87.f;
+    if (plain) {
+        f32x4 a;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float t = -1.44269504f * y[i];
-            const float f = __builtin_fmaf(-1.925963033500e-08f, y[i], __builtin_fmaf(-1.44269504f, y[i], -t));
-            float e = __builtin_amdgcn_exp2f(t);
-            e = __builtin_fmaf(e * f, 0.693147181f, e);
-            const float d = 1.f + e, r = __builtin_amdgcn_rcpf(d);
-            float q = g[i] * r;
-            q = __builtin_fmaf(__builtin_fmaf(-q, d, g[i]), r, q);
-            h[i] = q * u[i] * c.r[i];
+            const float d = 1.f + expf(-y[i]), r = __builtin_amdgcn_rcpf(d);
+            const float q = g[i] * r;
+            a[i] = __builtin_fmaf(__builtin_fmaf(-q, d, g[i]), r, q) * u[i];
+            h[i] = a[i] * c.r[i];
         }
-    } else {
+        plain = top(h) < 0x1p127f;                // (a (1 / s) may be infinite where a / s is not)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __builtin_fmaf(__builtin_fmaf(-h[i], s[i], a[i]), c.r[i], h[i]);
+    }
+    if (!plain)
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[i] = moe_act(g[i], act) * u[i] / s[i];
-    }
     return h;
 }
 

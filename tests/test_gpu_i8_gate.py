@@ -42,15 +42,15 @@ def layer(T, copies, act, u_scale, s_down, w_scale=1.0):
 
 
 def check(y, g, u, s_down, act, w_scale=1.0):
-    """The roundings, in units: the exponential three (one in the last place and a
-    correction), its sum with 1, the quotient and the product with u one each, the
-    division by s_down two (a reciprocal and a product), h / 127 and the product
-    with the scale one each.  gelu's argument 2 sqrt(2 / pi) (g + 0.044715 g^3): four
-    of the cubic term, the sum's, two of the factor's, all times the argument."""
+    """The roundings, in units: the exponential two (one in the last place), its sum
+    with 1, the quotient, the product with u, the division by s_down, h / 127 and the
+    product with the scale one each.  gelu's argument 2 sqrt(2 / pi) (g + 0.044715
+    g^3): four of the cubic term, the sum's, two of the factor's, all times the
+    argument."""
     arg = g if act == "silu" else 2 * np.sqrt(2 / np.pi) * (g + 0.044715 * g ** 3)
     with np.errstate(over="ignore"):
         want = 127 * w_scale * (g / (1 + np.exp(-arg))) * u / float(np.float32(s_down))
-    units = 10 + (0 if act == "silu" else 7 * np.abs(arg))
+    units = 8 + (0 if act == "silu" else 7 * np.abs(arg))
     fine = np.abs(arg) < 87.7                            # behind it the exponential overflows: 0 for less than 3e-37 u
     assert fine.sum() > 20
     off = np.abs(y - want)[fine] - (units * UNIT * (1 + 1e-4) * np.abs(want))[fine]
@@ -74,3 +74,36 @@ def test_gate_of_extreme_scales(T, copies):
         y, g, u = layer(T, copies, "silu", u_scale, s_down, w_scale)
         near = np.abs(g) < 10                            # act(g) u is a normal number
         check(y[near], g[near], u, s_down, "silu", w_scale)
+
+
+# (a, s) whose product with fp32(1 / s) is beyond fp32 and whose quotient is its largest number.
+LARGEST = [("0x1.dcf94ap+127", "0x1.dcf94cp-1"), ("0x1.eafbe2p+127", "0x1.eafbe4p-1"), ("0x1.c727b4p+127", "0x1.c727b6p-1"),
+           ("0x1.d3c832p+127", "0x1.d3c834p-1")]
+
+
+@pytest.mark.parametrize("a,s", LARGEST)
+@pytest.mark.parametrize("n", [1, 5100])
+def test_an_h_of_the_largest_number(T, a, s, n):
+    """h = 64 u / s_down = fp32's largest number beside an h of 127: finite, and the
+    output of a code of the small one, 0."""
+    say(f"moe_i8 largest h {a} / {s} n={n}")
+    a, s = np.float32(float.fromhex(a)), np.float32(float.fromhex(s))
+    assert a / s == np.finfo(np.float32).max
+    u_scale = next(v for k in range(-4, 5) for v in [np.float32(float(a / np.float32(64 * 127)) * (1 + k * 2.0 ** -24))] if v * np.float32(127) * np.float32(64) == a)
+    x = np.zeros((n, 16), np.float32)
+    x[:, 0], x[:, 1] = 127, 64
+    up, down = np.zeros((1, 32, 16), np.int8), np.zeros((1, 1, 16), np.int8)
+    up[0, 0, 1], up[0, 16, 0] = 1, 1                      # h of channel 0
+    up[0, 1, 1], up[0, 17, 0] = 1, 1                      # and of channel 1
+    down[0, 0, 1] = 127
+    scale = np.ones((1, 32), np.float32)
+    scale[0, 16] = u_scale
+    dev = lambda v: torch.from_numpy(np.ascontiguousarray(v)).cuda()
+    args = (f32_dev(x), i32_dev(np.zeros((n, 1))), f32_dev(np.ones((n, 1))), dict(s=f32_dev(np.ones(16)), codes=dev(up), scale=dev(scale)))
+    Y = T.ttq_moe_i8(*args, dict(s=dev(np.full((1, 16), s)), codes=dev(down), scale=f32_dev(np.ones((1, 1)))))
+    assert torch.count_nonzero(Y) == 0
+    down[0, 0, 0] = 1                                     # 127 fp32(h / 127) 2^-10
+    Y = T.ttq_moe_i8(*args, dict(s=dev(np.full((1, 16), s)), codes=dev(down), scale=f32_dev(np.full((1, 1), 2.0 ** -10))))
+    scale = np.finfo(np.float32).max / np.float32(127)
+    with np.errstate(over="ignore"):
+        assert np.all(host(Y) == np.float32(127) * scale * np.float32(2.0 ** -10))
