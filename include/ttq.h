@@ -486,6 +486,8 @@ size_t ttq_qgemm_adapters_workspace_bytes(int64_t T, int64_t K, int64_t M, int b
  * 16-byte aligned; scale [R] fp32; row r stands for codes * scale[r].  K a
  * positive multiple of 16, at most 2^17, so that a sum of K products of codes
  * of -127..127 is exact in int32.
+ * Outputs and workspaces of the calls below overlap neither each other nor an
+ * input.
  */
 
 /*
@@ -605,7 +607,7 @@ typedef struct ttq_expert_i8 {
 } ttq_expert_i8;
 
 /*
- * ttq_moe_i8 — ttq_moe on 8-bit experts, for any number of tokens.
+ * ttq_moe_i8 — ttq_moe on 8-bit experts, for long prompts too.
  *   Y[t] = sum_j w[t][j] D_e q(h),  h = act(g) * u / s_down,
  *   [g; u] = G_e q(X[t] / s_in),  e = ids[t][j],
  *   q(.) the row in 8 bits (ttq_quantize_rows), products as in ttq_gemm_i8; h

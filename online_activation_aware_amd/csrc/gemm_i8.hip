@@ -240,7 +240,7 @@ __global__ __launch_bounds__(kOneWaves * kWave) void k_i8_one(I8RowsArgs x, I8Pr
     }
 }
 
-// (64 KB of LDS in all.)
+// (33 KB of LDS at most.)
 bool i8_one_fits(int64_t T, int64_t K) { return T == 1 && K <= kOneWaves * kWave * kRowSeg * kOneSegs; }
 
 hipError_t launch_i8_one(const I8RowsArgs& x, const I8Product& q, bool yf32, hipStream_t st) {
@@ -278,7 +278,7 @@ hipError_t launch_i8_one(const I8RowsArgs& x, const I8Product& q, bool yf32, hip
 // read it, three phases ahead of its use.  (A step's 64 KB take longer than one
 // step's products to arrive.  A third slot of W for the smaller tiles: 64 x 4096 ->
 // 14336 15.1 us, two 14.5; 768 rows 55 and 54.)  Of 256 x 256: 8192 rows of 4096 ->
-// 4096 in 117 to 125 us, 2.2 to 2.35 POP/s, the matrix pipes busy for 55% of the
+// 4096 in 115 to 130 us, 2.1 to 2.4 POP/s, the matrix pipes busy for 55% of the
 // cycles; with all codes zero 100 us, so that power sets a part of it.
 template <int BM, int BN, int WM, int WN, int OUT>
 __global__ __launch_bounds__(WM * WN * kWave, 1) void k_i8_tile(I8Product p) {
@@ -520,7 +520,9 @@ static hipError_t tiled(const I8Product& p, int out, hipStream_t st) {
 // average, a third at most.  Some of them (us): 8192 rows of 4096 -> 4096: 256 x
 // 256 124, 256 x 128 153, 128 x 64 193; 2048: 56, 40, 52; 512: 57, 31, 18, 64 x 32
 // 20; 64: 64 x 32 12, streamed 14; 16: 12 and 7; 14336 -> 4096, 1024 rows: 256 x 128
-// in two parts 74, in one 103; 64 rows: 128 x 64 in eight parts 21, in one 48.
+// in two parts 74, in one 103; 64 rows: 128 x 64 in eight parts 21, in one 48.  (What their
+// bytes or products take: 4096 -> 4096, 8192 rows 131 at the library's rate, 2048 33, 512
+// 8.2, 64 3.4; 14336 -> 4096, 1024 rows 57, 64 rows 12.)
 //
 // A tile takes `start` and for each 128 channels `step`, `full` where every
 // compute unit has a tile and `more` for each further one that it works on at the

@@ -1,4 +1,4 @@
-// A gated mixture-of-experts layer of any number of tokens in 8-bit integers:
+// A gated mixture-of-experts layer, of long prompts too, in 8-bit integers:
 //   Y[t] = sum_j w[t][j] D_e h^,  h = act(g) u / s_down,  [g; u] = G_e x^,
 // x^ and h^ the rows of X / s_in and of h in 8 bits, e = ids[t][j].
 //

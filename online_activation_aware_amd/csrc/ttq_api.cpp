@@ -778,7 +778,7 @@ ttq_status check_codes(const char* name, const void* p, int64_t rows, int64_t K,
     return TTQ_OK;
 }
 
-ttq_status check_floats(const char* name, const void* p) {
+ttq_status check_words(const char* name, const void* p) {
     TTQ_REQUIRE(p != nullptr && aligned(p, 4), "%s: null or misaligned", name);
     return TTQ_OK;
 }
@@ -791,7 +791,7 @@ ttq_status check_product_i8(int64_t T, int64_t K, int64_t M, const int8_t* W, co
     if (ttq_status e = check_codes("W", W, T == 0 ? 0 : M, K, ldw)) return e;
     if (ttq_status e = check_output(Y, yt, T, M, ldy)) return e;
     if (T > 0 && M > 0)
-        if (ttq_status e = check_floats("w_scale", w_scale)) return e;
+        if (ttq_status e = check_words("w_scale", w_scale)) return e;
     if (ldw > kMaxLdI8) return fail(TTQ_ERR_UNSUPPORTED, "W: row stride above 2^22");
     if (!ttq::i8_product_fits(T, M, 0)) return fail(TTQ_ERR_UNSUPPORTED, "T x M is beyond one launch");
     return TTQ_OK;
@@ -809,11 +809,6 @@ ttq_status check_slots(int64_t T, int64_t topk) {
     TTQ_REQUIRE(dim_ok(T), "T out of range");
     TTQ_REQUIRE(topk >= 1 && topk <= ttq::kRouteMaxTopk, "topk must be in [1, %d]", ttq::kRouteMaxTopk);
     TTQ_REQUIRE(T * topk <= kMaxSlots, "T * topk above 2^30");
-    return TTQ_OK;
-}
-
-ttq_status check_ints(const char* name, const void* p) {
-    TTQ_REQUIRE(p != nullptr && aligned(p, 4), "%s: null or misaligned", name);
     return TTQ_OK;
 }
 
@@ -854,7 +849,7 @@ ttq_status ttq_quantize_rows(const void* X, int xt, int64_t R, int64_t K, int64_
     TTQ_REQUIRE(aligned(s, 16), "s: pointer not 16-byte aligned");
     if (ttq_status e = check_codes("codes", codes, R, K, ldc)) return e;
     if (R == 0) return TTQ_OK;
-    if (ttq_status e = check_floats("scale", scale)) return e;
+    if (ttq_status e = check_words("scale", scale)) return e;
     return device_status(ttq::launch_quantize_rows({X, xt == TTQ_F32, ldx, R, K, s, divide != 0, codes, ldc, scale},
                                                    as_stream(stream)),
                          "ttq_quantize_rows launch");
@@ -873,7 +868,7 @@ ttq_status ttq_gemm_i8(const int8_t* X, const float* x_scale, int64_t T, int64_t
     if (ttq_status e = check_codes("X", X, M == 0 ? 0 : T, K, ldx)) return e;
     if (ldx > kMaxLdI8) return fail(TTQ_ERR_UNSUPPORTED, "X: row stride above 2^22");
     if (T == 0 || M == 0) return TTQ_OK;
-    if (ttq_status e = check_floats("x_scale", x_scale)) return e;
+    if (ttq_status e = check_words("x_scale", x_scale)) return e;
     if (ttq_status e = check_ws(ws, ws_bytes, ttq_gemm_i8_workspace_bytes(T, K, M))) return e;
     return device_status(ttq::launch_i8_product({X, ldx, x_scale, T, K, W, ldw, w_scale, M, Y, ldy}, yt == TTQ_F32, ws,
                                                 as_stream(stream)),
@@ -917,11 +912,11 @@ ttq_status ttq_moe_sort(const int32_t* ids, int64_t T, int64_t topk, int64_t E, 
     g_last_error.clear();
     if (ttq_status e = check_slots(T, topk)) return e;
     TTQ_REQUIRE(E >= 1 && E <= ttq::kMoeMaxExperts, "E (experts) must be in [1, %d]", ttq::kMoeMaxExperts);
-    if (ttq_status e = check_ints("offsets", offsets)) return e;
+    if (ttq_status e = check_words("offsets", offsets)) return e;
     if (T > 0) {
-        if (ttq_status e = check_ints("ids", ids)) return e;
-        if (ttq_status e = check_ints("order", order)) return e;
-        if (ttq_status e = check_ints("pos", pos)) return e;
+        if (ttq_status e = check_words("ids", ids)) return e;
+        if (ttq_status e = check_words("order", order)) return e;
+        if (ttq_status e = check_words("pos", pos)) return e;
         if (ttq_status e = check_ws(ws, ws_bytes, ttq_moe_sort_workspace_bytes(T, topk, E))) return e;
     }
     return device_status(ttq::launch_moe_sort(ids, T * topk, (int)E, offsets, order, pos, (int32_t*)ws, as_stream(stream)),
@@ -936,7 +931,7 @@ ttq_status ttq_moe_gather(const void* X, int xt, int64_t T, int64_t K, int64_t l
     if (ttq_status e = check_matrix("X", X, xt, T, K, ldx)) return e;
     if (ttq_status e = check_rows_moe("R", R, xt, T == 0 ? 0 : rows, K, ldr)) return e;
     if (T == 0 || rows == 0) return TTQ_OK;
-    if (ttq_status e = check_ints("pos", pos)) return e;
+    if (ttq_status e = check_words("pos", pos)) return e;
     return device_status(ttq::launch_moe_gather(X, (int)esize(xt), T, K, ldx, pos, (int)topk, R, rows, ldr,
                                                 as_stream(stream)),
                          "ttq_moe_gather launch");
@@ -950,7 +945,7 @@ ttq_status ttq_moe_combine(const void* R, int rt, int64_t rows, int64_t ldr, con
     if (ttq_status e = check_rows_moe("R", R, rt, T == 0 || M == 0 ? 0 : rows, M, ldr)) return e;
     if (ttq_status e = check_output(Y, yt, T, M, ldy)) return e;
     if (T == 0 || M == 0) return TTQ_OK;
-    if (ttq_status e = check_ints("pos", pos)) return e;
+    if (ttq_status e = check_words("pos", pos)) return e;
     TTQ_REQUIRE(aligned(w, 4), "w: misaligned");
     return device_status(ttq::launch_moe_combine(R, rt == TTQ_F32, rows, ldr, pos, w, T, (int)topk, M, Y, yt == TTQ_F32,
                                                  ldy, as_stream(stream)),
@@ -973,7 +968,7 @@ ttq_status ttq_moe_combine_grad(const void* dY, int yt, int64_t T, int64_t M, in
     TTQ_REQUIRE(dR == nullptr || dR != R, "dR must not be R");
     TTQ_REQUIRE(aligned(w, 4) && aligned(dw, 4), "w or dw: misaligned");
     if (T == 0 || (dR == nullptr && dw == nullptr)) return TTQ_OK;
-    if (ttq_status e = check_ints("pos", pos)) return e;
+    if (ttq_status e = check_words("pos", pos)) return e;
     return device_status(ttq::launch_moe_combine_grad(dY, yt == TTQ_F32, lddy, R, rt == TTQ_F32, rows, ldr, pos, w, T,
                                                       (int)topk, M, dR, lddr, dw, as_stream(stream)),
                          "ttq_moe_combine_grad launch");

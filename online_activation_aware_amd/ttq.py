@@ -1005,8 +1005,8 @@ def _expert_i8(name: str, q: dict, E: int, rows: int, K: int, dev) -> ExpertI8:
 def ttq_moe_i8(X: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up: dict, down: dict, act: str = "silu",
                Y: Optional[torch.Tensor] = None, y_dtype=torch.float32, ws: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
-    """A gated mixture-of-experts layer in 8-bit integers, any number of
-    tokens: X [T][K], ids and w [T][topk] (ttq_moe_route); gate_up and down:
+    """A gated mixture-of-experts layer in 8-bit integers, long prompts too
+    (T topk up to 2^24, T K below 2^31): X [T][K], ids and w [T][topk] (ttq_moe_route); gate_up and down:
     dicts of ``codes`` int8 [E][rows][K], ``scale`` [E][rows] and ``s`` ([K],
     or [E][K] for scales per expert), with 2 I rows of K channels (gate first)
     and M rows of I channels.  Returns Y [T][M]."""
