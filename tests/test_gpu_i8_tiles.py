@@ -1,4 +1,4 @@
-"""8-bit products by every tile and in parts of the channels: an odd number of
+"""8-bit products by every kernel and in parts of the channels: an odd number of
 128-channel steps, ragged ends, every kind of result; sums are exact, so results
 equal their definition, or a call of few rows, whose kernel is another."""
 import pytest
@@ -30,8 +30,8 @@ def inputs(Tn, K, M, dt):
     return x, xs, w, ws, (sums.float() * xs[:, None] * ws[None, :]).to(DT[dt])
 
 
-# In tiles of 64 x 32, 128 x 64, 256 x 128 and 256 x 256.
-@pytest.mark.parametrize("Tn,K,M", [(139, 272, 65), (4193, 288, 332), (2429, 272, 2596), (3901, 288, 2624), (3901, 1328, 2624)])
+# Streamed for 32 rows at a time, in tiles of 64 x 32, 128 x 64, 256 x 128 and 256 x 256.
+@pytest.mark.parametrize("Tn,K,M", [(17, 1840, 159), (139, 272, 65), (4193, 288, 332), (2429, 272, 2596), (3901, 288, 2624), (3901, 1328, 2624)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_tiles_of_an_odd_number_of_steps(T, Tn, K, M, dt):
     say(f"gemm_i8 odd steps T={Tn} K={K} M={M} {dt}")
@@ -41,7 +41,7 @@ def test_tiles_of_an_odd_number_of_steps(T, Tn, K, M, dt):
         assert torch.equal(T.ttq_gemm_i8(x, xs, w, ws, y_dtype=DT[dt]), want)
 
 
-# The same tiles, 2 to 16 parts.
+# The tiles, with 2 to 16 parts.
 PARTS = [(145, 1888, 61), (131, 4976, 60), (2335, 4912, 269), (1421, 4432, 161), (797, 7472, 73), (433, 4976, 4728), (2085, 7792, 132), (3299, 9568, 542)]
 
 
@@ -114,3 +114,18 @@ def test_two_captured_graphs_in_parts(T):
             assert torch.equal(Y, want), turn
         jobs[turn % 2][0]()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("K,M", [(1040, 4097), (144, 6161), (4096, 40)])
+def test_one_token_of_fp32_into_bf16(T, K, M):
+    """One launch; equal to the same row in a call of two tokens."""
+    say(f"qgemm_i8 one fp32 token K={K} M={M}")
+    g = torch.Generator(device="cuda").manual_seed(K)
+    X, s = torch.randn((2, K), generator=g, device="cuda"), torch.rand(K, generator=g, device="cuda") + 0.5
+    W, ws = codes_like(g, M, K), torch.rand(M, generator=g, device="cuda")
+    for sv in (s, None):
+        one, two = (T.ttq_qgemm_i8(x, sv, W, ws, y_dtype=torch.bfloat16) for x in (X[:1], X))
+        q, xs = T.ttq_quantize_rows(X, sv, divide=True)
+        sums = q.double() @ W.double().t().contiguous()
+        assert torch.equal(two, (sums.float() * xs[:, None] * ws[None, :]).bfloat16())
+        assert torch.equal(one, two[:1])
