@@ -1017,389 +1017,6 @@ def ttq_moe_i8(X: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up: dic
     T, K = X.shape
     dev = X.get_device()
     if ids.dim() != 2 or gate_up["codes"].dim() != 3 or down["codes"].dim() != 3:
-        raise ValueError("ids must be [T][topk] and codes [E][rows][words]")
-    topk = ids.shape[1]
-    E, rows2, _ = gate_up["codes"].shape
-    M, I = down["codes"].shape[1], rows2 // 2
-    if rows2 % 2 or bits <= 0 or group <= 0:
-        raise ValueError("gate_up must have an even number of rows; bits and group must be positive")
-    Y = _output(Y, (T, M), y_dtype, X)
-    wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_moe_workspace_bytes(T, topk, K, I, M, E, bits, group),
-                          X)
-    a = MoeArgs(              # in the order of its fields
-        X.data_ptr(), _code(X), T, K, ldx, _dense(ids, "ids", torch.int32, (T, topk), dev),
-        _dense(w, "w", torch.float32, (T, topk), dev), topk, E, I, M,
-        _expert_state("gate_up", gate_up, E, rows2, K, bits, group, dev),
-        _expert_state("down", down, E, M, I, bits, group, dev), bits, group, TTQ_ACTS[act], Y.data_ptr(), _code(Y),
-        _row_stride(Y, "Y"))
-    _check(lib().ttq_moe(ctypes.byref(a), wp, wn, stream))
-    return Y
-
-
-def ttq_adapters_workspace_bytes(T: int, K: int, M: int, rank: int) -> int:
-    return int(lib().ttq_adapters_workspace_bytes(T, K, M, rank))
-
-
-def adapters_workspace(T: int, K: int, M: int, rank: int, device="cuda") -> torch.Tensor:
-    """Allocate a workspace tensor of ttq_adapters_workspace_bytes() bytes."""
-    return _bytes_tensor(ttq_adapters_workspace_bytes(T, K, M, rank), device)
-
-
-def _adapters(A, B, ids, ranks, scale, T: int, K: int, M: Optional[int], dev) -> AdaptersArgs:
-    if A.dim() != 3 or B.dim() != 3:
-        raise ValueError("A must be [n][rank][K] and B [n][M][rank]")
-    n, rank, _ = A.shape
-    dt = _code(A)
-    return AdaptersArgs(      # in the order of its fields
-        _dense(A, "A", A.dtype, (n, rank, K), dev),
-        _dense(B, "B", A.dtype, (n, B.shape[1] if M is None else M, rank), dev), dt, n, rank,
-        None if ranks is None else _dense(ranks, "ranks", torch.int32, (n,), dev),
-        None if scale is None else _dense(scale, "scale", torch.float32, (n,), dev),
-        _dense(ids, "ids", torch.int32, (T,), dev))
-
-
-@_on_tensor_device
-def ttq_adapters_add(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor,
-                     C: Optional[torch.Tensor] = None, ranks: Optional[torch.Tensor] = None,
-                     scale: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None, y_dtype=None,
-                     ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Y[t] = C[t] + scale[a] B[a] (A[a] X[t]), a = ids[t] (outside [0, n):
-    none): A [n][rank][K], B [n][M][rank], ranks int32 [n] (rows of A in use),
-    scale float32 [n].  C (default zeros) has Y's dtype; Y=C works in place."""
-    ldx = _row_stride(X, "X")
-    T, K = X.shape
-    dev = X.get_device()
-    ad = _adapters(A, B, ids, ranks, scale, T, K, None, dev)
-    M = B.shape[1]
-    if y_dtype is None:
-        y_dtype = torch.float32 if C is None else C.dtype
-    Y = _output(Y, (T, M), y_dtype, X)
-    cp, ldc = None, 0
-    if C is not None:
-        _output(C, (T, M), C.dtype, X, "C")
-        if C.dtype != Y.dtype:
-            raise TypeError("C must have Y's dtype")
-        cp, ldc = C.data_ptr(), _row_stride(C, "C")
-    wp, wn, ws = _scratch(ws, 0 if ws is not None else lib().ttq_adapters_workspace_bytes(T, K, M, ad.rank), X)
-    _check(lib().ttq_adapters_add(X.data_ptr(), _code(X), T, K, ldx, ctypes.byref(ad), M, cp, ldc, Y.data_ptr(),
-                                  _code(Y), _row_stride(Y, "Y"), wp, wn, stream))
-    return Y
-
-
-def ttq_qgemm_adapters_workspace_bytes(T: int, K: int, M: int, bits: int, group: int, rank: int) -> int:
-    return int(lib().ttq_qgemm_adapters_workspace_bytes(T, K, M, bits, group, rank))
-
-
-def qgemm_adapters_workspace(T: int, K: int, M: int, bits: int, group: int, rank: int, device="cuda") -> torch.Tensor:
-    """Allocate a workspace tensor of ttq_qgemm_adapters_workspace_bytes() bytes."""
-    return _bytes_tensor(ttq_qgemm_adapters_workspace_bytes(T, K, M, bits, group, rank), device)
-
-
-@_on_tensor_device
-def ttq_qgemm_adapters(X: torch.Tensor, s: torch.Tensor, codes: torch.Tensor, scale_f16: torch.Tensor,
-                       zero_f16: torch.Tensor, M: int, bits: int, group: int, A: torch.Tensor, B: torch.Tensor,
-                       ids: torch.Tensor, ranks: Optional[torch.Tensor] = None,
-                       scale: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
-                       y_dtype=torch.float32, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """ttq_qgemm on one shared quantized state plus each token's adapter (see
-    ttq_adapters_add); Y is rounded once."""
-    ldx = _row_stride(X, "X")
-    T, K = X.shape
-    dev = X.get_device()
-    if bits <= 0 or group <= 0:
-        raise ValueError("bits and group must be positive")
-    ad = _adapters(A, B, ids, ranks, scale, T, K, M, dev)
-    Y = _output(Y, (T, M), y_dtype, X)
-    wp, wn, ws = _scratch(
-        ws, 0 if ws is not None else lib().ttq_qgemm_adapters_workspace_bytes(T, K, M, bits, group, ad.rank), X)
-    _check(lib().ttq_qgemm_adapters(
-        X.data_ptr(), _code(X), T, K, ldx, _dense(s, "s", torch.float32, (K,), dev),
-        _dense(codes, "codes", torch.int32, (M, K * bits // 32), dev),
-        _dense(scale_f16, "scale_f16", torch.float16, (M, K // group), dev),
-        _dense(zero_f16, "zero_f16", torch.float16, (M, K // group), dev), M, bits, group, ctypes.byref(ad),
-        Y.data_ptr(), _code(Y), _row_stride(Y, "Y"), wp, wn, stream))
-    return Y
-
-
-# ------------------------------------------------------------------ 8-bit integers, sorted tokens
-
-def _rows8(codes: torch.Tensor, name: str, dev: int) -> int:
-    """Row stride of a matrix of 8-bit codes."""
-    try:
-        st, shape = codes.stride(), codes.shape
-        if codes.dtype is torch.int8 and codes.get_device() == dev and len(st) == 2 and st[1] == 1:
-            return st[0] if shape[0] > 1 else shape[1]
-    except AttributeError:
-        pass
-    if not isinstance(codes, torch.Tensor) or codes.dtype is not torch.int8:
-        raise TypeError(f"{name} must be a torch.int8 tensor")
-    if codes.get_device() != dev:
-        raise ValueError(f"{name} must be on device {dev}")
-    return _row_stride(codes, name)
-
-
-def _on(t: torch.Tensor, name: str, dev: int) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a device tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on device {dev}")
-    return t
-
-
-def _wide_stride(t: torch.Tensor, name: str) -> int:
-    """Row stride of a matrix whose rows need not be whole 16-byte pieces
-    long; that of a single row does not matter."""
-    st, (rows, row) = t.stride(), t.shape if t.dim() == 2 else (0, 0)
-    if len(st) != 2 or st[1] != 1 and row > 1:
-        raise ValueError(f"{name} must be 2-D with unit stride in its last dimension")
-    return st[0] if rows > 1 else -(-row // 8) * 8
-
-
-def _new_rows(rows: int, row: int, like: torch.Tensor) -> torch.Tensor:
-    """A matrix of `like`'s dtype whose rows begin at whole 16-byte pieces
-    (dense where their length allows it)."""
-    n = 16 // like.element_size()
-    return like.new_empty((rows, -(-row // n) * n))[:, :row]
-
-
-@_on_tensor_device
-def ttq_quantize_rows(X: torch.Tensor, s: Optional[torch.Tensor] = None, divide: bool = False,
-                      codes: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, stream=None):
-    """Rows of X [R][K] (times s [K], or with divide=True by it) in 8 bits:
-    codes int8 [R][K] and scale float32 [R]."""
-    ldx = _row_stride(X, "X")
-    R, K = X.shape
-    dev = X.get_device()
-    codes = _output(codes, (R, K), torch.int8, X, "codes")
-    ldc = _rows8(codes, "codes", dev)
-    if scale is None:
-        scale = X.new_empty((R,), dtype=torch.float32)
-    _check(lib().ttq_quantize_rows(X.data_ptr(), _code(X), R, K, ldx,
-                                   None if s is None else _dense(s, "s", torch.float32, (K,), dev), int(bool(divide)),
-                                   codes.data_ptr(), ldc, _dense(scale, "scale", torch.float32, (R,), dev), stream))
-    return codes, scale
-
-
-def ttq_gemm_i8_workspace_bytes(T: int, K: int, M: int) -> int:
-    return int(lib().ttq_gemm_i8_workspace_bytes(T, K, M))
-
-
-def gemm_i8_workspace(T: int, K: int, M: int, device="cuda") -> torch.Tensor:
-    """Allocate a workspace tensor of ttq_gemm_i8_workspace_bytes() bytes."""
-    return _bytes_tensor(ttq_gemm_i8_workspace_bytes(T, K, M), device)
-
-
-@_on_tensor_device
-def ttq_gemm_i8(X: torch.Tensor, x_scale: torch.Tensor, W: torch.Tensor, w_scale: torch.Tensor,
-                Y: Optional[torch.Tensor] = None, y_dtype=torch.float32, ws: Optional[torch.Tensor] = None,
-                stream=None) -> torch.Tensor:
-    """Product of 8-bit rows (ttq_quantize_rows): Y[t][o] = x_scale[t]
-    w_scale[o] sum_j X[t][j] W[o][j], X int8 [T][K], W int8 [M][K]."""
-    dev = X.get_device()
-    ldx, ldw = _rows8(X, "X", dev), _rows8(W, "W", dev)
-    T, K = X.shape
-    M = W.shape[0]
-    if W.shape[1] != K:
-        raise ValueError(f"W must be [M][{K}] (got {list(W.shape)})")
-    if Y is None:
-        Y, ldy = X.new_empty((T, M), dtype=y_dtype), M
-    else:
-        ldy = _row_stride(_output(Y, (T, M), None, X), "Y")
-    L = lib()
-    wp, wn, ws = _scratch(ws, 0 if ws is not None else L.ttq_gemm_i8_workspace_bytes(T, K, M), X)
-    _check(L.ttq_gemm_i8(X.data_ptr(), _dense(x_scale, "x_scale", torch.float32, (T,), dev), T, K, ldx, W.data_ptr(),
-                         _dense(w_scale, "w_scale", torch.float32, (M,), dev), M, ldw, Y.data_ptr(), _code(Y), ldy,
-                         wp, wn, stream))
-    return Y
-
-
-def ttq_qgemm_i8_workspace_bytes(T: int, K: int, M: int) -> int:
-    return int(lib().ttq_qgemm_i8_workspace_bytes(T, K, M))
-
-
-def qgemm_i8_workspace(T: int, K: int, M: int, device="cuda") -> torch.Tensor:
-    """Allocate a workspace tensor of ttq_qgemm_i8_workspace_bytes() bytes."""
-    return _bytes_tensor(ttq_qgemm_i8_workspace_bytes(T, K, M), device)
-
-
-@_on_tensor_device
-def ttq_qgemm_i8(X: torch.Tensor, s: Optional[torch.Tensor], W: torch.Tensor, w_scale: torch.Tensor,
-                 Y: Optional[torch.Tensor] = None, y_dtype=torch.float32, ws: Optional[torch.Tensor] = None,
-                 stream=None) -> torch.Tensor:
-    """The projection W_hat (X / s) in 8-bit integers: X [T][K] is quantized
-    per token (ttq_quantize_rows with divide=True), W int8 [M][K] and w_scale
-    [M] are the weight times s in 8 bits."""
-    dev = X.get_device()
-    ldx, ldw = _row_stride(X, "X"), _rows8(W, "W", dev)
-    T, K = X.shape
-    M = W.shape[0]
-    if W.shape[1] != K:
-        raise ValueError(f"W must be [M][{K}] (got {list(W.shape)})")
-    if Y is None:
-        Y, ldy = X.new_empty((T, M), dtype=y_dtype), M
-    else:
-        ldy = _row_stride(_output(Y, (T, M), None, X), "Y")
-    L = lib()
-    wp, wn, ws = _scratch(ws, 0 if ws is not None else L.ttq_qgemm_i8_workspace_bytes(T, K, M), X)
-    _check(L.ttq_qgemm_i8(X.data_ptr(), _code(X), T, K, ldx,
-                          None if s is None else _dense(s, "s", torch.float32, (K,), dev), W.data_ptr(),
-                          _dense(w_scale, "w_scale", torch.float32, (M,), dev), M, ldw, Y.data_ptr(), _code(Y), ldy,
-                          wp, wn, stream))
-    return Y
-
-
-def ttq_moe_sort_workspace_bytes(T: int, topk: int, E: int) -> int:
-    return int(lib().ttq_moe_sort_workspace_bytes(T, topk, E))
-
-
-def moe_sort_workspace(T: int, topk: int, E: int, device="cuda") -> torch.Tensor:
-    """Allocate a workspace tensor of ttq_moe_sort_workspace_bytes() bytes."""
-    return torch.empty(ttq_moe_sort_workspace_bytes(T, topk, E), dtype=torch.uint8, device=device)
-
-
-@_on_tensor_device
-def ttq_moe_sort(ids: torch.Tensor, E: int, offsets: Optional[torch.Tensor] = None,
-                 order: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
-                 ws: Optional[torch.Tensor] = None, stream=None):
-    """The slots of ids (int32 [T][topk]) sorted by expert, stably: offsets
-    [E + 1] (each expert's rows), order [T * topk] (each row's slot, -1 behind
-    the last) and pos [T][topk] (each slot's row, -1 without an expert)."""
-    if ids.dim() != 2:
-        raise ValueError("ids must be [T][topk]")
-    T, topk = ids.shape
-    dev = ids.get_device()
-    ip = _dense(ids, "ids", torch.int32, (T, topk), dev)
-    n = E + 1 if 0 <= E <= 1024 else 0       # others are refused below
-    L = lib()
-    if offsets is None:
-        offsets = ids.new_empty((n,))
-        fp = offsets.data_ptr()
-    else:
-        fp = _dense(offsets, "offsets", torch.int32, (n,), dev)
-    if order is None:
-        order = ids.new_empty((T * topk,))
-        op = order.data_ptr()
-    else:
-        op = _dense(order, "order", torch.int32, (T * topk,), dev)
-    if pos is None:
-        pos = ids.new_empty((T, topk))
-        pp = pos.data_ptr()
-    else:
-        pp = _dense(pos, "pos", torch.int32, (T, topk), dev)
-    if ws is None:
-        need = L.ttq_moe_sort_workspace_bytes(T, topk, E)
-        ws = ids.new_empty((need,), dtype=torch.uint8) if need else None
-    wp, wn = (None, 0) if ws is None else _scratch(ws, 0, ids)[:2]
-    _check(L.ttq_moe_sort(ip, T, topk, E, fp, op, pp, wp, wn, stream))
-    return offsets, order, pos
-
-
-@_on_tensor_device
-def ttq_moe_gather(X: torch.Tensor, pos: torch.Tensor, R: Optional[torch.Tensor] = None,
-                   stream=None) -> torch.Tensor:
-    """R[pos[t][j]] = X[t]: the tokens' rows in their experts' order (pos from
-    ttq_moe_sort).  R [rows][K] has X's dtype (default: new, a row for each
-    slot, its row stride K rounded up to 16 bytes); rows that no slot names
-    are left as they were."""
-    ldx = _wide_stride(X, "X")
-    T, K = X.shape
-    if pos.dim() != 2:
-        raise ValueError("pos must be [T][topk]")
-    topk = pos.shape[1]
-    if R is None:
-        R = _new_rows(T * topk, K, X)
-    elif _on(R, "R", X.get_device()).dtype != X.dtype or R.dim() != 2 or R.shape[1] != K:
-        raise ValueError(f"R must be [rows][{K}] of X's dtype")
-    _check(lib().ttq_moe_gather(X.data_ptr(), _code(X), T, K, ldx,
-                                _dense(pos, "pos", torch.int32, (T, topk), X.get_device()), topk, R.data_ptr(),
-                                R.shape[0], _wide_stride(R, "R"), stream))
-    return R
-
-
-@_on_tensor_device
-def ttq_moe_combine(R: torch.Tensor, pos: torch.Tensor, w: Optional[torch.Tensor] = None,
-                    Y: Optional[torch.Tensor] = None, y_dtype=None, stream=None) -> torch.Tensor:
-    """Y[t] = sum_j w[t][j] R[pos[t][j]] (w None: ones, the gradient of
-    ttq_moe_gather); a slot without a row adds nothing.  Y: R's dtype unless
-    given."""
-    ldr = _wide_stride(R, "R")
-    rows, M = R.shape
-    if pos.dim() != 2:
-        raise ValueError("pos must be [T][topk]")
-    T, topk = pos.shape
-    dev = R.get_device()
-    if Y is None:
-        Y = R.new_empty((T, M), dtype=R.dtype if y_dtype is None else y_dtype)
-        ldy = M
-    else:
-        ldy = _row_stride(_output(Y, (T, M), None, R), "Y")
-    _check(lib().ttq_moe_combine(R.data_ptr(), _code(R), rows, ldr, _dense(pos, "pos", torch.int32, (T, topk), dev),
-                                 None if w is None else _dense(w, "w", torch.float32, (T, topk), dev), T, topk, M,
-                                 Y.data_ptr(), _code(Y), ldy, stream))
-    return Y
-
-
-@_on_tensor_device
-def ttq_moe_combine_grad(dY: torch.Tensor, R: torch.Tensor, pos: torch.Tensor, w: Optional[torch.Tensor] = None,
-                         dR: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, stream=None):
-    """The gradient of ttq_moe_combine: (dR [rows][M], dw [T][topk]) from dY
-    [T][M].  dR (default: new, its row stride M rounded up to 16 bytes) keeps
-    the rows that no slot names."""
-    lddy, ldr = _wide_stride(dY, "dY"), _wide_stride(R, "R")
-    T, M = dY.shape
-    dev = dY.get_device()
-    if _on(R, "R", dev).shape[1] != M or pos.dim() != 2:
-        raise ValueError(f"R must be [rows][{M}] and pos [T][topk]")
-    topk = pos.shape[1]
-    rt = _code(R)
-    dR = _new_rows(R.shape[0], M, R) if dR is None else _output(dR, R.shape, R.dtype, dY, "dR")
-    if dR.dtype is not R.dtype:
-        raise TypeError("dR must have R's dtype")
-    if dw is None:
-        dw = dY.new_empty((T, topk), dtype=torch.float32)
-        dwp = dw.data_ptr()
-    else:
-        dwp = _dense(dw, "dw", torch.float32, (T, topk), dev)
-    _check(lib().ttq_moe_combine_grad(dY.data_ptr(), _code(dY), T, M, lddy, R.data_ptr(), rt, R.shape[0], ldr,
-                                      _dense(pos, "pos", torch.int32, (T, topk), dev),
-                                      None if w is None else _dense(w, "w", torch.float32, (T, topk), dev), topk,
-                                      dR.data_ptr(), _wide_stride(dR, "dR"), dwp, stream))
-    return dR, dw
-
-
-def ttq_moe_i8_workspace_bytes(T: int, topk: int, K: int, I: int, M: int, E: int) -> int:
-    return int(lib().ttq_moe_i8_workspace_bytes(T, topk, K, I, M, E))
-
-
-def moe_i8_workspace(T: int, topk: int, K: int, I: int, M: int, E: int, device="cuda") -> torch.Tensor:
-    """Allocate a workspace tensor of ttq_moe_i8_workspace_bytes() bytes."""
-    return _bytes_tensor(ttq_moe_i8_workspace_bytes(T, topk, K, I, M, E), device)
-
-
-def _expert_i8(name: str, q: dict, E: int, rows: int, K: int, dev) -> ExpertI8:
-    s = q["s"]
-    per = isinstance(s, torch.Tensor) and s.dim() == 2
-    return ExpertI8(          # in the order of its fields
-        _dense(s, name + " s", torch.float32, (E, K) if per else (K,), dev), K if per else 0,
-        _dense(q["codes"], name + " codes", torch.int8, (E, rows, K), dev),
-        _dense(q["scale"], name + " scale", torch.float32, (E, rows), dev))
-
-
-@_on_tensor_device
-def ttq_moe_i8(X: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, gate_up: dict, down: dict, act: str = "silu",
-               Y: Optional[torch.Tensor] = None, y_dtype=torch.float32, ws: Optional[torch.Tensor] = None,
-               stream=None) -> torch.Tensor:
-    """A gated mixture-of-experts layer in 8-bit integers, long prompts too
-    (T topk up to 2^24, T K below 2^31): X [T][K], ids and w [T][topk] (ttq_moe_route); gate_up and down:
-    dicts of ``codes`` int8 [E][rows][K], ``scale`` [E][rows] and ``s`` ([K],
-    or [E][K] for scales per expert), with 2 I rows of K channels (gate first)
-    and M rows of I channels.  Returns Y [T][M]."""
-    if act not in TTQ_ACTS:
-        raise ValueError(f"act must be one of {sorted(TTQ_ACTS)}")
-    ldx = _row_stride(X, "X")
-    T, K = X.shape
-    dev = X.get_device()
-    if ids.dim() != 2 or gate_up["codes"].dim() != 3 or down["codes"].dim() != 3:
         raise ValueError("ids must be [T][topk] and codes [E][rows][channels]")
     topk = ids.shape[1]
     E, rows2, _ = gate_up["codes"].shape
